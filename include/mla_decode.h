@@ -59,7 +59,8 @@ typedef enum {
   MLA_ERR_UNSUPPORTED = 2,
   MLA_ERR_WORKSPACE_TOO_SMALL = 3,
   MLA_ERR_CUDA = 4,
-  MLA_ERR_TIMEOUT = 5
+  MLA_ERR_TIMEOUT = 5,
+  MLA_ERR_NO_PAGES = 6 /* mla_pool_*: not enough free pages */
 } mla_status_t;
 
 #define MLA_HEAD_DIM 576
@@ -70,6 +71,37 @@ typedef enum {
 #define MLA_MAX_SPLITS 256  /* per-request split cap of the GB300 planner and the kernels */
 #define MLA_PAGES_SPLIT_CAP 128 /* the pages' planner cap (issue #20510, "Repro 2") */
 #define MLA_MAX_ROWS 1024   /* num_heads * q_len */
+#define MLA_FP4_BLOCK 32         /* latent values that share a scale in the 4-bit cache */
+#define MLA_FP4_PAGE_BYTES 10752 /* 32 x 256 code bytes, 16 x 32 scale bytes, 32 x 64 rope bytes */
+
+/*
+ * Kinds of paged cache.
+ *   MLA_CACHE_FP8   E4M3 [num_pages, 32, 576], values kv_scale * code.
+ *   MLA_CACHE_BF16  BF16 [num_pages, 32, 576].
+ *   MLA_CACHE_FP4   uint8 [num_pages, MLA_FP4_PAGE_BYTES]: the latent part in 4
+ *                   bits, the rope part in E4M3 (336 bytes a row instead of
+ *                   576).  A page holds three planes:
+ *     bytes [0, 8192)      codes, 32 rows x 256 bytes
+ *     bytes [8192, 8704)   scale codes, 16 blocks x 32 rows (byte 32 * block + row)
+ *     bytes [8704, 10752)  rope part, 32 rows x 64 E4M3 codes
+ *   Block k of a row is its latent values [32 k, 32 k + 32).  Its values are
+ *   kv_scale * 2^(e - 8) * v with the scale code e in 0..14 and v the E2M1
+ *   value of its code, +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} for the magnitude codes
+ *   0..7.  Scale code 15 marks a block that held a NaN: all of it reads as NaN.
+ *   Only the low 4 bits of a scale byte are read.  A row's codes are 64
+ *   little-endian 32-bit words of 8 values each: bits [4j, 4j + 3) are value
+ *   j's magnitude code, and bits 7, 15, 23, 31, 3, 11, 19, 27 the signs of
+ *   values 0, 1, ..., 7.
+ *   Encoding a block x (already divided by kv_scale): e is the smallest in
+ *   0..14 with max|x| <= 7 * 2^(e - 8), or 14; each value is the E2M1 value
+ *   nearest to x * 2^(8 - e), ties to the even code, magnitudes above
+ *   6 * 2^(e - 8) saturating.  A block with a NaN gets e = 15 and zero codes.
+ *   Every such value is an E4M3 number times kv_scale, so an FP4 page expands
+ *   to an FP8 page exactly.
+ */
+#define MLA_CACHE_FP8 0
+#define MLA_CACHE_BF16 1
+#define MLA_CACHE_FP4 2
 
 /*
  * Split planner (host only; issue #20510, "Repro 2": per-request plan
@@ -396,6 +428,162 @@ MLA_API int mla_kv_append(const void* rows_bf16, int64_t n_tokens, const int32_t
                           const int32_t* positions, const int32_t* page_table,
                           int32_t max_pages_per_req, int32_t batch, void* kv_pages_fp8,
                           int64_t num_pages, float kv_scale, int32_t* status, void* stream);
+
+/*
+ * Prologue of a decode step or of a prompt's chunk: what turns the projected
+ * rows of n_tokens new tokens into what the decode reads, in one pass (the
+ * whole of TensorRT-LLM PR #17273's prologue: norm, rotation, quantisation,
+ * scatter; mla_kv_append is its last part alone).
+ *
+ *   key row:   latent' = latent * rsqrt(mean(latent^2) + norm_eps) * weight,
+ *              rope' = R(pos) rope; [latent' rope'] / kv_scale goes to slot
+ *              pos % 32 of page page_table[req][pos / 32] in the cache's format.
+ *   query row: q' = [q[0:512], R(pos) q[512:576]] / q_scale, E4M3 or BF16.
+ *   R(pos):    for the 32 pairs (a, b) of the rope part,
+ *              (a cos_i - b sin_i, b cos_i + a sin_i) with row `pos` of cos_sin.
+ * All of it is computed in fp32 (the mean as well) and rounded once, to
+ * nearest even; quantisation multiplies by the fp32 reciprocal of the scale
+ * (mla_kv_append divides; for scales that are powers of two these are the same
+ * numbers) and saturates (E4M3 at 448, FP4 at 384).  A NaN stays one.
+ *
+ * positions     device int32 [n_tokens]: each token's index within its request.
+ * cos_sin       device fp32 [rope_rows][64], 16-byte aligned: 32 cosines, then
+ *               32 sines per position; NULL (with rope_rows 0): no rotation.
+ * rope_positions  device int32 [n_tokens] or NULL: rows of cos_sin, where they
+ *               are not `positions`.
+ * rope_halves   0: pairs (2i, 2i + 1); 1: pairs (i, i + 32).
+ * kv_rows       BF16, token t's row at kv_rows + t * kv_row_stride (elements, a
+ *               multiple of 8, >= 576; 0 = 576), 16-byte aligned; NULL: no key
+ *               part (the fields down to kv_scale are then not read).
+ * norm_weight   fp32 [512], 16-byte aligned, or NULL: no norm.
+ * norm_eps      >= 0.
+ * req_idx       device int32 [n_tokens]; -1 marks a padding token, neither of
+ *               whose rows is written (also where only queries are given, then
+ *               optional).
+ * page_table, max_pages_per_req, batch, kv_pages, num_pages, cache_kind
+ *               the cache; kv_pages 16-byte aligned.
+ * kv_scale      MLA_CACHE_BF16: 1.  Its reciprocal must be a normal number.
+ * q_rows        BF16, head h of token t at q_rows + t * q_token_stride +
+ *               h * q_head_stride (elements, multiples of 8; 0 = contiguous
+ *               [n_tokens, num_heads, 576]), 16-byte aligned; NULL: no queries.
+ * q_out         [n_tokens, num_heads, 576], E4M3 (q_kind MLA_CACHE_FP8) or BF16
+ *               (MLA_CACHE_BF16; q_scale 1), 16-byte aligned.  It may not
+ *               overlap q_rows.
+ * status        device int32 or NULL: set to MLA_ERR_INVALID_ARG if a token had
+ *               an out-of-range request, position, rope position or page id
+ *               (the rows that need it are skipped); never cleared by the call.
+ * Tokens with the same (request, position) race; the caller keeps them unique.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (q_kind MLA_CACHE_FP4),
+ * MLA_ERR_CUDA.  Zero-initialise the structure.
+ */
+typedef struct {
+  int64_t n_tokens;
+  const int32_t* positions;
+  const float* cos_sin;
+  const int32_t* rope_positions;
+  int32_t rope_rows;
+  int32_t rope_halves;
+  const void* kv_rows;
+  int64_t kv_row_stride;
+  const float* norm_weight;
+  float norm_eps;
+  int32_t max_pages_per_req;
+  const int32_t* req_idx;
+  const int32_t* page_table;
+  void* kv_pages;
+  int64_t num_pages;
+  int32_t batch;
+  int32_t cache_kind;
+  float kv_scale;
+  float q_scale;
+  const void* q_rows;
+  int64_t q_token_stride;
+  int64_t q_head_stride;
+  void* q_out;
+  int32_t num_heads;
+  int32_t q_kind;
+  int32_t* status;
+} mla_prologue_args_t;
+
+MLA_API int mla_prologue(const mla_prologue_args_t* args, void* stream);
+
+/*
+ * Page copies: for every i < n, the first rows[i] rows (all 32 where rows is
+ * NULL) of page src_ids[i] of one pool go to the same rows of page dst_ids[i]
+ * of another or the same pool; what lies behind them in the destination stays.
+ * Between pools of different kinds the rows are converted:
+ *   FP8 -> FP4   demotion: the E4M3 values encoded as MLA_CACHE_FP4 says (the
+ *                rope part copied), both pools with the same kv_scale;
+ *   FP4 -> FP8   promotion, exact.
+ * BF16 pages are only copied to BF16 pools (MLA_ERR_UNSUPPORTED otherwise).
+ *
+ * src_ids, dst_ids  device int32 [n]; an entry with -1 in either is skipped.
+ * rows          device int32 [n] or NULL, each in 0..32.
+ * status        device int32 or NULL: set to MLA_ERR_INVALID_ARG if an entry
+ *               had an id outside its pool or a bad row count (that entry is
+ *               skipped); never cleared by the call.
+ * Pools are 16-byte aligned; two different pools do not overlap.  No page may
+ * be the destination of two entries, nor (in one pool) both a destination and
+ * a source: the copies of one call run in no order.
+ */
+MLA_API int mla_pages_copy(const void* src_pool, int64_t src_pages, int32_t src_kind,
+                           void* dst_pool, int64_t dst_pages, int32_t dst_kind,
+                           const int32_t* src_ids, const int32_t* dst_ids, const int32_t* rows,
+                           int64_t n, int32_t* status, void* stream);
+
+/*
+ * Rewrites page tables after a compaction: every entry p in 0..num_pages - 1
+ * of the n_entries becomes page_map[p] (device int32 [num_pages]); negative
+ * entries (unused slots) stay.  status as for mla_pages_copy (an entry >=
+ * num_pages, which stays as it is).
+ */
+MLA_API int mla_pages_remap(int32_t* page_table, int64_t n_entries, const int32_t* page_map,
+                            int64_t num_pages, int32_t* status, void* stream);
+
+/*
+ * Page pool: which pages of a cache are in use, by how many holders (host
+ * only; it owns no device memory and touches none).  A page is free, or held
+ * `references` times: by the page tables of the requests that share it.  Calls
+ * on one pool from several threads are serialised inside.  A call that fails
+ * changes nothing.
+ */
+typedef struct mla_pool mla_pool_t;
+
+MLA_API int mla_pool_create(int64_t num_pages, mla_pool_t** pool_out);
+MLA_API void mla_pool_destroy(mla_pool_t* pool);
+/* Number of free pages (-1: null pool), references of a page (0: free; -1: bad argument). */
+MLA_API int64_t mla_pool_free_pages(mla_pool_t* pool);
+MLA_API int64_t mla_pool_references(mla_pool_t* pool, int32_t page);
+/* Takes the n lowest free pages, one reference each, in ascending order.
+ * MLA_ERR_NO_PAGES when fewer are free. */
+MLA_API int mla_pool_alloc(mla_pool_t* pool, int64_t n, int32_t* ids_out);
+/* Gives back one reference of each listed page (a page may be listed as often
+ * as it is held); pages without any are free again. */
+MLA_API int mla_pool_release(mla_pool_t* pool, const int32_t* ids, int64_t n);
+/*
+ * Forks a request with kv_len tokens in the pages ids[0 .. ceil(kv_len / 32))
+ * into n_forks further ones.  Full pages are shared (one more reference per
+ * fork); where kv_len ends inside a page each fork gets a page of its own for
+ * the rest, to be filled by mla_pages_copy from the returned lists.
+ * ids_out   host int32 [n_forks][ceil(kv_len / 32)]: the forks' page lists.
+ * src_out, dst_out, rows_out   host int32 [n_forks]: the copies to make.
+ * n_copies_out   how many there are: n_forks, or 0 (kv_len a multiple of 32).
+ */
+MLA_API int mla_pool_fork(mla_pool_t* pool, const int32_t* ids, int64_t kv_len, int64_t n_forks,
+                          int32_t* ids_out, int32_t* src_out, int32_t* dst_out,
+                          int32_t* rows_out, int64_t* n_copies_out);
+/*
+ * Compaction: moves the pages in use to the low end of the pool, so that they
+ * become pages 0 .. used - 1 and the rest is free.  The pages that are in use
+ * at or above `used` move to the free pages below it, lowest to lowest;
+ * references move along.  At most max_moves pages move (the lowest first);
+ * a later call moves the rest.
+ * src_out, dst_out   host int32 [max_moves]: the copies for mla_pages_copy.
+ * map_out   host int32 [num_pages]: new id of each page (its own where it does
+ *           not move), for mla_pages_remap.
+ */
+MLA_API int mla_pool_compact(mla_pool_t* pool, int64_t max_moves, int32_t* src_out,
+                             int32_t* dst_out, int32_t* map_out, int64_t* n_moves_out);
 
 /* Synchronously reads the status word at the head of `workspace` (MLA_OK,
  * MLA_ERR_INVALID_ARG for a bad page id or inconsistent plan arrays,

@@ -25,7 +25,9 @@ __all__ = [
     "mla_decode_static_ws", "mla_decode_static_ws_status", "mla_kv_append", "mla_decode_ex",
     "mla_decode_bf16", "mla_decode_sparse", "mla_decode_plan_items", "mla_decode_bf16_ex",
     "mla_decode_bf16_sparse", "mla_decode_plan_items_bf16", "DecodeOptions",
-    "decode", "merge",
+    "decode", "merge", "MLA_ERR_NO_PAGES", "CACHE_FP8", "CACHE_BF16", "CACHE_FP4",
+    "FP4_PAGE_BYTES", "PrologueArgs", "mla_prologue", "mla_pages_copy", "mla_pages_remap",
+    "PagePool", "copy_pages", "fp4_pool",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -35,9 +37,11 @@ MLA_ERR_UNSUPPORTED = 2
 MLA_ERR_WORKSPACE_TOO_SMALL = 3
 MLA_ERR_CUDA = 4
 MLA_ERR_TIMEOUT = 5
+MLA_ERR_NO_PAGES = 6
 _STATUS_NAMES = {
     0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED",
     3: "MLA_ERR_WORKSPACE_TOO_SMALL", 4: "MLA_ERR_CUDA", 5: "MLA_ERR_TIMEOUT",
+    6: "MLA_ERR_NO_PAGES",
 }
 EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_workspace_size", "mla_decode_workspace_init",
                     "mla_decode", "mla_decode_splitkv", "mla_decode_merge", "mla_merge",
@@ -45,7 +49,10 @@ EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_workspace_size", "mla_decode_
                     "mla_decode_static_ws", "mla_decode_static_ws_status", "mla_kv_append",
                     "mla_decode_ex", "mla_decode_bf16", "mla_decode_sparse",
                     "mla_decode_plan_items", "mla_decode_bf16_ex", "mla_decode_bf16_sparse",
-                    "mla_decode_plan_items_bf16", "mla_debug_set_expire")
+                    "mla_decode_plan_items_bf16", "mla_debug_set_expire", "mla_prologue",
+                    "mla_pages_copy", "mla_pages_remap", "mla_pool_create", "mla_pool_destroy",
+                    "mla_pool_free_pages", "mla_pool_references", "mla_pool_alloc",
+                    "mla_pool_release", "mla_pool_fork", "mla_pool_compact")
 
 HEAD_DIM = 576
 LATENT_DIM = 512
@@ -53,6 +60,10 @@ PAGE_SIZE = 32
 TILE_TOKENS = 128
 MAX_SPLITS = 256
 PAGES_SPLIT_CAP = 128
+# Kinds of paged cache (mla_decode.h: MLA_CACHE_*) and the bytes of a 4-bit page.
+CACHE_FP8, CACHE_BF16, CACHE_FP4 = 0, 1, 2
+FP4_BLOCK = 32
+FP4_PAGE_BYTES = 10752
 
 
 class DecodeOptions(ctypes.Structure):
@@ -63,6 +74,23 @@ class DecodeOptions(ctypes.Structure):
                 ("kv_bounds", ctypes.c_void_p), ("cta_items", ctypes.c_void_p),
                 ("num_ctas", ctypes.c_int32), ("persistent_ctas", ctypes.c_int32),
                 ("phases", ctypes.c_int32)]
+
+
+class PrologueArgs(ctypes.Structure):
+    """mla_prologue_args_t (include/mla_decode.h)."""
+    _fields_ = [("n_tokens", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("cos_sin", ctypes.c_void_p), ("rope_positions", ctypes.c_void_p),
+                ("rope_rows", ctypes.c_int32), ("rope_halves", ctypes.c_int32),
+                ("kv_rows", ctypes.c_void_p), ("kv_row_stride", ctypes.c_int64),
+                ("norm_weight", ctypes.c_void_p), ("norm_eps", ctypes.c_float),
+                ("max_pages_per_req", ctypes.c_int32), ("req_idx", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("kv_pages", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("cache_kind", ctypes.c_int32), ("kv_scale", ctypes.c_float),
+                ("q_scale", ctypes.c_float), ("q_rows", ctypes.c_void_p),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("num_heads", ctypes.c_int32),
+                ("q_kind", ctypes.c_int32), ("status", ctypes.c_void_p)]
 
 
 # mla_decode_options_t.phases: both phases, the split-KV kernel only, the merge only.
@@ -136,6 +164,28 @@ def load_library() -> ctypes.CDLL:
         lib.mla_decode_static_ws_status.argtypes = [vp]
         lib.mla_kv_append.restype = ctypes.c_int
         lib.mla_kv_append.argtypes = [vp, i64, vp, vp, vp, i32, i32, vp, i64, f32, vp, vp]
+        lib.mla_prologue.restype = ctypes.c_int
+        lib.mla_prologue.argtypes = [ctypes.POINTER(PrologueArgs), vp]
+        lib.mla_pages_copy.restype = ctypes.c_int
+        lib.mla_pages_copy.argtypes = [vp, i64, i32, vp, i64, i32, vp, vp, vp, i64, vp, vp]
+        lib.mla_pages_remap.restype = ctypes.c_int
+        lib.mla_pages_remap.argtypes = [vp, i64, vp, i64, vp, vp]
+        lib.mla_pool_create.restype = ctypes.c_int
+        lib.mla_pool_create.argtypes = [i64, ctypes.POINTER(vp)]
+        lib.mla_pool_destroy.restype = None
+        lib.mla_pool_destroy.argtypes = [vp]
+        lib.mla_pool_free_pages.restype = i64
+        lib.mla_pool_free_pages.argtypes = [vp]
+        lib.mla_pool_references.restype = i64
+        lib.mla_pool_references.argtypes = [vp, i32]
+        lib.mla_pool_alloc.restype = ctypes.c_int
+        lib.mla_pool_alloc.argtypes = [vp, i64, vp]
+        lib.mla_pool_release.restype = ctypes.c_int
+        lib.mla_pool_release.argtypes = [vp, vp, i64]
+        lib.mla_pool_fork.restype = ctypes.c_int
+        lib.mla_pool_fork.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp]
+        lib.mla_pool_compact.restype = ctypes.c_int
+        lib.mla_pool_compact.argtypes = [vp, i64, vp, vp, vp, vp]
         lib.mla_debug_set_wait_limit.restype = None
         lib.mla_debug_set_wait_limit.argtypes = [ctypes.c_longlong]
         lib.mla_debug_set_expire.restype = None
@@ -428,6 +478,181 @@ def mla_kv_append(rows_bf16, n_tokens: int, req_idx, positions, page_table,
         _ptr(status), _stream_handle(stream)))
 
 
+def _device_tensor(t, name: str, dtype=None, contiguous: bool = True):
+    """Address of a CUDA tensor (None for None), after the checks that a raw
+    address cannot carry: its device, type and contiguity."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call_on(tensor, fn, *args, stream=None) -> None:
+    """fn(*args, stream) with the tensor's device current: on `stream`, or on
+    that device's current stream."""
+    import torch
+    dev = tensor.device
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        handle = _stream_handle(stream)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, handle))
+
+
+def mla_prologue(n_tokens: int, *, positions=None, cos_sin=None, rope_positions=None,
+                 rope_rows: Optional[int] = None, rope_halves: bool = False, kv_rows=None,
+                 norm_weight=None, norm_eps: float = 1e-6, req_idx=None, page_table=None,
+                 max_pages_per_req: int = 0, batch: int = 0, kv_pages=None, num_pages: int = 0,
+                 cache_kind: int = CACHE_FP8, kv_scale: float = 1.0, q_rows=None,
+                 num_heads: int = 0, q_out=None, q_kind: int = CACHE_FP8, q_scale: float = 1.0,
+                 status=None, stream=None) -> None:
+    """Norm, rotate, quantise and scatter new key rows and rotate and quantise
+    the queries, in one launch (see mla_prologue in mla_decode.h).
+
+    kv_rows BF16 [n_tokens, 576] and q_rows BF16 [n_tokens, num_heads, 576] may
+    be strided views whose last dimension is dense; either may be None.
+    cos_sin is fp32 [rope_rows, 64] (32 cosines, then 32 sines)."""
+    import torch
+    a = PrologueArgs()
+    a.n_tokens = int(n_tokens)
+    a.positions = _device_tensor(positions, "positions", torch.int32)
+    a.rope_halves = 1 if rope_halves else 0
+    if cos_sin is not None:
+        a.cos_sin = _device_tensor(cos_sin, "cos_sin", torch.float32)
+        a.rope_rows = int(cos_sin.shape[0] if rope_rows is None else rope_rows)
+        a.rope_positions = _device_tensor(rope_positions, "rope_positions", torch.int32)
+    a.req_idx = _device_tensor(req_idx, "req_idx", torch.int32)
+    a.status = _device_tensor(status, "status", torch.int32)
+    if kv_rows is not None:
+        a.kv_rows = _device_tensor(kv_rows, "kv_rows", torch.bfloat16, contiguous=False)
+        if kv_rows.dim() != 2 or kv_rows.shape[1] != HEAD_DIM or kv_rows.stride(1) != 1:
+            raise ValueError("kv_rows must be [n_tokens, 576] with dense rows")
+        a.kv_row_stride = kv_rows.stride(0) if kv_rows.shape[0] > 1 else HEAD_DIM
+        a.norm_weight = _device_tensor(norm_weight, "norm_weight", torch.float32)
+        a.norm_eps = float(norm_eps)
+        a.max_pages_per_req = int(max_pages_per_req)
+        a.page_table = _device_tensor(page_table, "page_table", torch.int32)
+        a.kv_pages = _device_tensor(kv_pages, "kv_pages")
+        a.num_pages = int(num_pages)
+        a.batch = int(batch)
+        a.cache_kind = int(cache_kind)
+        a.kv_scale = float(kv_scale)
+    if q_rows is not None:
+        a.q_rows = _device_tensor(q_rows, "q_rows", torch.bfloat16, contiguous=False)
+        if q_rows.dim() != 3 or q_rows.shape[2] != HEAD_DIM or q_rows.stride(2) != 1:
+            raise ValueError("q_rows must be [n_tokens, num_heads, 576] with dense rows")
+        a.q_token_stride = q_rows.stride(0) if q_rows.shape[0] > 1 else 0
+        a.q_head_stride = q_rows.stride(1) if q_rows.shape[1] > 1 else 0
+        a.q_out = _device_tensor(q_out, "q_out")
+        a.num_heads = int(num_heads)
+        a.q_kind = int(q_kind)
+        a.q_scale = float(q_scale)
+    where = kv_rows if kv_rows is not None else q_rows
+    if where is None:
+        raise ValueError("mla_prologue needs kv_rows, q_rows or both")
+    _call_on(where, load_library().mla_prologue, ctypes.byref(a), stream=stream)
+
+
+def mla_pages_copy(src_pool, src_pages: int, src_kind: int, dst_pool, dst_pages: int,
+                   dst_kind: int, src_ids, dst_ids, n: int, rows=None, status=None,
+                   stream=None) -> None:
+    """Copy (or convert, between FP8 and FP4 pools) the first rows[i] rows of
+    page src_ids[i] to page dst_ids[i], i < n; ids and rows are int32 CUDA
+    tensors."""
+    import torch
+    i32 = torch.int32
+    _call_on(dst_pool, load_library().mla_pages_copy, _device_tensor(src_pool, "src_pool"),
+             int(src_pages), int(src_kind), _device_tensor(dst_pool, "dst_pool"), int(dst_pages),
+             int(dst_kind), _device_tensor(src_ids, "src_ids", i32),
+             _device_tensor(dst_ids, "dst_ids", i32), _device_tensor(rows, "rows", i32), int(n),
+             _device_tensor(status, "status", i32), stream=stream)
+
+
+def mla_pages_remap(page_table, n_entries: int, page_map, num_pages: int, status=None,
+                    stream=None) -> None:
+    """Replace every page id p >= 0 of a page table by page_map[p], in place."""
+    import torch
+    i32 = torch.int32
+    _call_on(page_table, load_library().mla_pages_remap,
+             _device_tensor(page_table, "page_table", i32), int(n_entries),
+             _device_tensor(page_map, "page_map", i32), int(num_pages),
+             _device_tensor(status, "status", i32), stream=stream)
+
+
+class PagePool:
+    """Reference-counted pages of one cache (mla_pool_*): which are free, forks
+    and compactions.  Host only; page ids are int32 numpy arrays.  The copies
+    that fork and compact plan run with copy_pages."""
+
+    def __init__(self, num_pages: int):
+        self._lib = load_library()
+        self.num_pages = int(num_pages)
+        handle = ctypes.c_void_p()
+        _check(self._lib.mla_pool_create(self.num_pages, ctypes.byref(handle)))
+        self._handle = handle
+
+    def __del__(self):
+        if getattr(self, "_handle", None):
+            self._lib.mla_pool_destroy(self._handle)
+            self._handle = None
+
+    @property
+    def free_pages(self) -> int:
+        return int(self._lib.mla_pool_free_pages(self._handle))
+
+    def references(self, page: int) -> int:
+        return int(self._lib.mla_pool_references(self._handle, int(page)))
+
+    def alloc(self, n: int) -> np.ndarray:
+        """The n lowest free pages; MlaError (MLA_ERR_NO_PAGES) if fewer are free."""
+        ids = np.zeros(max(0, int(n)), dtype=np.int32)
+        _check(self._lib.mla_pool_alloc(self._handle, int(n), ids.ctypes.data))
+        return ids
+
+    def release(self, ids) -> None:
+        """Give back one reference of each listed page."""
+        ids = np.ascontiguousarray(ids, dtype=np.int32).reshape(-1)
+        _check(self._lib.mla_pool_release(self._handle, ids.ctypes.data, ids.shape[0]))
+
+    def fork(self, ids, kv_len: int, n_forks: int):
+        """Fork a request of kv_len tokens: (page lists [n_forks, pages], src,
+        dst, rows), the last three the copies to make."""
+        ids = np.ascontiguousarray(ids, dtype=np.int32).reshape(-1)
+        pages = (int(kv_len) + PAGE_SIZE - 1) // PAGE_SIZE
+        if ids.shape[0] < pages:
+            raise ValueError(f"kv_len {kv_len} needs {pages} pages, got {ids.shape[0]}")
+        forks = max(0, int(n_forks))
+        out = np.zeros((forks, max(0, pages)), dtype=np.int32)
+        src, dst, rows = (np.zeros(forks, dtype=np.int32) for _ in range(3))
+        n = ctypes.c_int64(0)
+        _check(self._lib.mla_pool_fork(self._handle, ids.ctypes.data, int(kv_len), int(n_forks),
+                                       out.ctypes.data, src.ctypes.data, dst.ctypes.data,
+                                       rows.ctypes.data, ctypes.addressof(n)))
+        k = int(n.value)
+        return out, src[:k], dst[:k], rows[:k]
+
+    def compact(self, max_moves: Optional[int] = None):
+        """Move the pages in use to the low end: (src, dst, map), the copies to
+        make and each page's new id."""
+        cap = self.num_pages if max_moves is None else int(max_moves)
+        src, dst = (np.zeros(max(0, cap), dtype=np.int32) for _ in range(2))
+        page_map = np.zeros(self.num_pages, dtype=np.int32)
+        n = ctypes.c_int64(0)
+        _check(self._lib.mla_pool_compact(self._handle, cap, src.ctypes.data, dst.ctypes.data,
+                                          page_map.ctypes.data, ctypes.addressof(n)))
+        k = int(n.value)
+        return src[:k], dst[:k], page_map
+
+
 def mla_debug_set_wait_limit(cycles: int) -> None:
     """Test hook: limit of the kernel's pipeline waits (0 = default)."""
     load_library().mla_debug_set_wait_limit(int(cycles))
@@ -553,6 +778,63 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
     if check_status:
         mla_decode_status(ws, stream)
     return out, lse, out_f32
+
+
+def fp4_pool(num_pages: int, device="cuda"):
+    """A zeroed 4-bit page pool, uint8 [num_pages, FP4_PAGE_BYTES] (CACHE_FP4)."""
+    import torch
+    return torch.zeros((num_pages, FP4_PAGE_BYTES), dtype=torch.uint8, device=device)
+
+
+def _cache_kind(pool) -> int:
+    """The kind of a page pool, from its type and shape."""
+    import torch
+    if pool.dtype is torch.uint8 and tuple(pool.shape[1:]) == (FP4_PAGE_BYTES,):
+        return CACHE_FP4
+    if tuple(pool.shape[1:]) == (PAGE_SIZE, HEAD_DIM):
+        if pool.dtype in (torch.uint8, torch.float8_e4m3fn):
+            return CACHE_FP8
+        if pool.dtype is torch.bfloat16:
+            return CACHE_BF16
+    raise ValueError("a page pool is uint8 [pages, 32, 576] (E4M3), bfloat16 [pages, 32, 576] "
+                     "or uint8 [pages, 10752] (4 bits)")
+
+
+def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> None:
+    """Copy pages (the lists of PagePool.fork or compact, or any host lists)
+    within a pool or between pools, converting between E4M3 and 4-bit pools.
+
+    Lists in which a page would be written twice, or both read and written,
+    are refused (ValueError): the copies of one call run in no order."""
+    import torch
+    src, dst = (np.ascontiguousarray(x, dtype=np.int32).reshape(-1) for x in (src_ids, dst_ids))
+    if src.shape != dst.shape:
+        raise ValueError("src_ids and dst_ids must have the same length")
+    n = int(src.shape[0])
+    if n == 0:
+        return
+    if src.min() < 0 or src.max() >= src_pool.shape[0] or dst.min() < 0 or \
+            dst.max() >= dst_pool.shape[0]:
+        raise ValueError("page id outside its pool")
+    if np.unique(dst).shape[0] != n:
+        raise ValueError("a page is the destination of two copies")
+    if src_pool.data_ptr() == dst_pool.data_ptr() and np.intersect1d(src, dst).size:
+        raise ValueError("a page is both a source and a destination")
+    lists = [src, dst]
+    if rows is not None:
+        lists.append(np.broadcast_to(np.asarray(rows, dtype=np.int32), (n,)))
+        if lists[2].min() < 0 or lists[2].max() > PAGE_SIZE:
+            raise ValueError("rows must be in 0..32")
+    # One upload for the lists, on the stream that the copy runs on (the lists
+    # are pageable host memory: the upload has read them when it returns).
+    dev = dst_pool.device
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+        lists_d = torch.from_numpy(np.stack(lists)).to(dev)
+        mla_pages_copy(src_pool, src_pool.shape[0], _cache_kind(src_pool), dst_pool,
+                       dst_pool.shape[0], _cache_kind(dst_pool), lists_d[0], lists_d[1], n,
+                       rows=lists_d[2] if rows is not None else None)
 
 
 def merge(partial_o, partial_ml, kv_split: int, want_f32: bool = True, stream=None):

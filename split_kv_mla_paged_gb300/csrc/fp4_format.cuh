@@ -1,0 +1,97 @@
+// The 4-bit cache page: encoding and expansion shared by the prologue, the
+// page operators and the FP4 decode.
+//
+// A page of 32 rows is 10,752 bytes in three planes, so that each plane of a
+// row is contiguous and 16-byte aligned:
+//   [0, 8192)      latent codes: 32 rows x 256 bytes, two E2M1 values a byte
+//   [8192, 8704)   scale codes: 16 blocks x 32 rows, one byte each
+//   [8704, 10752)  rope part: 32 rows x 64 E4M3 codes
+// A block is 32 consecutive latent values of a row.  With scale code e in
+// 0..14 its values are kv_scale * 2^(e - 8) * v, v one of +-{0, .5, 1, 1.5, 2,
+// 3, 4, 6}.  Scale code 15 (and no other) marks a block with a NaN: every
+// value of it reads as NaN.  Only the low 4 bits of a scale byte count.
+//
+// 2^(e - 8) * v is an E4M3 number for every e in 0..14 (the smallest step,
+// 2^-9, is E4M3's, and 6 * 2^6 = 384 <= 448), so a block expands to E4M3 codes
+// without any rounding: the decode's tensor-core path and every result over an
+// FP4 cache equal those over the E4M3 cache that it expands to.
+//
+// Bit layout of a 32-bit word (8 consecutive values, little endian): the low
+// three bits of nibble j are value j's magnitude code; the top bits of nibbles
+// 1, 3, 5, 7 are the signs of values 0 to 3 and those of nibbles 0, 2, 4, 6
+// the signs of values 4 to 7.  The magnitudes are then byte-permute selectors
+// into the scale's eight E4M3 codes, and the signs of values 0-3 already sit
+// at the four bytes' sign bits: 7 instructions expand 8 values, where signs
+// kept in their own nibbles need 9.
+#pragma once
+#include <cstdint>
+
+#include "mla_internal.h"
+
+namespace mla {
+
+constexpr int kFp4RowCodes = MLA_LATENT_DIM / 2;                                // 256 bytes
+constexpr int kFp4Blocks = MLA_LATENT_DIM / MLA_FP4_BLOCK;                      // 16
+constexpr int kFp4ScaleOffset = MLA_PAGE_SIZE * kFp4RowCodes;                   // 8192
+constexpr int kFp4RopeOffset = kFp4ScaleOffset + kFp4Blocks * MLA_PAGE_SIZE;    // 8704
+static_assert(kFp4RopeOffset + MLA_PAGE_SIZE * MLA_ROPE_DIM == MLA_FP4_PAGE_BYTES, "FP4 page");
+constexpr int kFp4NanScale = 15;
+
+#ifdef __CUDACC__
+// Scale code of a block from its largest magnitude (as float bits without the
+// sign; a NaN's bits are above infinity's): the smallest e in 0..14 with
+// amax <= 7 * 2^(e - 8), 14 where none is.  7 is half a step above the largest
+// code, 6, so under that scale no value is more than half a step from its code;
+// larger values saturate at 384.  7 * 2^(k - 8) has the bits ((121 + k) << 23)
+// + 0x600000, and positive floats order like their bits.
+__device__ __forceinline__ int fp4_scale_code(uint32_t amax_bits) {
+  if (amax_bits > 0x7F800000u) return kFp4NanScale;
+  const int k = ((static_cast<int>(amax_bits) - 0x600001) >> 23) - 120;
+  return min(max(k, 0), 14);
+}
+
+// 2^(8 - e), exactly.
+__device__ __forceinline__ float fp4_inv_scale(int e) { return __int_as_float((135 - e) << 23); }
+
+// Eight values times 2^(8 - e) as one word of the format: nearest E2M1, ties
+// to even, saturating at 6.
+__device__ __forceinline__ uint32_t fp4_encode8(const float (&x)[8], float inv) {
+  uint32_t w;
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+      " mov.b32 %0, {b0, b1, b2, b3};\n}"
+      : "=r"(w)
+      : "f"(x[0] * inv), "f"(x[1] * inv), "f"(x[2] * inv), "f"(x[3] * inv), "f"(x[4] * inv),
+        "f"(x[5] * inv), "f"(x[6] * inv), "f"(x[7] * inv));
+  // Signs from their own nibbles (bits 4j + 3) to the format's places.
+  const uint32_t up = w << 4;  // even nibbles' signs at their bytes' top bits
+  const uint32_t lo = __byte_perm(up, w, 0x5140) & 0x80808080u;         // values 0-3
+  const uint32_t hi = (__byte_perm(up, w, 0x7362) & 0x80808080u) >> 4;  // values 4-7
+  return (w & 0x77777777u) | lo | hi;
+}
+
+// The eight E4M3 codes of scale code e's magnitudes, as two words (e = 15: NaN).
+__device__ __forceinline__ uint2 fp4_table_entry(int e) {
+  if (e == kFp4NanScale) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  const float s = __int_as_float((119 + e) << 23);  // 2^(e - 8)
+  uint16_t a, b, c, d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(0.5f * s), "f"(0.0f));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(1.5f * s), "f"(s));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(3.0f * s), "f"(2.0f * s));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(6.0f * s), "f"(4.0f * s));
+  return make_uint2(a | (static_cast<uint32_t>(b) << 16), c | (static_cast<uint32_t>(d) << 16));
+}
+
+// Expands a word of the format to the E4M3 codes of its eight values.
+__device__ __forceinline__ uint2 fp4_expand8(uint32_t w, uint2 table) {
+  const uint32_t sel = w & 0x77777777u;
+  const uint32_t lo = __byte_perm(table.x, table.y, sel);
+  const uint32_t hi = __byte_perm(table.x, table.y, sel >> 16);
+  return make_uint2(lo | (w & 0x80808080u), hi | ((w << 4) & 0x80808080u));
+}
+#endif
+
+}  // namespace mla

@@ -1,0 +1,236 @@
+// Page operators: copies of pages within and between pools (forks,
+// compaction), conversion between the E4M3 and the 4-bit cache (demotion,
+// promotion) and the rewrite of page tables after a compaction.
+//
+// All of it is data movement: bound by the bytes read and written.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+#include "fp4_format.cuh"
+#include "mla_device.cuh"
+
+namespace mla {
+
+constexpr int kCopyThreads = 256;
+
+struct PagesParams {
+  const uint8_t* src;
+  uint8_t* dst;
+  int64_t src_pages, dst_pages;
+  const int32_t* src_ids;
+  const int32_t* dst_ids;
+  const int32_t* rows;
+  int32_t* status;
+};
+
+// Entry i: its pages and row count; false where it is skipped (-1) or bad
+// (reported by one thread of the CTA).
+__device__ __forceinline__ bool pages_entry(const PagesParams& p, int64_t i, int64_t& s,
+                                            int64_t& d, int& rows) {
+  s = __ldg(p.src_ids + i);
+  d = __ldg(p.dst_ids + i);
+  rows = p.rows ? __ldg(p.rows + i) : MLA_PAGE_SIZE;
+  if (s == -1 || d == -1) return false;
+  if (s < 0 || s >= p.src_pages || d < 0 || d >= p.dst_pages || rows < 0 ||
+      rows > MLA_PAGE_SIZE) {
+    if (p.status && threadIdx.x == 0) atomicCAS(p.status, 0, MLA_ERR_INVALID_ARG);
+    return false;
+  }
+  return true;
+}
+
+// Copies `n` 16-byte vectors with the CTA's threads.
+__device__ __forceinline__ void copy_vectors(const uint8_t* s, uint8_t* d, int n) {
+  const uint4* sv = reinterpret_cast<const uint4*>(s);
+  uint4* dv = reinterpret_cast<uint4*>(d);
+  for (int k = threadIdx.x; k < n; k += kCopyThreads) dv[k] = sv[k];
+}
+
+// Same-kind copy: one CTA per entry.  A page of kRowBytes-byte rows is
+// contiguous; the FP4 page has three planes.
+template <int kRowBytes>
+__global__ void __launch_bounds__(kCopyThreads) mla_pages_copy_kernel(const PagesParams p) {
+  int64_t sp, dp;
+  int rows;
+  if (!pages_entry(p, blockIdx.x, sp, dp, rows)) return;
+  constexpr int64_t kPage = static_cast<int64_t>(kRowBytes) * MLA_PAGE_SIZE;
+  copy_vectors(p.src + sp * kPage, p.dst + dp * kPage, rows * (kRowBytes / 16));
+}
+
+__global__ void __launch_bounds__(kCopyThreads) mla_pages_copy_fp4_kernel(const PagesParams p) {
+  int64_t sp, dp;
+  int rows;
+  if (!pages_entry(p, blockIdx.x, sp, dp, rows)) return;
+  const uint8_t* s = p.src + sp * MLA_FP4_PAGE_BYTES;
+  uint8_t* d = p.dst + dp * MLA_FP4_PAGE_BYTES;
+  if (rows == MLA_PAGE_SIZE) {
+    copy_vectors(s, d, MLA_FP4_PAGE_BYTES / 16);
+    return;
+  }
+  copy_vectors(s, d, rows * (kFp4RowCodes / 16));
+  copy_vectors(s + kFp4RopeOffset, d + kFp4RopeOffset, rows * (MLA_ROPE_DIM / 16));
+  for (int k = threadIdx.x; k < kFp4Blocks * MLA_PAGE_SIZE; k += kCopyThreads)
+    if (k % MLA_PAGE_SIZE < rows) d[kFp4ScaleOffset + k] = s[kFp4ScaleOffset + k];
+}
+
+// Demotion: one CTA per entry, one warp per row at a time.  A row's latent
+// part is 32 16-byte vectors of 16 E4M3 values, one per lane: a block of the
+// 4-bit format is two lanes.
+__global__ void __launch_bounds__(kCopyThreads) mla_pages_demote_kernel(const PagesParams p) {
+  int64_t sp, dp;
+  int rows;
+  if (!pages_entry(p, blockIdx.x, sp, dp, rows)) return;
+  const uint8_t* s = p.src + sp * (MLA_PAGE_SIZE * MLA_HEAD_DIM);
+  uint8_t* d = p.dst + dp * MLA_FP4_PAGE_BYTES;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int row = warp; row < rows; row += kCopyThreads / 32) {
+    const uint4* sv = reinterpret_cast<const uint4*>(s + row * MLA_HEAD_DIM);
+    const uint4 v = sv[lane];
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if (lane < 4) r = sv[32 + lane];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float x[2][8];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = unpack_e4m3x2(static_cast<uint16_t>(w[k] & 0xFFFFu));
+      const float2 b = unpack_e4m3x2(static_cast<uint16_t>(w[k] >> 16));
+      float* o = &x[k >> 1][4 * (k & 1)];
+      o[0] = a.x;
+      o[1] = a.y;
+      o[2] = b.x;
+      o[3] = b.y;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) amax = max(amax, __float_as_uint(o[m]) & 0x7FFFFFFFu);
+    }
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const int e = fp4_scale_code(amax);
+    const float inv = fp4_inv_scale(e);
+    uint2 c = make_uint2(0u, 0u);
+    if (e != kFp4NanScale) c = make_uint2(fp4_encode8(x[0], inv), fp4_encode8(x[1], inv));
+    reinterpret_cast<uint2*>(d + row * kFp4RowCodes)[lane] = c;
+    if ((lane & 1) == 0)
+      d[kFp4ScaleOffset + (lane >> 1) * MLA_PAGE_SIZE + row] = static_cast<uint8_t>(e);
+    if (lane < 4)
+      reinterpret_cast<uint4*>(d + kFp4RopeOffset + row * MLA_ROPE_DIM)[lane] = r;
+  }
+}
+
+// Promotion: one CTA per entry.  A 16-byte vector of codes is one block: 32
+// E4M3 codes out.
+__global__ void __launch_bounds__(kCopyThreads) mla_pages_promote_kernel(const PagesParams p) {
+  __shared__ uint2 table[16];
+  if (threadIdx.x < 16) table[threadIdx.x] = fp4_table_entry(threadIdx.x);
+  __syncthreads();
+  int64_t sp, dp;
+  int rows;
+  if (!pages_entry(p, blockIdx.x, sp, dp, rows)) return;
+  const uint8_t* s = p.src + sp * MLA_FP4_PAGE_BYTES;
+  uint8_t* d = p.dst + dp * (MLA_PAGE_SIZE * MLA_HEAD_DIM);
+  for (int k = threadIdx.x; k < rows * kFp4Blocks; k += kCopyThreads) {
+    const int row = k / kFp4Blocks, blk = k % kFp4Blocks;
+    const uint4 v = reinterpret_cast<const uint4*>(s)[k];
+    const uint2 t = table[s[kFp4ScaleOffset + blk * MLA_PAGE_SIZE + row] & 15];
+    const uint2 a = fp4_expand8(v.x, t), b = fp4_expand8(v.y, t);
+    const uint2 c = fp4_expand8(v.z, t), e = fp4_expand8(v.w, t);
+    uint4* o = reinterpret_cast<uint4*>(d + row * MLA_HEAD_DIM) + 2 * blk;
+    o[0] = make_uint4(a.x, a.y, b.x, b.y);
+    o[1] = make_uint4(c.x, c.y, e.x, e.y);
+  }
+  for (int k = threadIdx.x; k < rows * 4; k += kCopyThreads)
+    reinterpret_cast<uint4*>(d + (k / 4) * MLA_HEAD_DIM + MLA_LATENT_DIM)[k % 4] =
+        reinterpret_cast<const uint4*>(s + kFp4RopeOffset)[k];
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    mla_pages_remap_kernel(int32_t* __restrict__ table, int64_t n,
+                           const int32_t* __restrict__ map, int64_t num_pages, int32_t* status) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
+  if (i >= n) return;
+  const int32_t page = table[i];
+  if (page < 0) return;
+  if (page >= num_pages) {
+    if (status) atomicCAS(status, 0, MLA_ERR_INVALID_ARG);
+    return;
+  }
+  table[i] = __ldg(map + page);
+}
+
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_pages_copy(const void* src_pool, int64_t src_pages, int32_t src_kind,
+                              void* dst_pool, int64_t dst_pages, int32_t dst_kind,
+                              const int32_t* src_ids, const int32_t* dst_ids, const int32_t* rows,
+                              int64_t n, int32_t* status, void* stream) {
+  auto bad = [](const char* what) {
+    set_error(std::string("mla_pages_copy: ") + what);
+    return MLA_ERR_INVALID_ARG;
+  };
+  auto known = [](int32_t k) {
+    return k == MLA_CACHE_FP8 || k == MLA_CACHE_BF16 || k == MLA_CACHE_FP4;
+  };
+  if (n < 0 || src_pages < 1 || dst_pages < 1) return bad("n >= 0, src_pages and dst_pages >= 1");
+  if (!known(src_kind) || !known(dst_kind)) return bad("unknown cache kind");
+  if (src_kind != dst_kind && (src_kind == MLA_CACHE_BF16 || dst_kind == MLA_CACHE_BF16)) {
+    set_error("mla_pages_copy: BF16 pages are only copied to BF16 pools");
+    return MLA_ERR_UNSUPPORTED;
+  }
+  if (src_kind != dst_kind && src_pool && src_pool == dst_pool)
+    return bad("one pool has one kind");
+  if (n == 0) return MLA_OK;
+  if (!src_pool || !dst_pool || !src_ids || !dst_ids) return bad("null pointer argument");
+  if (!aligned(src_pool, 16) || !aligned(dst_pool, 16))
+    return bad("the pools need 16-byte alignment");
+  if (n > 0x7FFFFFFF) {
+    set_error("mla_pages_copy: too many pages for one launch");
+    return MLA_ERR_UNSUPPORTED;
+  }
+  PagesParams p;
+  p.src = reinterpret_cast<const uint8_t*>(src_pool);
+  p.dst = reinterpret_cast<uint8_t*>(dst_pool);
+  p.src_pages = src_pages;
+  p.dst_pages = dst_pages;
+  p.src_ids = src_ids;
+  p.dst_ids = dst_ids;
+  p.rows = rows;
+  p.status = status;
+  void (*kernel)(PagesParams) = mla_pages_copy_kernel<MLA_HEAD_DIM>;
+  if (src_kind != dst_kind)
+    kernel = dst_kind == MLA_CACHE_FP4 ? mla_pages_demote_kernel : mla_pages_promote_kernel;
+  else if (src_kind == MLA_CACHE_BF16)
+    kernel = mla_pages_copy_kernel<2 * MLA_HEAD_DIM>;
+  else if (src_kind == MLA_CACHE_FP4)
+    kernel = mla_pages_copy_fp4_kernel;
+  kernel<<<static_cast<unsigned>(n), kCopyThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail("mla_pages_copy: launch", e);
+  return MLA_OK;
+}
+
+extern "C" int mla_pages_remap(int32_t* page_table, int64_t n_entries, const int32_t* page_map,
+                               int64_t num_pages, int32_t* status, void* stream) {
+  if (n_entries < 0 || num_pages < 1) {
+    set_error("mla_pages_remap: n_entries >= 0 and num_pages >= 1");
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (n_entries == 0) return MLA_OK;
+  if (!page_table || !page_map) {
+    set_error("mla_pages_remap: null pointer argument");
+    return MLA_ERR_INVALID_ARG;
+  }
+  const int64_t blocks = (n_entries + kCopyThreads - 1) / kCopyThreads;
+  if (blocks > 0x7FFFFFFF) {
+    set_error("mla_pages_remap: too many entries for one launch");
+    return MLA_ERR_UNSUPPORTED;
+  }
+  mla_pages_remap_kernel<<<static_cast<unsigned>(blocks), kCopyThreads, 0,
+                           reinterpret_cast<cudaStream_t>(stream)>>>(page_table, n_entries,
+                                                                     page_map, num_pages, status);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail("mla_pages_remap: launch", e);
+  return MLA_OK;
+}
