@@ -379,6 +379,38 @@ MLA_API int mla_decode_bf16_sparse(const void* q_bf16, const void* kv_pages_bf16
                                    float* out_f32_debug, const mla_decode_options_t* options,
                                    void* stream);
 
+/*
+ * Decode over a 4-bit cache (MLA_CACHE_FP4), dense and over selected pages:
+ * mla_decode_ex and mla_decode_sparse with kv_pages_fp4 uint8 [num_pages,
+ * MLA_FP4_PAGE_BYTES], 16-byte aligned.  Q is E4M3; a key's values are kv_scale
+ * times those of its codes.  Plans, workspace, status, outputs and options are
+ * as there; item lists come from mla_decode_plan_items_bf16 (row groups of at
+ * most 48 rows), and persistent_ctas is MLA_ERR_UNSUPPORTED.  options may be
+ * NULL.  Outputs are those of mla_decode over the E4M3 cache that the pages
+ * expand to (bit for bit where both have the same row groups: up to 48 rows);
+ * a NaN among a request's keys (a later draft token's under causal included)
+ * leaves its rows without a defined result, as there; NaNs or stale bytes past
+ * kv_lens, outside kv_bounds or in pages that are not selected have no effect.
+ */
+MLA_API int mla_decode_fp4(const void* q_fp8, const void* kv_pages_fp4, int64_t num_pages,
+                           const int32_t* page_table, int32_t max_pages_per_req,
+                           const int32_t* kv_lens, const int32_t* splits, const int32_t* chunks,
+                           int32_t max_splits, int32_t kv_split, int32_t batch, int32_t q_len,
+                           int32_t num_heads, int32_t causal, float q_scale, float kv_scale,
+                           float softmax_scale, void* workspace, size_t workspace_bytes,
+                           void* out_bf16, float* lse_f32, float* out_f32_debug,
+                           const mla_decode_options_t* options, void* stream);
+MLA_API int mla_decode_fp4_sparse(const void* q_fp8, const void* kv_pages_fp4,
+                                  int64_t num_pages, const int32_t* page_table,
+                                  int32_t max_pages_per_req, const int32_t* kv_lens,
+                                  const int32_t* block_idx, int32_t topk, const int32_t* splits,
+                                  const int32_t* chunks, int32_t max_splits, int32_t kv_split,
+                                  int32_t batch, int32_t q_len, int32_t num_heads,
+                                  int32_t causal, float q_scale, float kv_scale,
+                                  float softmax_scale, void* workspace, size_t workspace_bytes,
+                                  void* out_bf16, float* lse_f32, float* out_f32_debug,
+                                  const mla_decode_options_t* options, void* stream);
+
 /* Zero the 256-byte status header of a new workspace (async on `stream`).
  * Call once per workspace before its first mla_decode; after that the
  * header only changes when the device reports a condition, and

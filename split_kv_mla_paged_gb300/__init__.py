@@ -26,7 +26,7 @@ __all__ = [
     "mla_decode_bf16", "mla_decode_sparse", "mla_decode_plan_items", "mla_decode_bf16_ex",
     "mla_decode_bf16_sparse", "mla_decode_plan_items_bf16", "DecodeOptions",
     "decode", "merge", "MLA_ERR_NO_PAGES", "CACHE_FP8", "CACHE_BF16", "CACHE_FP4",
-    "FP4_PAGE_BYTES", "PrologueArgs", "mla_prologue", "mla_pages_copy", "mla_pages_remap",
+    "FP4_PAGE_BYTES", "mla_decode_fp4", "mla_decode_fp4_sparse", "PrologueArgs", "mla_prologue", "mla_pages_copy", "mla_pages_remap",
     "PagePool", "copy_pages", "fp4_pool",
     "EXPORTED_SYMBOLS",
 ]
@@ -50,6 +50,7 @@ EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_workspace_size", "mla_decode_
                     "mla_decode_ex", "mla_decode_bf16", "mla_decode_sparse",
                     "mla_decode_plan_items", "mla_decode_bf16_ex", "mla_decode_bf16_sparse",
                     "mla_decode_plan_items_bf16", "mla_debug_set_expire", "mla_prologue",
+                    "mla_decode_fp4", "mla_decode_fp4_sparse",
                     "mla_pages_copy", "mla_pages_remap", "mla_pool_create", "mla_pool_destroy",
                     "mla_pool_free_pages", "mla_pool_references", "mla_pool_alloc",
                     "mla_pool_release", "mla_pool_fork", "mla_pool_compact")
@@ -142,6 +143,10 @@ def load_library() -> ctypes.CDLL:
         lib.mla_decode_sparse.restype = ctypes.c_int
         lib.mla_decode_sparse.argtypes = (dec_args[:6] + [vp, i32] + dec_args[6:-1]
                                           + [ctypes.POINTER(DecodeOptions), vp])
+        lib.mla_decode_fp4.restype = ctypes.c_int
+        lib.mla_decode_fp4.argtypes = lib.mla_decode_ex.argtypes
+        lib.mla_decode_fp4_sparse.restype = ctypes.c_int
+        lib.mla_decode_fp4_sparse.argtypes = lib.mla_decode_sparse.argtypes
         lib.mla_decode_bf16.restype = ctypes.c_int
         lib.mla_decode_bf16.argtypes = dec_args[:14] + [f32] + dec_args[17:]
         lib.mla_decode_bf16_ex.restype = ctypes.c_int
@@ -410,6 +415,64 @@ def mla_decode_sparse(q_fp8, kv_pages_fp8, num_pages, page_table, max_pages_per_
                                  int(workspace_bytes), _ptr(out_bf16), _ptr(lse_f32),
                                  _ptr(out_f32_debug), ctypes.byref(opts),
                                  _stream_handle(stream)))
+
+
+def _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks, query_lens,
+                 kv_bounds, cta_items, phases):
+    """The options structure, or None where every option is off."""
+    if (q_scale_dev is None and kv_scale_dev is None and softmax_scale_dev is None
+            and output_scale == 1.0 and sinks is None and query_lens is None
+            and kv_bounds is None and cta_items is None and phases == PHASE_ALL):
+        return None
+    return ctypes.byref(DecodeOptions(
+        _ptr(q_scale_dev), _ptr(kv_scale_dev), _ptr(softmax_scale_dev), float(output_scale),
+        _ptr(sinks), _ptr(query_lens), _ptr(kv_bounds), _ptr(cta_items),
+        0 if cta_items is None else int(cta_items.numel()), 0, int(phases)))
+
+
+def _fp4_pages(pool) -> int:
+    import torch
+    if pool.dim() != 2 or pool.shape[1] != FP4_PAGE_BYTES:
+        raise ValueError(f"a 4-bit page pool is uint8 [pages, {FP4_PAGE_BYTES}]")
+    return _device_tensor(pool, "kv_pages_fp4", torch.uint8)
+
+
+def mla_decode_fp4(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req, kv_lens, splits,
+                   chunks, max_splits, kv_split, batch, q_len, num_heads, causal, q_scale,
+                   kv_scale, softmax_scale, workspace, workspace_bytes, out_bf16, lse_f32=None,
+                   out_f32_debug=None, *, q_scale_dev=None, kv_scale_dev=None,
+                   softmax_scale_dev=None, output_scale: float = 1.0, sinks=None,
+                   query_lens=None, kv_bounds=None, cta_items=None, phases: int = PHASE_ALL,
+                   stream=None) -> None:
+    """Decode over a 4-bit cache, uint8 [pages, FP4_PAGE_BYTES]; options as for
+    mla_decode_ex (no persistent CTAs; item lists from
+    mla_decode_plan_items_bf16)."""
+    opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
+                        query_lens, kv_bounds, cta_items, phases)
+    _call_on(q_fp8, load_library().mla_decode_fp4, _ptr(q_fp8), _fp4_pages(kv_pages_fp4),
+             num_pages, _ptr(page_table), max_pages_per_req, _ptr(kv_lens), _ptr(splits),
+             _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads, 1 if causal else 0,
+             q_scale, kv_scale, softmax_scale, _ptr(workspace), workspace_bytes, _ptr(out_bf16),
+             _ptr(lse_f32), _ptr(out_f32_debug), opts, stream=stream)
+
+
+def mla_decode_fp4_sparse(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req, kv_lens,
+                          block_idx, topk, splits, chunks, max_splits, kv_split, batch, q_len,
+                          num_heads, causal, q_scale, kv_scale, softmax_scale, workspace,
+                          workspace_bytes, out_bf16, lse_f32=None, out_f32_debug=None, *,
+                          q_scale_dev=None, kv_scale_dev=None, softmax_scale_dev=None,
+                          output_scale: float = 1.0, sinks=None, query_lens=None, kv_bounds=None,
+                          cta_items=None, phases: int = PHASE_ALL, stream=None) -> None:
+    """Sparse decode over the selected pages block_idx [batch, topk] of a 4-bit
+    cache (plan with the compact lengths 32 * topk)."""
+    opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
+                        query_lens, kv_bounds, cta_items, phases)
+    _call_on(q_fp8, load_library().mla_decode_fp4_sparse, _ptr(q_fp8), _fp4_pages(kv_pages_fp4),
+             num_pages, _ptr(page_table), max_pages_per_req, _ptr(kv_lens), _ptr(block_idx), topk,
+             _ptr(splits), _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads,
+             1 if causal else 0, q_scale, kv_scale, softmax_scale, _ptr(workspace),
+             workspace_bytes, _ptr(out_bf16), _ptr(lse_f32), _ptr(out_f32_debug), opts,
+             stream=stream)
 
 
 def mla_decode_splitkv(*args, **kw) -> None:
@@ -688,7 +751,8 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
     q_fp8 uint8 [B, q, H, 576] and kv_pages_fp8 uint8 [P, 32, 576] (E4M3 codes)
     and page_table int32 [B, max_pages] are CUDA tensors; kv_lens is a host
     sequence.  With torch.bfloat16 q and kv this runs mla_decode_bf16 (no
-    q/kv scales there).  query_lens [B], kv_bounds [B, 2] and block_idx
+    q/kv scales there), with a 4-bit pool (uint8 [P, FP4_PAGE_BYTES])
+    mla_decode_fp4.  query_lens [B], kv_bounds [B, 2] and block_idx
     [B, topk] (selected pages: mla_decode_sparse / mla_decode_bf16_sparse,
     planned on the compact lengths) restrict the visible keys.  use_items
     (default: when the plan has empty split slots) launches the split kernel
@@ -723,10 +787,13 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
     if use_items is None:
         use_items = bool(np.any(plan.splits < plan.max_splits)) or persistent_ctas > 0
     is_bf16 = q_fp8.dtype == torch.bfloat16
+    is_fp4 = not is_bf16 and kv_pages_fp8.dim() == 2
+    if is_fp4 and persistent_ctas > 0:
+        raise ValueError("the 4-bit cache has no persistent CTAs")
     items_d = None
     if use_items:
         items_d = torch.from_numpy(
-            mla_decode_plan_items(plan.splits, num_heads, q_len, bf16=is_bf16)).to(dev)
+            mla_decode_plan_items(plan.splits, num_heads, q_len, bf16=is_bf16 or is_fp4)).to(dev)
 
     def _dev_i32(x):
         return None if x is None else torch.as_tensor(x, dtype=torch.int32).to(dev).contiguous()
@@ -752,7 +819,7 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
                 mla_decode_bf16_sparse(*common[:6], bi_d, topk, *common[6:], sm_h, ws, ws_bytes,
                                        out, lse, out_f32, **extra)
     elif (sinks is None and output_scale == 1.0 and not device_scales and not restricted
-          and items_d is None and persistent_ctas == 0):
+          and items_d is None and persistent_ctas == 0 and not is_fp4):
         mla_decode(*common, q_scale, kv_scale, softmax_scale, ws, ws_bytes, out, lse, out_f32,
                    stream)
     else:
@@ -769,7 +836,17 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
                      kv_scale_dev=None if dev_s is None else dev_s[1:2],
                      softmax_scale_dev=None if dev_s is None else dev_s[2:3],
                      output_scale=output_scale, sinks=sk, query_lens=ql_d, kv_bounds=kb_d,
-                     cta_items=items_d, persistent_ctas=persistent_ctas, stream=stream)
+                     cta_items=items_d, stream=stream)
+        if is_fp4:
+            if bi_d is None:
+                mla_decode_fp4(*common, *host, ws, ws_bytes, out, lse, out_f32, **extra)
+            else:
+                mla_decode_fp4_sparse(*common[:6], bi_d, topk, *common[6:], *host, ws, ws_bytes,
+                                      out, lse, out_f32, **extra)
+            if check_status:
+                mla_decode_status(ws, stream)
+            return out, lse, out_f32
+        extra["persistent_ctas"] = persistent_ctas
         if bi_d is None:
             mla_decode_ex(*common, *host, ws, ws_bytes, out, lse, out_f32, **extra)
         else:

@@ -10,6 +10,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_NAME = "libmla_decode.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = [os.path.join(CSRC, "mla_decode.cu"), os.path.join(CSRC, "mla_decode_bf16.cu"),
+           os.path.join(CSRC, "mla_decode_fp4.cu"),
            os.path.join(CSRC, "mla_merge.cu"), os.path.join(CSRC, "kv_append.cu"),
            os.path.join(CSRC, "prologue.cu"), os.path.join(CSRC, "pages.cu"),
            os.path.join(CSRC, "page_pool.cpp"), os.path.join(CSRC, "plan.cpp")]
@@ -18,6 +19,7 @@ DEPENDS = SOURCES + [
     os.path.join(CSRC, "mla_internal.h"),
     os.path.join(CSRC, "sm103_ptx.cuh"),
     os.path.join(CSRC, "mla_device.cuh"),
+    os.path.join(CSRC, "mla_split_kv.cuh"),
     os.path.join(CSRC, "fp4_format.cuh"),
     os.path.join(os.path.dirname(HERE), "include", "mla_decode.h"),
 ]

@@ -85,6 +85,22 @@ __device__ __forceinline__ uint2 fp4_table_entry(int e) {
   return make_uint2(a | (static_cast<uint32_t>(b) << 16), c | (static_cast<uint32_t>(d) << 16));
 }
 
+// The same table by arithmetic, for kernels without room for one in shared
+// memory: from e = 3 up all codes are normal E4M3 numbers, 4 (e - 2) eighths
+// of an exponent step apart from e = 2's pattern, so each word is one
+// multiply-add; the few smaller scales and NaN blocks take their constants.
+__device__ __forceinline__ uint2 fp4_scale_table(uint32_t e) {
+  uint2 t = make_uint2(0x0C080000u + (e - 2u) * 0x08080800u,
+                       0x1C181410u + (e - 2u) * 0x08080808u);
+  if (e - 3u >= 12u) {
+    t = e == 0 ? make_uint2(0x03020100u, 0x0C080604u)
+        : e == 1 ? make_uint2(0x06040200u, 0x14100C08u)
+        : e == 2 ? make_uint2(0x0C080400u, 0x1C181410u)
+                 : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  }
+  return t;
+}
+
 // Expands a word of the format to the E4M3 codes of its eight values.
 __device__ __forceinline__ uint2 fp4_expand8(uint32_t w, uint2 table) {
   const uint32_t sel = w & 0x77777777u;

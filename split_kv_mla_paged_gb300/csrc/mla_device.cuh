@@ -70,6 +70,7 @@ struct DecodeParams {
   __nv_bfloat16* out;
   float* lse;
   float* out_f32;
+  const uint8_t* kv_fp4;   // 4-bit page pool (mla_decode_fp4 only)
 };
 
 // Barrier indices inside the aux block.  The BF16 kernels use the first 17;

@@ -163,6 +163,34 @@ def test_prologue_other_refusals(lib):
     assert lib.mla_prologue(_args(n_tokens=0, positions=None), None) == mla.MLA_OK  # touches nothing
 
 
+def test_decode_fp4_refusals(lib):
+    args = [FAKE, FAKE, 4, FAKE, 4, FAKE, FAKE, FAKE, 2, 2, 1, 1, 12, 0, 1.0, 1.0, 0.1, FAKE, 1 << 30, FAKE, None, None]
+
+    def call(opts=None, **at):
+        a = list(args)
+        for k, v in at.items():
+            a[int(k[1:])] = v
+        return lib.mla_decode_fp4(*a, None if opts is None else ctypes.byref(opts), None)
+    for at in (dict(a0=None), dict(a1=None), dict(a1=FAKE + 8), dict(a2=0), dict(a3=None), dict(a10=0), dict(a8=0), dict(a9=3),
+               dict(a16=float("nan")), dict(a17=None), dict(a19=None)):
+        assert call(**at) == mla.MLA_ERR_INVALID_ARG, at
+    assert call(a11=8, a12=256) == mla.MLA_ERR_UNSUPPORTED  # rows
+    assert call(a2=1 << 27) == mla.MLA_ERR_UNSUPPORTED      # pool too large for 32-bit rows
+    assert call(a18=16) == mla.MLA_ERR_WORKSPACE_TOO_SMALL
+    O = mla.DecodeOptions
+    assert call(O(None, None, None, 1.0, None, None, None, FAKE, 2, 1)) == mla.MLA_ERR_UNSUPPORTED
+    assert "persistent" in mla.mla_last_error()
+    assert call(O(None, None, None, float("inf"))) == mla.MLA_ERR_INVALID_ARG
+    assert call(O(None, None, None, 1.0, None, None, None, FAKE, 0)) == mla.MLA_ERR_INVALID_ARG
+    assert call(O(None, None, None, 1.0, None, None, None, None, 0, 0, 3)) == mla.MLA_ERR_INVALID_ARG
+    # 96 rows are two row groups, so an item list may be twice as long as splits.
+    assert call(O(None, None, None, 1.0, None, None, None, FAKE, 5), a11=8) == mla.MLA_ERR_INVALID_ARG
+    sp = args[:6] + [FAKE, 8] + args[6:]
+    assert lib.mla_decode_fp4_sparse(*sp[:6], None, *sp[7:], None, None) == mla.MLA_ERR_INVALID_ARG
+    assert lib.mla_decode_fp4_sparse(*sp[:7], 0, *sp[8:], None, None) == mla.MLA_ERR_INVALID_ARG
+    assert lib.mla_decode_fp4_sparse(*sp[:20], 16, *sp[21:], None, None) == mla.MLA_ERR_WORKSPACE_TOO_SMALL
+
+
 def test_pages_copy_refusals(lib):
     def copy(src=FAKE, sp=4, sk=0, dst=2 * FAKE, dp=4, dk=0, si=FAKE, di=FAKE, n=2):
         return lib.mla_pages_copy(src, sp, sk, dst, dp, dk, si, di, None, n, None, None)
