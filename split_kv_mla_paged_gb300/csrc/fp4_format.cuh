@@ -86,12 +86,16 @@ __device__ __forceinline__ uint2 fp4_table_entry(int e) {
 }
 
 // The same table by arithmetic, for kernels without room for one in shared
-// memory: from e = 3 up all codes are normal E4M3 numbers, 4 (e - 2) eighths
-// of an exponent step apart from e = 2's pattern, so each word is one
-// multiply-add; the few smaller scales and NaN blocks take their constants.
+// memory: from e = 3 to 14 all codes are normal E4M3 numbers, e - 2 exponents
+// above e = 2's pattern, so each word is one multiply-add.
+__device__ __forceinline__ uint2 fp4_scale_table_normal(uint32_t e) {
+  return make_uint2(0x0C080000u - 2u * 0x08080800u + e * 0x08080800u,
+                    0x1C181410u - 2u * 0x08080808u + e * 0x08080808u);
+}
+
+// For every e: the smaller scales and NaN blocks take their constants.
 __device__ __forceinline__ uint2 fp4_scale_table(uint32_t e) {
-  uint2 t = make_uint2(0x0C080000u + (e - 2u) * 0x08080800u,
-                       0x1C181410u + (e - 2u) * 0x08080808u);
+  uint2 t = fp4_scale_table_normal(e);
   if (e - 3u >= 12u) {
     t = e == 0 ? make_uint2(0x03020100u, 0x0C080604u)
         : e == 1 ? make_uint2(0x06040200u, 0x14100C08u)

@@ -45,7 +45,8 @@ struct Cfg {
   static_assert(kTmemUsed <= 512, "TMEM");
   // Softmax warpgroups: two (each owning half the rows) from 32 rows up,
   // three (32 rows each) for the 96-row configuration.
-  static constexpr int SWG = kWide ? 3 : NR >= 32 ? 2 : 1;
+  // (4-bit cache: two for 16 rows as well, whose tiles come 1.7 times as fast.)
+  static constexpr int SWG = kWide ? 3 : (NR >= 32 || kFp4) ? 2 : 1;
   static constexpr int NRH = NR / SWG;
   static_assert(NRH % 8 == 0, "rows per softmax warpgroup");
   // Warp 0 TMA, warp 1 QK issuer (and TMEM owner), warp 2 PV issuer, then
@@ -891,8 +892,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       // page, a "chunk") at a time, each lane loads one 16-byte block of codes
       // of 8 of them and those blocks' scales, expands them to E4M3 codes in
       // registers and stores them where TMA's 128-byte swizzle would have put
-      // an E4M3 cache's bytes.  The next chunk's loads are in flight while one
-      // is expanded; going through registers instead of a staging buffer saves
+      // an E4M3 cache's bytes.  Going through registers instead of a staging buffer saves
       // a write and a read of shared memory, whose bandwidth the two MMAs'
       // operand reads already fill.
       //
@@ -934,35 +934,49 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       };
       int key0, key0_next;
       int window = chunk_window(0, key0), window_next = chunk_window(1, key0_next);
-      struct Chunk {
-        uint4 v[8];  // codes of tokens 2 k + par
-        uint4 sc;    // the block's 16 scale codes
-        int hidden;  // tokens of the chunk before a key window (they come first)
-        bool loaded;
-      };
-      auto load = [&](int ch, Chunk& c) {
+      // A chunk in registers: the codes of tokens 2 k + par, the block's 16
+      // scale codes and (restricted key sets) how many of its tokens, which
+      // come first, lie before the key window.
+      uint4 v[8], sc;
+      const uint8_t* src;  // the page whose codes are loaded next
+      int hidden = 0, hidden_next = 0;
+      bool loaded, loaded_next;
+      const int half = (ew & 1) * 16;
+      static_assert(C::kExpandWarps % 2 == 0, "a warp's chunks are the same half of their pages");
+      // Page of chunk ch, in order (page 0 for one that is not loaded, so that
+      // its loads need no condition: a merge with the old values would wait
+      // for them).
+      auto locate = [&](int ch) {
         if ((ch & 31) == 0 && ch > 0) {
           window = window_next;
           key0 = key0_next;
           window_next = chunk_window((ch >> 5) + 1, key0_next);
         }
         const int pg = __shfl_sync(0xffffffffu, window, ch & 31);
-        c.loaded = ch < n_chunks && pg >= 0;
-        c.hidden = kGather ? win_lo - __shfl_sync(0xffffffffu, key0, ch & 31) - (ew & 1) * 16 : 0;
-        if (c.loaded) {
-          const int half = (ew & 1) * 16;
-          const uint8_t* src = p.kv_fp4 + static_cast<int64_t>(pg) * MLA_FP4_PAGE_BYTES;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            c.v[k] = ldg_stream(src + (half + 2 * k + par) * kFp4RowCodes + blk * 16);
-          c.sc = ldg_stream(src + kFp4ScaleOffset + blk * MLA_PAGE_SIZE + half);
-        }
+        loaded_next = pg >= 0;
+        if constexpr (kGather)
+          hidden_next = win_lo - __shfl_sync(0xffffffffu, key0, ch & 31) - half;
+        src = p.kv_fp4 + static_cast<int64_t>(max(pg, 0)) * MLA_FP4_PAGE_BYTES;
       };
-      static_assert(C::kExpandWarps % 2 == 0, "a warp's chunks are the same half of their pages");
+      auto codes_of = [&](int k) {
+        return ldg_stream(src + (half + 2 * k + par) * kFp4RowCodes + blk * 16);
+      };
+      auto scales = [&]() { return ldg_stream(src + kFp4ScaleOffset + blk * MLA_PAGE_SIZE + half); };
+      locate(0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = codes_of(k);
+      sc = scales();
       int st = 0, round = 0;
-      // Expands chunk ch into its stage; false once a wait ran out.
-      auto expand = [&](int ch, const Chunk& c) -> bool {
+#pragma unroll 1
+      for (int ch = 0; ch < n_chunks; ++ch) {
         const int sub = ch % kPerTile;
+        loaded = loaded_next;
+        hidden = hidden_next;
+        // This lane's scale codes: bytes 2 k + par, two to a word.
+        uint32_t scw[4] = {(sc.x >> (8 * par)) & 0x000F000Fu, (sc.y >> (8 * par)) & 0x000F000Fu,
+                           (sc.z >> (8 * par)) & 0x000F000Fu, (sc.w >> (8 * par)) & 0x000F000Fu};
+        locate(ch + 1);
+        sc = scales();
         if (sub == 0 && round > 0) {
           bool w = mbar_wait_abort(bar(BAR_EMPTY0 + st), (round - 1) & 1, p.wait_cycles,
                                    abort_flag);
@@ -972,27 +986,44 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
               report(p.status, MLA_ERR_TIMEOUT);
               *abort_flag = 1;
             }
-            return false;
+            break;
           }
         }
-        if (c.loaded) {
-          uint8_t* row = base + C::kKV + st * kTileBytes + (lane >> 3) * kLatBlockBytes +
-                         ((ew + sub * C::kExpandWarps) * 16 + par) * 128;
-          const uint32_t scw[4] = {c.sc.x >> (8 * par), c.sc.y >> (8 * par), c.sc.z >> (8 * par),
-                                   c.sc.w >> (8 * par)};
+        uint8_t* row = base + C::kKV + st * kTileBytes + (lane >> 3) * kLatBlockBytes +
+                       ((ew + sub * C::kExpandWarps) * 16 + par) * 128;
+        const uint32_t c0 = (((lane & 3) * 2) ^ par) * 16;  // swizzled chunk of token par
+        // Scales below 2^-5 and NaN blocks, which the arithmetic table does
+        // not cover: rare, and decided once per chunk for the whole warp.
+        bool odd_scale = false;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          odd_scale |= (((scw[m] - 0x00030003u) | (scw[m] + 0x00010001u)) & 0x80108010u) != 0;
+        odd_scale = __any_sync(0xffffffffu, odd_scale || (kGather && hidden > 0));
+        // One block a step: expand, store, and load the next chunk's codes into
+        // the same registers, so that a whole chunk is always in flight.
+        auto step = [&](int k, uint2 t) {
+          const uint2 a = fp4_expand8(v[k].x, t), bb = fp4_expand8(v[k].y, t);
+          const uint2 cc = fp4_expand8(v[k].z, t), dd = fp4_expand8(v[k].w, t);
+          v[k] = codes_of(k);
+          uint8_t* dst = row + k * 256;
+          const uint32_t c = c0 ^ ((2 * k & 7) * 16);
+          *reinterpret_cast<uint4*>(dst + c) = make_uint4(a.x, a.y, bb.x, bb.y);
+          *reinterpret_cast<uint4*>(dst + (c ^ 16)) = make_uint4(cc.x, cc.y, dd.x, dd.y);
+        };
+        if (!loaded) {  // the QK warp zeroes this page's rows
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = codes_of(k);
+        } else if (!odd_scale) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            step(k, fp4_scale_table_normal((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu));
+        } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            uint2 t = fp4_scale_table((scw[k >> 1] >> (16 * (k & 1))) & 15u);
+            uint2 t = fp4_scale_table((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
             // A key before the window has weight 0, and so must not be a NaN.
-            if (kGather && 2 * k + par < c.hidden) t = make_uint2(0u, 0u);
-            const uint2 a = fp4_expand8(c.v[k].x, t), bb = fp4_expand8(c.v[k].y, t);
-            const uint2 cc = fp4_expand8(c.v[k].z, t), dd = fp4_expand8(c.v[k].w, t);
-            const int sw = (2 * k + par) & 7;
-            uint8_t* dst = row + k * 256;
-            *reinterpret_cast<uint4*>(dst + (((lane & 3) * 2) ^ sw) * 16) =
-                make_uint4(a.x, a.y, bb.x, bb.y);
-            *reinterpret_cast<uint4*>(dst + (((lane & 3) * 2 + 1) ^ sw) * 16) =
-                make_uint4(cc.x, cc.y, dd.x, dd.y);
+            if (kGather && 2 * k + par < hidden) t = make_uint2(0u, 0u);
+            step(k, t);
           }
         }
         if (sub == kPerTile - 1) {
@@ -1004,16 +1035,6 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             ++round;
           }
         }
-        return true;
-      };
-      Chunk c0, c1;
-      load(0, c0);
-      for (int ch = 0; ch < n_chunks; ch += 2) {
-        load(ch + 1, c1);
-        if (!expand(ch, c0)) break;
-        if (ch + 1 >= n_chunks) break;
-        load(ch + 2, c0);
-        if (!expand(ch + 1, c1)) break;
       }
     }
   } else {
