@@ -26,6 +26,14 @@ constexpr uint32_t kPageRopeBytes = MLA_PAGE_SIZE * 64;      // 2048
 constexpr uint32_t kPageBytes = MLA_PAGE_SIZE * MLA_HEAD_DIM;
 
 
+#ifndef EW16
+#define EW16 8
+#endif
+constexpr int kExpandWarps16 = EW16;
+#ifndef PFT
+#define PFT 6
+#endif
+constexpr int kPrefetchTiles = PFT;
 // kFp4: the 4-bit cache.  Everything downstream of the KV stages is the E4M3
 // kernel; only how a stage is filled differs (see the expander warps).
 template <int NR, bool kFp4 = false>
@@ -70,7 +78,7 @@ struct Cfg {
                 "register split");
   // 4-bit cache: expander warps after the softmax warps.
   static_assert(!kFp4 || !kWide, "the 4-bit cache has row groups of at most 48 rows");
-  static constexpr int kExpandWarps = !kFp4 ? 0 : NR == 16 ? 8 : 4;
+  static constexpr int kExpandWarps = !kFp4 ? 0 : NR == 16 ? kExpandWarps16 : 4;
   static constexpr int kExpandWarp0 = kSoftmaxWarp0 + 4 * SWG;
   static constexpr int kThreads = 32 * (kExpandWarp0 + kExpandWarps);
   static constexpr uint32_t kTmemCols =
@@ -391,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       mbar_init(bar(BAR_EMPTY0 + k), 1);
     }
     if constexpr (kFp4) {
-      for (int k = 0; k < C::NST; ++k) mbar_init(sbase + C::expanded_bar(k), C::kExpandWarps);
+      for (int k = 0; k < C::NST; ++k) mbar_init(sbase + C::expanded_bar(k), 8);
     }
     if constexpr (C::kBlockStages) {
       for (int k = 0; k < C::NST; ++k)
@@ -464,7 +472,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         MLA_ITEM_NAMES(item);
         // Q of this item, once the previous item's QKs are done with the buffer.
         if (nq > 0) {
-          bool q_ok = mbar_wait_abort(bar(BAR_QFREE), (nq - 1) & 1, p.wait_cycles, abort_flag);
+          bool q_ok = mbar_wait_abort<kFp4>(bar(BAR_QFREE), (nq - 1) & 1, p.wait_cycles, abort_flag);
           q_ok = __all_sync(0xffffffffu, q_ok && !*abort_flag);
           if (!q_ok) {
             if (lane == 0) {
@@ -536,15 +544,35 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         int window_nv, window_next_nv;
         int window = load_window(0, window_nv);
         int window_next = load_window(1, window_next_nv);
+        // 4-bit cache: pages go to L2 kPrefetch tiles ahead, so that the
+        // expanders' loads, of which registers hold one tile, find them there.
+        constexpr int kPrefetch = kPrefetchTiles;
+        auto prefetch_tile = [&](int j, int i) {
+          if constexpr (kFp4) {
+            const bool here = (j >> 3) == (i >> 3);
+            const int from = (j & 7) * 4 + (lane & 3);
+            const int pg = __shfl_sync(0xffffffffu, here ? window : window_next, from);
+            bool wanted = page0 + j * 4 + (lane & 3) < page_end;
+            if constexpr (kGather)
+              wanted = __shfl_sync(0xffffffffu, here ? window_nv : window_next_nv, from) > 0;
+            if (lane < 4 && j < n_tiles && wanted)
+              l2_prefetch(p.kv_fp4 + static_cast<int64_t>(pg) * MLA_FP4_PAGE_BYTES,
+                          MLA_FP4_PAGE_BYTES);
+          }
+        };
+        if constexpr (kFp4) {
+          for (int j = 0; j < kPrefetch; ++j) prefetch_tile(j, 0);
+        }
         for (int i = 0; i < n_tiles; ++i) {
           if (i > 0 && (i & 7) == 0) {
             window = window_next;
             window_nv = window_next_nv;
             window_next = load_window((i >> 3) + 1, window_next_nv);
           }
+          if constexpr (kFp4) prefetch_tile(i + kPrefetch, i);
           ok = !expired_here(p, WAIT_STAGE_FREE, i);
           if (ok && round > 0 && !C::kBlockStages)
-            ok = mbar_wait_abort(bar(BAR_EMPTY0 + st), (round - 1) & 1, p.wait_cycles, abort_flag);
+            ok = mbar_wait_abort<kFp4>(bar(BAR_EMPTY0 + st), (round - 1) & 1, p.wait_cycles, abort_flag);
           ok = __all_sync(0xffffffffu, ok && !*abort_flag);
           if (!ok) {
             if (lane == 0) {
@@ -584,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             for (int bi = 0; bi < 5; ++bi) {
               const int blk = (bi == 0) ? 4 : bi - 1;
               if (round > 0) {
-                ok = mbar_wait_abort(empty_blk(st, blk), (round - 1) & 1, p.wait_cycles,
+                ok = mbar_wait_abort<kFp4>(empty_blk(st, blk), (round - 1) & 1, p.wait_cycles,
                                      abort_flag);
                 ok = __all_sync(0xffffffffu, ok && !*abort_flag);
                 if (!ok) break;
@@ -686,10 +714,18 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         tc_fence_after();
         const uint32_t kv = sbase + C::kKV + jst * kTileBytes;
         const uint32_t pbuf = C::kPInStage ? kv + kRopeOffset : sbase + C::kP + pb * C::kPBytes;
+        const uint32_t a0 = smem_desc_lo(kv, 16384), b0 = smem_desc_lo(pbuf, 128);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
+            if constexpr (kFp4) {
+              umma_f8_halves(tmem + C::kOCol + d * C::OW,
+                             a0 + ((d * kLatBlockBytes + ks * 4096) >> 4),
+                             smem_desc_hi(1024, kLayoutSW128), b0 + ((ks * 512) >> 4),
+                             smem_desc_hi(2048, kLayoutNone), kIdPV, (ks > 0 || j > 0) ? 1u : 0u);
+              continue;
+            }
             const uint64_t a = smem_desc(kv + d * kLatBlockBytes + ks * 4096, 16384, 1024,
                                          kLayoutSW128);
             const uint32_t acc = (j > 0 || ks > 0) ? 1u : 0u;
@@ -729,6 +765,24 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       // QK of tile i (KV in stage ist) into S buffer sb; lane 0 issues.
       auto issue_qk = [&](int ist, int sb) {
         tc_fence_after();
+        if constexpr (kFp4) {
+          const uint32_t kv = sbase + C::kKV + ist * kTileBytes;
+          const uint32_t a0 = smem_desc_lo(kv, 16), b0 = smem_desc_lo(sbase + C::kQ, 16);
+          const uint32_t d = tmem + sb * NR;
+#pragma unroll
+          for (int kk = 0; kk < 16; ++kk)
+            umma_f8_halves(d, a0 + (((kk >> 2) * kLatBlockBytes + (kk & 3) * 32) >> 4),
+                           smem_desc_hi(1024, kLayoutSW128),
+                           b0 + (((kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4),
+                           smem_desc_hi(1024, kLayoutSW128), kIdQK, kk > 0 ? 1u : 0u);
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+            umma_f8_halves(d, a0 + ((kRopeOffset + sub * 32) >> 4),
+                           smem_desc_hi(512, kLayoutSW64), b0 + ((4 * NR * 128 + sub * 32) >> 4),
+                           smem_desc_hi(512, kLayoutSW64), kIdQK, 1u);
+          umma_commit(bar(BAR_SFULL0 + sb));
+          return;
+        }
 #pragma unroll
         for (int kk = 0; kk < 18; ++kk) qk_step(ist, sb, kk, kk > 0);
         umma_commit(bar(BAR_SFULL0 + sb));
@@ -747,28 +801,28 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           if (r == 1) continue;
           MLA_ITEM_NAMES(item);
           ++nq;
-          bool w = mbar_wait_abort(bar(BAR_QFULL), (nq - 1) & 1, p.wait_cycles, abort_flag);
+          bool w = mbar_wait_abort<kFp4>(bar(BAR_QFULL), (nq - 1) & 1, p.wait_cycles, abort_flag);
           ok = __all_sync(0xffffffffu, w && !*abort_flag);
           for (int j = 0; ok && j < n_tiles; ++j, ++g) {
             const int sb = (C::NS == 2) ? (g & 1) : 0;
             const int use = (C::NS == 2) ? (g >> 1) : g;
             // Block stages: the rope block arrives first.
             w = !expired_here(p, WAIT_TILE_FULL, j) &&
-                mbar_wait_abort(C::kBlockStages ? full_blk(st, 4) : bar(BAR_FULL0 + st), round & 1,
+                mbar_wait_abort<kFp4>(C::kBlockStages ? full_blk(st, 4) : bar(BAR_FULL0 + st), round & 1,
                                 p.wait_cycles, abort_flag);
             if constexpr (kFp4) {
               if (w)
-                w = mbar_wait_abort(sbase + C::expanded_bar(st), round & 1, p.wait_cycles,
+                w = mbar_wait_abort<kFp4>(sbase + C::expanded_bar(st), round & 1, p.wait_cycles,
                                     abort_flag);
             }
             if (w && use >= 1)
-              w = mbar_wait_abort(bar(BAR_SFREE0 + sb), (use - 1) & 1, p.wait_cycles, abort_flag);
+              w = mbar_wait_abort<kFp4>(bar(BAR_SFREE0 + sb), (use - 1) & 1, p.wait_cycles, abort_flag);
             // The 96-row CTA needs no PV(g - 2) wait: its softmax waited for
             // PV(g - 2) (the P^T buffer) before writing P(g - 1), which keeps its
             // wait for PV(g - 1) within one phase; the tile's stage implies
             // PV(g - 2) anyway.
             if (w && g >= 2 && !C::kWide)
-              w = mbar_wait_abort(bar(((g - 2) & 1) ? C::kBarOdone1 : BAR_ODONE),
+              w = mbar_wait_abort<kFp4>(bar(((g - 2) & 1) ? C::kBarOdone1 : BAR_ODONE),
                                   ((g - 2) >> 1) & 1, p.wait_cycles, abort_flag);
             w = __all_sync(0xffffffffu, w && !*abort_flag);
             if (!w) {
@@ -789,7 +843,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
               const bool partial = kGather ? (info != 0x20202020u) : (valid < kTileTokens);
               if (partial) {
                 for (int blk = 0; w && blk < 4; ++blk)
-                  w = mbar_wait_abort(full_blk(st, blk), round & 1, p.wait_cycles, abort_flag);
+                  w = mbar_wait_abort<kFp4>(full_blk(st, blk), round & 1, p.wait_cycles, abort_flag);
                 w = __all_sync(0xffffffffu, w && !*abort_flag);
                 if (!w) {
                   ok = false;
@@ -805,7 +859,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
               __syncwarp();
               for (int blk = 0; blk < 4; ++blk) {
                 if (!partial) {
-                  w = mbar_wait_abort(full_blk(st, blk), round & 1, p.wait_cycles, abort_flag);
+                  w = mbar_wait_abort<kFp4>(full_blk(st, blk), round & 1, p.wait_cycles, abort_flag);
                   w = __all_sync(0xffffffffu, w && !*abort_flag);
                   if (!w) break;
                 }
@@ -828,7 +882,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
               __syncwarp();
             } else {
               zero_unloaded_rows<kGather>(base + C::kKV + st * kTileBytes, lane, info, valid);
-              if (lane == 0) issue_qk(st, sb);
+              if (kFp4 ? elect_one() : lane == 0) issue_qk(st, sb);
               __syncwarp();
             }
             if (++st == C::NST) {
@@ -838,7 +892,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           }
           // Q is free for the next item once these QKs complete (also on the
           // way out: the drain below waits for it).
-          if (lane == 0) umma_commit(bar(BAR_QFREE));
+          if (kFp4 ? elect_one() : lane == 0) umma_commit(bar(BAR_QFREE));
           __syncwarp();
         }
         if (!ok) fail();
@@ -858,26 +912,26 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           ++nq;
           if (nq > 1) {
             const bool w =
-                mbar_wait_abort(bar(BAR_OFREE), (nq - 2) & 1, p.wait_cycles, abort_flag);
+                mbar_wait_abort<kFp4>(bar(BAR_OFREE), (nq - 2) & 1, p.wait_cycles, abort_flag);
             ok = __all_sync(0xffffffffu, w && !*abort_flag);
           }
           for (int i = 0; ok && i < n_tiles; ++i, ++g) {
             const int pb = (C::NPB == 1) ? 0 : (g & 1);
             const int use = (C::NPB == 1) ? g : (g >> 1);
             bool w = !expired_here(p, WAIT_P_FULL, i) &&
-                     mbar_wait_abort(bar(BAR_PFULL0 + pb), use & 1, p.wait_cycles, abort_flag);
+                     mbar_wait_abort<kFp4>(bar(BAR_PFULL0 + pb), use & 1, p.wait_cycles, abort_flag);
             w = __all_sync(0xffffffffu, w && !*abort_flag);
             if (!w) {
               ok = false;
               break;
             }
-            if (lane == 0) issue_pv(i, g, st, pb);
+            if (kFp4 ? elect_one() : lane == 0) issue_pv(i, g, st, pb);
             __syncwarp();
             if (++st == C::NST) st = 0;
           }
           // One commit after the item's last PV: the epilogue reads O^T after
           // it (every QK result has been consumed by then).
-          if (lane == 0) umma_commit(bar(BAR_FINAL));
+          if (kFp4 ? elect_one() : lane == 0) umma_commit(bar(BAR_FINAL));
           __syncwarp();
         }
         if (!ok) fail();
@@ -902,23 +956,22 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       // together hit the 8 chunks of two neighbouring swizzled rows, all
       // banks once.
       MLA_ITEM_NAMES(first);
-      constexpr int kPerTile = 8 / C::kExpandWarps;  // chunks of this warp per tile
+      constexpr int W = C::kExpandWarps;
       const int ew = warp - C::kExpandWarp0;
       const int blk = (lane >> 3) * 4 + (lane & 3), par = (lane >> 2) & 1;
-      const int n_chunks = n_tiles * kPerTile;
+      const int n_chunks = n_tiles * 8;  // this warp takes chunks ew, ew + W, ...
       const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
       const int page0 = t0 / MLA_PAGE_SIZE;
       const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;  // exclusive
-      // Page of this warp's chunk 32 w + lane (-1: not loaded; the QK warp
+      // Page of this warp's chunk number 32 w + lane (-1: not loaded; the QK warp
       // zeroes those rows).  Bad ids are reported by the producer, which reads
       // page 0 in their place, as here.
       // key0 (restricted key sets): the first key position of the page.
       auto chunk_window = [&](int w, int& key0) -> int {
         key0 = 0;
-        const int ch = w * 32 + lane;
+        const int ch = ew + W * (w * 32 + lane);
         if (ch >= n_chunks) return -1;
-        const int pi =
-            page0 + (ch / kPerTile) * 4 + ((ew + (ch % kPerTile) * C::kExpandWarps) >> 1);
+        const int pi = page0 + (ch >> 1);
         if (pi >= page_end) return -1;
         int lp = pi;
         if constexpr (kGather) {
@@ -942,20 +995,20 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       int hidden = 0, hidden_next = 0;
       bool loaded, loaded_next;
       const int half = (ew & 1) * 16;
-      static_assert(C::kExpandWarps % 2 == 0, "a warp's chunks are the same half of their pages");
-      // Page of chunk ch, in order (page 0 for one that is not loaded, so that
+      static_assert(W % 2 == 0, "a warp's chunks are the same half of their pages");
+      // Page of this warp's chunk number n, in order (page 0 for one that is not loaded, so that
       // its loads need no condition: a merge with the old values would wait
       // for them).
-      auto locate = [&](int ch) {
-        if ((ch & 31) == 0 && ch > 0) {
+      auto locate = [&](int n) {
+        if ((n & 31) == 0 && n > 0) {
           window = window_next;
           key0 = key0_next;
-          window_next = chunk_window((ch >> 5) + 1, key0_next);
+          window_next = chunk_window((n >> 5) + 1, key0_next);
         }
-        const int pg = __shfl_sync(0xffffffffu, window, ch & 31);
+        const int pg = __shfl_sync(0xffffffffu, window, n & 31);
         loaded_next = pg >= 0;
         if constexpr (kGather)
-          hidden_next = win_lo - __shfl_sync(0xffffffffu, key0, ch & 31) - half;
+          hidden_next = win_lo - __shfl_sync(0xffffffffu, key0, n & 31) - half;
         src = p.kv_fp4 + static_cast<int64_t>(max(pg, 0)) * MLA_FP4_PAGE_BYTES;
       };
       auto codes_of = [&](int k) {
@@ -966,19 +1019,18 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = codes_of(k);
       sc = scales();
-      int st = 0, round = 0;
 #pragma unroll 1
-      for (int ch = 0; ch < n_chunks; ++ch) {
-        const int sub = ch % kPerTile;
+      for (int ch = ew, n = 0; ch < n_chunks; ch += W, ++n) {
+        const int tile = ch >> 3, st = tile % C::NST, round = tile / C::NST;
         loaded = loaded_next;
         hidden = hidden_next;
         // This lane's scale codes: bytes 2 k + par, two to a word.
         uint32_t scw[4] = {(sc.x >> (8 * par)) & 0x000F000Fu, (sc.y >> (8 * par)) & 0x000F000Fu,
                            (sc.z >> (8 * par)) & 0x000F000Fu, (sc.w >> (8 * par)) & 0x000F000Fu};
-        locate(ch + 1);
+        locate(n + 1);
         sc = scales();
-        if (sub == 0 && round > 0) {
-          bool w = mbar_wait_abort(bar(BAR_EMPTY0 + st), (round - 1) & 1, p.wait_cycles,
+        if (round > 0) {
+          bool w = mbar_wait_abort<kFp4>(bar(BAR_EMPTY0 + st), (round - 1) & 1, p.wait_cycles,
                                    abort_flag);
           w = __all_sync(0xffffffffu, w && !*abort_flag);
           if (!w) {
@@ -990,7 +1042,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           }
         }
         uint8_t* row = base + C::kKV + st * kTileBytes + (lane >> 3) * kLatBlockBytes +
-                       ((ew + sub * C::kExpandWarps) * 16 + par) * 128;
+                       ((ch & 7) * 16 + par) * 128;
         const uint32_t c0 = (((lane & 3) * 2) ^ par) * 16;  // swizzled chunk of token par
         // Scales below 2^-5 and NaN blocks, which the arithmetic table does
         // not cover: rare, and decided once per chunk for the whole warp.
@@ -1026,15 +1078,9 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             step(k, t);
           }
         }
-        if (sub == kPerTile - 1) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sbase + C::expanded_bar(st));
-          if (++st == C::NST) {
-            st = 0;
-            ++round;
-          }
-        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sbase + C::expanded_bar(st));
       }
     }
   } else {
@@ -1166,7 +1212,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         for (int i = 0; i < n_tiles; ++i) {
           if (ok)
             ok = !expired_here(p, WAIT_S_FULL, i) &&
-                 mbar_wait_abort(bar(BAR_SFULL0), (g + i) & 1, p.wait_cycles, abort_flag);
+                 mbar_wait_abort<kFp4>(bar(BAR_SFULL0), (g + i) & 1, p.wait_cycles, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok && lane == 0) *abort_flag = 1;  // the other roles stop waiting
           float t[NRH];
@@ -1240,7 +1286,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
               // Rescale the O^T columns of rows whose reference moved (rare),
               // once PV(i - 1) is done (its completion barrier is within one
               // phase of the awaited one, as in the other configurations).
-              ok = mbar_wait_abort(bar(((g + i - 1) & 1) ? C::kBarOdone1 : BAR_ODONE),
+              ok = mbar_wait_abort<kFp4>(bar(((g + i - 1) & 1) ? C::kBarOdone1 : BAR_ODONE),
                                    ((g + i - 1) >> 1) & 1, p.wait_cycles, abort_flag);
               ok = __all_sync(0xffffffffu, ok);
               if (ok) {
@@ -1277,7 +1323,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           // P^T (one buffer): wait until PV(i - 1) has read it.
           if (ok && expired_here(p, WAIT_P_FREE, i)) ok = false;
           if (ok && g + i >= 1)
-            ok = mbar_wait_abort(bar(BAR_PFREE0), (g + i - 1) & 1, p.wait_cycles, abort_flag);
+            ok = mbar_wait_abort<kFp4>(bar(BAR_PFREE0), (g + i - 1) & 1, p.wait_cycles, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok && lane == 0) *abort_flag = 1;
           if (ok) {
@@ -1309,7 +1355,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           const int use = (C::NS == 2) ? ((g + i) >> 1) : (g + i);
           if (ok)
             ok = !expired_here(p, WAIT_S_FULL, i) &&
-                 mbar_wait_abort(bar(BAR_SFULL0 + sb), use & 1, p.wait_cycles, abort_flag);
+                 mbar_wait_abort<kFp4>(bar(BAR_SFULL0 + sb), use & 1, p.wait_cycles, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok && lane == 0) *abort_flag = 1;  // the other roles stop waiting
           float t[NRH];
@@ -1382,7 +1428,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
               // two barriers, and the one of PV(i-1)'s parity is within one phase
               // of the awaited one: s_full(i) implies PV(i-2) completed (QK(i)
               // waits for it) and PV(i+1) needs a later tile's P^T.
-              ok = mbar_wait_abort(bar(((g + i - 1) & 1) ? C::kBarOdone1 : BAR_ODONE),
+              ok = mbar_wait_abort<kFp4>(bar(((g + i - 1) & 1) ? C::kBarOdone1 : BAR_ODONE),
                                    ((g + i - 1) >> 1) & 1, p.wait_cycles, abort_flag);
               ok = __all_sync(0xffffffffu, ok);
               if (ok) {
@@ -1421,7 +1467,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           const int puse = (g + i) >> 1;
           if (ok && !C::kPInStage && expired_here(p, WAIT_P_FREE, i)) ok = false;
           if (ok && !C::kPInStage && puse >= 1)
-            ok = mbar_wait_abort(bar(BAR_PFREE0 + pb), (puse - 1) & 1, p.wait_cycles, abort_flag);
+            ok = mbar_wait_abort<kFp4>(bar(BAR_PFREE0 + pb), (puse - 1) & 1, p.wait_cycles, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok && lane == 0) *abort_flag = 1;
           if (ok) {

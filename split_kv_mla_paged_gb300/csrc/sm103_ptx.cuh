@@ -45,6 +45,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// mbar_try_wait that lets the hardware suspend the thread for up to `ns`
+// nanoseconds (it wakes when the phase completes).
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.b32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
 // Non-blocking probe of a phase.
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -72,14 +85,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
 // mbar_wait that also gives up (returns false) once *abort is set, for the
 // pipeline waits of a CTA in which another role has already failed.  The
 // first test is the same as mbar_wait's, so a phase that has completed costs
-// nothing extra.
+// nothing extra.  kSuspend: the waiting warps are suspended for up to 20 us at
+// a time instead of polling, which leaves their issue slots to other warps.
+template <bool kSuspend = false>
 __device__ __forceinline__ bool mbar_wait_abort(uint32_t bar, uint32_t parity,
                                                 long long limit_cycles,
                                                 const volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (kSuspend ? mbar_try_wait_for(bar, parity, 20000u) : mbar_try_wait(bar, parity)) return true;
     if (*abort || clock64() - t0 > limit_cycles) return false;
   }
 }
@@ -116,6 +131,11 @@ __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void* tmap,
       " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
+}
+
+// Brings `bytes` (a multiple of 16) from a 16-byte aligned global address to L2.
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // 16 bytes of read-only data that is used once: not kept in L1.
@@ -209,6 +229,37 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(layout & 7u) << 61;
   return d;
+}
+
+// The same descriptor in halves: the low word is an addition away from a
+// neighbouring tile's (shared memory ends below 2^18, so start addresses never
+// carry out of their 14 bits), the high word a constant.
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return (saddr >> 4) + ((lbo_bytes >> 4) << 16);
+}
+__host__ __device__ constexpr uint32_t smem_desc_hi(uint32_t sbo_bytes, uint32_t layout) {
+  return (sbo_bytes >> 4) | (1u << 14) | (layout << 29);
+}
+
+// umma_f8 with the descriptors in halves.
+__device__ __forceinline__ void umma_f8_halves(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                               uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// True in one lane of a converged warp.  Unlike a test of the lane number it
+// tells the compiler that warp-uniform values stay so inside the branch.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.b32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
 }
 
 // Instruction descriptor for kind::f8f6f4 with E4M3 A and B, fp32 D.
