@@ -27,11 +27,17 @@ constexpr uint32_t kPageBytes = MLA_PAGE_SIZE * MLA_HEAD_DIM;
 
 
 #ifndef EW16
-#define EW16 8
+#define EW16 12
+#endif
+#ifndef RL
+#define RL 80
+#define RS 72
+#define RE 96
+#define RLOW 48
 #endif
 constexpr int kExpandWarps16 = EW16;
 #ifndef PFT
-#define PFT 6
+#define PFT 3
 #endif
 constexpr int kPrefetchTiles = PFT;
 // kFp4: the 4-bit cache.  Everything downstream of the KV stages is the E4M3
@@ -56,6 +62,9 @@ struct Cfg {
   // (4-bit cache: two for 16 rows as well, whose tiles come 1.7 times as fast.)
   static constexpr int SWG = kWide ? 3 : (NR >= 32 || kFp4) ? 2 : 1;
   static constexpr int NRH = NR / SWG;
+  // Each softmax thread keeps its own row sums across tiles, and a warpgroup's
+  // rows are its own affair (votes and references synchronise 128 threads).
+  static constexpr bool kThreadSums = kWide || (kFp4 && NR == 16);
   static_assert(NRH % 8 == 0, "rows per softmax warpgroup");
   // Warp 0 TMA, warp 1 QK issuer (and TMEM owner), warp 2 PV issuer, then
   // the softmax warpgroups.  Each issuer blocks on its own barriers; for the
@@ -70,9 +79,13 @@ struct Cfg {
   // Measured against two softmax warpgroups of 48 rows at 168 registers
   // (which spilled): MTP q8 B16 128K 371.6 -> 361.2 us, B1 45.1 -> 41.4 us,
   // H96 q8 B1 1M 1332.7 -> 1305.7 us.
-  static constexpr int kIdleWarps = kWide ? 1 : 0;
+  // 4-bit cache, 16 rows: 28 warps at 72 registers a thread; warpgroup 0 drops
+  // to 40 and the expanders rise to 80, which hold a chunk in flight each.
+  static constexpr bool kSplitRegs = kWide || (kFp4 && NR == 16);
+  static constexpr int kIdleWarps = kSplitRegs ? 1 : 0;
   static constexpr int kSoftmaxWarp0 = 1 + kMmaWarps + kIdleWarps;
-  static constexpr int kRegsLaunch = 128, kRegsLow = 56, kRegsHigh = 152;
+  static constexpr int kRegsLaunch = kFp4 ? RL : 128, kRegsLow = kFp4 ? RLOW : 56,
+                       kRegsHigh = kFp4 ? RS : 152, kRegsExpand = RE;
   static_assert(!kWide || (kRegsLow * 128 + kRegsHigh * 128 * SWG <= kRegsLaunch * 512 &&
                            32 * kSoftmaxWarp0 + 128 * SWG == 512),
                 "register split");
@@ -81,6 +94,9 @@ struct Cfg {
   static constexpr int kExpandWarps = !kFp4 ? 0 : NR == 16 ? kExpandWarps16 : 4;
   static constexpr int kExpandWarp0 = kSoftmaxWarp0 + 4 * SWG;
   static constexpr int kThreads = 32 * (kExpandWarp0 + kExpandWarps);
+  static constexpr int kRegsSplit =
+      kRegsLow * 128 + kRegsHigh * 128 * SWG + (kFp4 ? kRegsExpand * 32 * kExpandWarps : 0);
+  static_assert(!kSplitRegs || kRegsSplit <= kRegsLaunch * kThreads, "register split");
   static constexpr uint32_t kTmemCols =
       kTmemUsed <= 32 ? 32 : kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128
       : kTmemUsed <= 256 ? 256 : 512;
@@ -448,7 +464,8 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
   if (warp < C::kSoftmaxWarp0) {
     // Producer, MMA issuers (and the 96-row configuration's idle warp): one
     // warpgroup, whose registers go to the softmax warpgroups.
-    if constexpr (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsLow));
+    if constexpr (C::kSplitRegs)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsLow));
     if (warp == 0) {
       // ================= TMA producer =================
       if (lane == 0) {
@@ -719,24 +736,24 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         for (int d = 0; d < 4; ++d) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t acc = (j > 0 || ks > 0) ? 1u : 0u;
             if constexpr (kFp4) {
               umma_f8_halves(tmem + C::kOCol + d * C::OW,
                              a0 + ((d * kLatBlockBytes + ks * 4096) >> 4),
                              smem_desc_hi(1024, kLayoutSW128), b0 + ((ks * 512) >> 4),
-                             smem_desc_hi(2048, kLayoutNone), kIdPV, (ks > 0 || j > 0) ? 1u : 0u);
-              continue;
-            }
-            const uint64_t a = smem_desc(kv + d * kLatBlockBytes + ks * 4096, 16384, 1024,
-                                         kLayoutSW128);
-            const uint32_t acc = (j > 0 || ks > 0) ? 1u : 0u;
-            // B = P^T, MN-major: 16-row groups 2048 B apart (hi groups, then lo
-            // groups), 8-token groups 128 B apart.
-            const uint64_t bd = smem_desc(pbuf + ks * 512, 128, 2048, kLayoutNone);
-            umma_f8(tmem + C::kOCol + d * C::OW, a, bd, kIdPV, acc);
-            if constexpr (C::kWide) {
-              // The lo term: a second MMA into the same O^T columns.
-              const uint64_t bl = smem_desc(pbuf + C::kPHalf + ks * 512, 128, 2048, kLayoutNone);
-              umma_f8(tmem + C::kOCol + d * C::OW, a, bl, kIdPV, 1u);
+                             smem_desc_hi(2048, kLayoutNone), kIdPV, acc);
+            } else {
+              const uint64_t a = smem_desc(kv + d * kLatBlockBytes + ks * 4096, 16384, 1024,
+                                           kLayoutSW128);
+              // B = P^T, MN-major: 16-row groups 2048 B apart (hi groups, then lo
+              // groups), 8-token groups 128 B apart.
+              const uint64_t bd = smem_desc(pbuf + ks * 512, 128, 2048, kLayoutNone);
+              umma_f8(tmem + C::kOCol + d * C::OW, a, bd, kIdPV, acc);
+              if constexpr (C::kWide) {
+                // The lo term: a second MMA into the same O^T columns.
+                const uint64_t bl = smem_desc(pbuf + C::kPHalf + ks * 512, 128, 2048, kLayoutNone);
+                umma_f8(tmem + C::kOCol + d * C::OW, a, bl, kIdPV, 1u);
+              }
             }
           }
           // Latent block d of the stage is free once these MMAs complete.
@@ -780,11 +797,10 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             umma_f8_halves(d, a0 + ((kRopeOffset + sub * 32) >> 4),
                            smem_desc_hi(512, kLayoutSW64), b0 + ((4 * NR * 128 + sub * 32) >> 4),
                            smem_desc_hi(512, kLayoutSW64), kIdQK, 1u);
-          umma_commit(bar(BAR_SFULL0 + sb));
-          return;
-        }
+        } else {
 #pragma unroll
-        for (int kk = 0; kk < 18; ++kk) qk_step(ist, sb, kk, kk > 0);
+          for (int kk = 0; kk < 18; ++kk) qk_step(ist, sb, kk, kk > 0);
+        }
         umma_commit(bar(BAR_SFULL0 + sb));
       };
       if (warp == 1) {
@@ -941,6 +957,8 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     }
   } else if (kFp4 && warp >= C::kExpandWarp0) {
     if constexpr (kFp4) {
+      if constexpr (C::kSplitRegs && C::kRegsExpand > C::kRegsLaunch)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsExpand));
       // ================= expanders (4-bit cache) =================
       // They fill the four latent blocks of each stage: 16 tokens (half a
       // page, a "chunk") at a time, each lane loads one 16-byte block of codes
@@ -1084,7 +1102,10 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       }
     }
   } else {
-    if constexpr (C::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsHigh));
+    if constexpr (C::kSplitRegs && C::kRegsHigh > C::kRegsLaunch)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsHigh));
+    else if constexpr (C::kSplitRegs && C::kRegsHigh < C::kRegsLaunch)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsHigh));
     // ===== softmax warpgroups (warps kSoftmaxWarp0 .. kSoftmaxWarp0 + 4*SWG - 1) =====
     // SWG warpgroups share each tile: warpgroup g owns rows [g*NRH, (g+1)*NRH)
     // of every token (two warps per SM sub-partition when SWG = 2, so one
@@ -1103,10 +1124,10 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     // rows, so that a warpgroup's vote and reference update synchronise only
     // its own 128 threads (named barriers per warpgroup).
     const int wgi = (warp - C::kSoftmaxWarp0) >> 2;
-    const int own = C::kWide ? (((sid & 127) < NRH) ? rbase + (sid & 127) : -1)
-                             : (sid < NR ? sid : -1);
-    const uint32_t vote_bar = C::kWide ? kVoteBarrierWg0 + wgi : kVoteBarrier;
-    const uint32_t smx_bar = C::kWide ? kSoftmaxBarrierWg0 + wgi : kSoftmaxBarrier;
+    const int own = C::kThreadSums ? (((sid & 127) < NRH) ? rbase + (sid & 127) : -1)
+                                   : (sid < NR ? sid : -1);
+    const uint32_t vote_bar = C::kThreadSums ? kVoteBarrierWg0 + wgi : kVoteBarrier;
+    const uint32_t smx_bar = C::kThreadSums ? kSoftmaxBarrierWg0 + wgi : kSoftmaxBarrier;
     (void)vote_bar;
     (void)smx_bar;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
@@ -1127,14 +1148,14 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       // instead (owners write them only between B1 and B2, when every thread
       // has passed the tile's vote and none has reached its weights), which
       // keeps the 32-row thread within its registers.
-      float kreg[C::kWide ? 1 : NRH];
+      float kreg[C::kThreadSums ? 1 : NRH];
 #pragma unroll
-      for (int k = 0; k < (C::kWide ? 1 : NRH); ++k) kreg[k] = -INFINITY;
+      for (int k = 0; k < (C::kThreadSums ? 1 : NRH); ++k) kreg[k] = -INFINITY;
       // 96 rows: this thread's sums of its token's weights per row, relative to
       // the row's current reference (reduced once, after the last tile).
-      float lsum[C::kWide ? NRH : 1];
+      float lsum[C::kThreadSums ? NRH : 1];
 #pragma unroll
-      for (int k = 0; k < (C::kWide ? NRH : 1); ++k) lsum[k] = 0.0f;
+      for (int k = 0; k < (C::kThreadSums ? NRH : 1); ++k) lsum[k] = 0.0f;
       const float c = c_log2;
       // Smallest visibility limit over this group's rows (MTP verify: the first
       // query token of the block sees the fewest keys).
@@ -1349,6 +1370,125 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             mbar_arrive(bar(BAR_PFULL0));
           }
         }
+      } else if constexpr (C::kThreadSums) {
+        // 16 rows of a 4-bit cache: each thread holds 8 rows of one token.  The
+        // tiles come faster than with an E4M3 cache, so what is left per tile
+        // is the chain from S^T to P^T: thresholds (k + 0.75) and exponent
+        // offsets in registers, weights by softmax_weight_kc, sums kept per
+        // thread, and nothing for row quads that hold no row.
+        float thr[NRH];
+        int kci[NRH];
+#pragma unroll
+        for (int k = 0; k < NRH; ++k) {
+          thr[k] = -INFINITY;
+          kci[k] = kKcNone;
+        }
+        for (int i = 0; i < n_tiles; ++i) {
+          const int sb = i & 1;
+          if (ok)
+            ok = !expired_here(p, WAIT_S_FULL, i) &&
+                 mbar_wait_abort<kFp4>(bar(BAR_SFULL0 + sb), (i >> 1) & 1, p.wait_cycles,
+                                       abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok && lane == 0) *abort_flag = 1;  // the other roles stop waiting
+          float t[NRH];
+          if (ok) {
+            tc_fence_after();
+            uint32_t r[NRH];
+            tmem_ld8(tmem + lane_addr + sb * NR + rbase, *reinterpret_cast<uint32_t(*)[8]>(&r[0]));
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < NRH; ++k) t[k] = __uint_as_float(r[k]);
+            tc_fence_before();
+            mbar_arrive(bar(BAR_SFREE0 + sb));
+          } else {
+#pragma unroll
+            for (int k = 0; k < NRH; ++k) t[k] = 0.0f;
+          }
+          scale_mask(t, i);
+          bool over = false;
+#pragma unroll
+          for (int k = 0; k < NRH; ++k) over |= t[k] > thr[k];
+          if (bar_sync_or(vote_bar, 128, over)) {
+            {
+              float tm[NRH];
+#pragma unroll
+              for (int k = 0; k < NRH; ++k) tm[k] = t[k];
+              warp_reduce_rows<NRH, true>(tm, lane, red_max + quad * NR + rbase);
+            }
+            named_bar_sync(smx_bar, 128);  // B1: tile maxima ready
+            if (own >= 0) {
+              const float mt = fmaxf(fmaxf(red_max[own], red_max[NR + own]),
+                                     fmaxf(red_max[2 * NR + own], red_max[3 * NR + own]));
+              float k_new = k_row;
+              if (mt > k_row + 0.75f) k_new = ceilf(mt);
+              float alpha = 1.0f;
+              if (k_new != k_row && k_row != -INFINITY) {
+                const int e = static_cast<int>(k_row - k_new);
+                alpha = (e < -126) ? 0.0f : pow2i(e);
+              }
+              k_row = k_new;
+              kref[own] = k_new;
+              alpha_s[own] = alpha;
+            }
+            named_bar_sync(smx_bar, 128);  // B2: references ready
+            bool corr = false;
+#pragma unroll
+            for (int k = 0; k < NRH; ++k) {
+              const float kr = kref[rbase + k], al = alpha_s[rbase + k];
+              thr[k] = kr + 0.75f;
+              kci[k] = (kr == -INFINITY) ? kKcNone : 135 - 0x4B400000 - static_cast<int>(kr);
+              lsum[k] *= al;
+              corr |= al != 1.0f;
+            }
+            if (ok && corr && i > 0) {
+              // Rescale the O^T columns of rows whose reference moved (rare),
+              // once PV(i - 1) is done; S^T(i) implies that PV(i - 2) is, so
+              // the barrier is within one phase of the awaited one.
+              ok = mbar_wait_abort<kFp4>(bar(((i - 1) & 1) ? C::kBarOdone1 : BAR_ODONE),
+                                         ((i - 1) >> 1) & 1, p.wait_cycles, abort_flag);
+              ok = __all_sync(0xffffffffu, ok);
+              if (ok) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int d = 0; d < 8; ++d) {  // latent block d / 2, its hi or lo columns
+                  uint32_t r[8];
+                  const uint32_t addr = tmem + lane_addr + C::kOCol + d * NR + rbase;
+                  tmem_ld8(addr, r);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha_s[rbase + k]);
+                  tmem_st8(addr, r);
+                }
+                tmem_st_wait();
+              }
+            }
+          }
+          uint2 vh = make_uint2(0u, 0u), vl = make_uint2(0u, 0u);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (4 * q < my_rows) {  // the same for the whole warpgroup
+#pragma unroll
+              for (int k = 4 * q; k < 4 * q + 4; ++k) {
+                t[k] = softmax_weight_kc(t[k], kci[k]);
+                lsum[k] += t[k];
+              }
+              split_e4m3x4(&t[4 * q], q ? vh.y : vh.x, q ? vl.y : vl.x);
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok && lane == 0) *abort_flag = 1;
+          if (ok) {
+            uint8_t* pbuf = base + C::kKV + (i % C::NST) * kTileBytes + kRopeOffset +
+                            tok_lane * 16 + rbase;
+            *reinterpret_cast<uint2*>(pbuf) = vh;
+            *reinterpret_cast<uint2*>(pbuf + C::kPHalf) = vl;
+            fence_proxy_async_smem();
+            tc_fence_before();
+            mbar_arrive(bar(BAR_PFULL0 + sb));
+          }
+        }
       } else {
         for (int i = 0; i < n_tiles; ++i) {
           const int sb = (C::NS == 2) ? ((g + i) & 1) : 0;
@@ -1518,7 +1658,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         *abort_flag = 1;
       }
       // ---- epilogue ----
-      if constexpr (C::kWide) {
+      if constexpr (C::kThreadSums) {
         // The per-thread sums, reduced over the 32 tokens of each warp; the
         // owners add the four lane quadrants below.
         warp_reduce_rows<NRH, false>(lsum, lane, red_sum + quad * NR + rbase);
@@ -1528,7 +1668,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       float* scale_s = alpha_s;
       if (own >= 0) {
         if (n_tiles > 0) {
-          const float* rs = red_sum + (C::kWide ? 0 : ((n_tiles - 1) & 1) * 4 * NR);
+          const float* rs = red_sum + (C::kThreadSums ? 0 : ((n_tiles - 1) & 1) * 4 * NR);
           l_row += (rs[own] + rs[NR + own]) + (rs[2 * NR + own] + rs[3 * NR + own]);
         }
         const float m_s = (k_row == -INFINITY) ? -INFINITY : k_row - 8.0f;
@@ -1730,14 +1870,14 @@ static cudaError_t launch_split_t(const void* q, const void* kv, int64_t num_pag
                                            static_cast<int>(C::kSmemBytes), attr_done);
     if (e != cudaSuccess) return e;
   }
-  if constexpr (C::kWide) {
+  if constexpr (C::kSplitRegs) {
     // setmaxnreg.inc waits until the registers exist: launch only if the
     // kernel's register count covers the split.
     cudaFuncAttributes fa;
-    const cudaError_t e = cudaFuncGetAttributes(&fa, mla_split_kv_kernel<NR, kGather, kMode>);
+    const cudaError_t e =
+        cudaFuncGetAttributes(&fa, mla_split_kv_kernel<NR, kGather, kMode, kFp4>);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs * C::kThreads < C::kRegsLow * 128 + C::kRegsHigh * 128 * C::SWG)
-      return cudaErrorInvalidConfiguration;
+    if (fa.numRegs * C::kThreads < C::kRegsSplit) return cudaErrorInvalidConfiguration;
   }
   CUtensorMap kv_lat, kv_rope, q_lat, q_rope;
   const uint64_t kv_rows = static_cast<uint64_t>(num_pages) * MLA_PAGE_SIZE;

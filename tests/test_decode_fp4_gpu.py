@@ -2,8 +2,11 @@
 
 Every value of a 4-bit page times its block's scale is an E4M3 number, so the
 kernel's tensor-core operands are those of the E4M3 cache that the pages expand
-to: with the same plan and row groups its outputs equal mla_decode's bit for
-bit.  The oracle runs on that expanded cache (expanded by oracle.cache, not by
+to: with the same plan and row groups its outputs equal mla_decode's, bit for
+bit from 17 to 48 rows.  Up to 16 rows only the row sums differ, which are added
+in another order: at most 128 tiles of a split, one after the other, then a tree
+over 128 tokens, 136 roundings on either side, 2 * 136 * 2^-24 < 2^-15 relative
+(and as much, absolute, in the natural logarithm).  The oracle runs on that expanded cache (expanded by oracle.cache, not by
 the kernel under test), with the decode tests' tolerances.
 """
 import numpy as np
@@ -60,6 +63,16 @@ def _same(a, b):
         assert torch.equal(x, y)
 
 
+def _equal(a, b, rows):
+    """Outputs (bf16, lse, fp32) of the 4-bit and the E4M3 decode of `rows` rows a request."""
+    if rows > 16:
+        return _same(a, b)
+    (o, l, f), (ob, lb, fb) = a, b
+    assert ((f - fb).abs() <= 2.0 ** -15 * fb.abs()).all()
+    assert ((l - lb).abs() <= 2.0 ** -15).all()
+    assert ((o.float() - ob.float()).abs() <= 2.0 ** -7 * ob.float().abs()).all()  # one BF16 step
+
+
 SHAPES = [
     # batch, heads, q_len, lens, causal
     (1, 12, 1, [1], False),
@@ -91,16 +104,16 @@ def test_matches_oracle(batch, heads, q_len, lens, causal):
 
 @pytest.mark.parametrize("batch, heads, q_len, lens, causal", [s for s in SHAPES if s[1] * s[2] <= 48])
 @pytest.mark.parametrize("target", [0, 7, 40])
-def test_equals_the_e4m3_decode_bit_for_bit(batch, heads, q_len, lens, causal, target):
+def test_equals_the_e4m3_decode(batch, heads, q_len, lens, causal, target):
     inp, pool = _case(batch, heads, q_len, lens, seed=60 + heads)
     plan = mla.mla_decode_plan(lens, heads, q_len, sm_count=152, target_ctas=target)
-    _same(_decode(inp, pool, causal, plan=plan), _decode(inp, inp.kv, causal, plan=plan))
+    _equal(_decode(inp, pool, causal, plan=plan), _decode(inp, inp.kv, causal, plan=plan), heads * q_len)
 
 
 def test_long_request_over_every_sm():
     inp, pool = _case(1, 12, 1, [70001], seed=71)
     got = _decode(inp, pool, False)
-    _same(got, _decode(inp, inp.kv, False))
+    _equal(got, _decode(inp, inp.kv, False), 12)
     ref_o, ref_l = oracle.decode_rows(inp.q, inp.kv, inp.page_table, inp.kv_lens, q_len=1, num_heads=12, causal=False,
                                       softmax_scale=SOFTMAX_SCALE)
     assert_parity(got[0], got[1], ref_o, ref_l)
@@ -151,7 +164,7 @@ def test_selected_pages(heads, q_len):
                                       softmax_scale=SOFTMAX_SCALE, block_idx=sel)
     assert_parity(out, lse, ref_o, ref_l)
     if heads * q_len <= 48:
-        _same((out, lse, f32), _decode(inp, inp.kv, q_len > 1, block_idx=torch.from_numpy(sel)))
+        _equal((out, lse, f32), _decode(inp, inp.kv, q_len > 1, block_idx=torch.from_numpy(sel)), heads * q_len)
 
 
 def test_nans_reach_only_the_rows_that_see_them():
