@@ -427,10 +427,12 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     mbar_init(bar(BAR_QFULL), 1);
     mbar_init(bar(BAR_SFULL0), 1);
     mbar_init(bar(BAR_SFULL1), 1);
-    mbar_init(bar(BAR_SFREE0), 128 * C::SWG);
-    mbar_init(bar(BAR_SFREE1), 128 * C::SWG);
-    mbar_init(bar(BAR_PFULL0), 128 * C::SWG);
-    mbar_init(bar(BAR_PFULL1), 128 * C::SWG);
+    // One arrival per softmax thread, or (16 rows of a 4-bit cache) per warp.
+    constexpr uint32_t kArrivals = kFp4 && NR == 16 ? 4 * C::SWG : 128 * C::SWG;
+    mbar_init(bar(BAR_SFREE0), kArrivals);
+    mbar_init(bar(BAR_SFREE1), kArrivals);
+    mbar_init(bar(BAR_PFULL0), kArrivals);
+    mbar_init(bar(BAR_PFULL1), kArrivals);
     if constexpr (!kFp4 || !C::kPInStage) mbar_init(bar(BAR_PFREE0), 1);
     mbar_init(bar(BAR_PFREE1), 1);
     mbar_init(bar(BAR_ODONE), 1);
@@ -1011,7 +1013,6 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       uint4 v[8], sc;
       const uint8_t* src;  // the page whose codes are loaded next
       int hidden = 0, hidden_next = 0;
-      bool loaded, loaded_next;
       const int half = (ew & 1) * 16;
       static_assert(W % 2 == 0, "a warp's chunks are the same half of their pages");
       // Page of this warp's chunk number n, in order (page 0 for one that is not loaded, so that
@@ -1024,7 +1025,6 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           window_next = chunk_window((n >> 5) + 1, key0_next);
         }
         const int pg = __shfl_sync(0xffffffffu, window, n & 31);
-        loaded_next = pg >= 0;
         if constexpr (kGather)
           hidden_next = win_lo - __shfl_sync(0xffffffffu, key0, n & 31) - half;
         src = p.kv_fp4 + static_cast<int64_t>(max(pg, 0)) * MLA_FP4_PAGE_BYTES;
@@ -1040,7 +1040,6 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
 #pragma unroll 1
       for (int ch = ew, n = 0; ch < n_chunks; ch += W, ++n) {
         const int tile = ch >> 3, st = tile % C::NST, round = tile / C::NST;
-        loaded = loaded_next;
         hidden = hidden_next;
         // This lane's scale codes: bytes 2 k + par, two to a word.
         uint32_t scw[4] = {(sc.x >> (8 * par)) & 0x000F000Fu, (sc.y >> (8 * par)) & 0x000F000Fu,
@@ -1080,10 +1079,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           *reinterpret_cast<uint4*>(dst + c) = make_uint4(a.x, a.y, bb.x, bb.y);
           *reinterpret_cast<uint4*>(dst + (c ^ 16)) = make_uint4(cc.x, cc.y, dd.x, dd.y);
         };
-        if (!loaded) {  // the QK warp zeroes this page's rows
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = codes_of(k);
-        } else if (!odd_scale) {
+        if (!odd_scale) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             step(k, fp4_scale_table_normal((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu));
@@ -1400,7 +1396,8 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < NRH; ++k) t[k] = __uint_as_float(r[k]);
             tc_fence_before();
-            mbar_arrive(bar(BAR_SFREE0 + sb));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(BAR_SFREE0 + sb));
           } else {
 #pragma unroll
             for (int k = 0; k < NRH; ++k) t[k] = 0.0f;
@@ -1486,7 +1483,8 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             *reinterpret_cast<uint2*>(pbuf + C::kPHalf) = vl;
             fence_proxy_async_smem();
             tc_fence_before();
-            mbar_arrive(bar(BAR_PFULL0 + sb));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(BAR_PFULL0 + sb));
           }
         }
       } else {
