@@ -383,11 +383,11 @@ MLA_API int mla_decode_bf16_sparse(const void* q_bf16, const void* kv_pages_bf16
  * Decode over a 4-bit cache (MLA_CACHE_FP4), dense and over selected pages:
  * mla_decode_ex and mla_decode_sparse with kv_pages_fp4 uint8 [num_pages,
  * MLA_FP4_PAGE_BYTES], 16-byte aligned.  Q is E4M3; a key's values are kv_scale
- * times those of its codes.  Plans, workspace, status, outputs and options are
- * as there; item lists come from mla_decode_plan_items_bf16 (row groups of at
- * most 48 rows), and persistent_ctas is MLA_ERR_UNSUPPORTED.  options may be
- * NULL.  Outputs are those of mla_decode over the E4M3 cache that the pages
- * expand to (bit for bit where both have the same row groups: up to 48 rows);
+ * times those of its codes.  Plans, item lists, workspace, status, outputs and
+ * options are as there, but persistent_ctas is MLA_ERR_UNSUPPORTED.  options
+ * may be NULL.  Outputs are those of mla_decode over the E4M3 cache that the
+ * pages expand to (up to 16 rows, to the order of its fp32 row sums; from 17
+ * on, bit for bit);
  * a NaN among a request's keys (a later draft token's under causal included)
  * leaves its rows without a defined result, as there; NaNs or stale bytes past
  * kv_lens, outside kv_bounds or in pages that are not selected have no effect.

@@ -445,8 +445,7 @@ def mla_decode_fp4(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req
                    query_lens=None, kv_bounds=None, cta_items=None, phases: int = PHASE_ALL,
                    stream=None) -> None:
     """Decode over a 4-bit cache, uint8 [pages, FP4_PAGE_BYTES]; options as for
-    mla_decode_ex (no persistent CTAs; item lists from
-    mla_decode_plan_items_bf16)."""
+    mla_decode_ex (no persistent CTAs)."""
     opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
                         query_lens, kv_bounds, cta_items, phases)
     _call_on(q_fp8, load_library().mla_decode_fp4, _ptr(q_fp8), _fp4_pages(kv_pages_fp4),
@@ -793,7 +792,7 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
     items_d = None
     if use_items:
         items_d = torch.from_numpy(
-            mla_decode_plan_items(plan.splits, num_heads, q_len, bf16=is_bf16 or is_fp4)).to(dev)
+            mla_decode_plan_items(plan.splits, num_heads, q_len, bf16=is_bf16)).to(dev)
 
     def _dev_i32(x):
         return None if x is None else torch.as_tensor(x, dtype=torch.int32).to(dev).contiguous()

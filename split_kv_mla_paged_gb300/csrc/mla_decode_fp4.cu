@@ -29,9 +29,6 @@ static cudaError_t launch_fp4(const void* q, const void* kv, int64_t num_pages,
 static int decode_fp4(const void* q, const void* kv, int64_t num_pages,
                       const mla_decode_options_t* options, const char* who, DecodeLaunch* dl,
                       cudaStream_t st) {
-  // Row groups of at most 48 rows, as for the BF16 kernels.
-  dl->rg = row_groups(dl->prm.rows_per_req);
-  dl->prm.rows_per_group = dl->rg.rows;
   dl->prm.kv_fp4 = reinterpret_cast<const uint8_t*>(kv);
   if (options && options->persistent_ctas != 0) {
     set_error(std::string(who) + ": persistent CTAs are not available for the 4-bit cache");
@@ -54,6 +51,10 @@ static int decode_fp4(const void* q, const void* kv, int64_t num_pages,
       case 48:
         e = gather ? launch_fp4<48, true>(q, kv, num_pages, *dl, st)
                    : launch_fp4<48, false>(q, kv, num_pages, *dl, st);
+        break;
+      case kMaxRowsPerCtaFp8:
+        e = gather ? launch_fp4<kMaxRowsPerCtaFp8, true>(q, kv, num_pages, *dl, st)
+                   : launch_fp4<kMaxRowsPerCtaFp8, false>(q, kv, num_pages, *dl, st);
         break;
       default:
         set_error(std::string(who) + ": internal row grouping error");

@@ -26,20 +26,18 @@ constexpr uint32_t kPageRopeBytes = MLA_PAGE_SIZE * 64;      // 2048
 constexpr uint32_t kPageBytes = MLA_PAGE_SIZE * MLA_HEAD_DIM;
 
 
-#ifndef EW16
-#define EW16 12
+#ifndef RHW
+#define RHW 120
+#define REW 72
+#define RHM 128
+#define REM 88
 #endif
-#ifndef RL
-#define RL 80
-#define RS 72
-#define RE 96
-#define RLOW 48
-#endif
-constexpr int kExpandWarps16 = EW16;
 #ifndef PFT
 #define PFT 3
 #endif
-constexpr int kPrefetchTiles = PFT;
+#ifndef PFW
+#define PFW 3
+#endif
 // kFp4: the 4-bit cache.  Everything downstream of the KV stages is the E4M3
 // kernel; only how a stage is filled differs (see the expander warps).
 template <int NR, bool kFp4 = false>
@@ -79,19 +77,20 @@ struct Cfg {
   // Measured against two softmax warpgroups of 48 rows at 168 registers
   // (which spilled): MTP q8 B16 128K 371.6 -> 361.2 us, B1 45.1 -> 41.4 us,
   // H96 q8 B1 1M 1332.7 -> 1305.7 us.
-  // 4-bit cache, 16 rows: 28 warps at 72 registers a thread; warpgroup 0 drops
-  // to 40 and the expanders rise to 80, which hold a chunk in flight each.
-  static constexpr bool kSplitRegs = kWide || (kFp4 && NR == 16);
+  // 4-bit cache: launched with 80 (16 rows, 768 threads) or 96 registers per
+  // thread (640 threads), warpgroup 0 drops to 48 and the rest goes to the
+  // softmax and expander warpgroups as each needs, the split using up the
+  // launch's registers.
+  static constexpr bool kSplitRegs = kWide || kFp4;
   static constexpr int kIdleWarps = kSplitRegs ? 1 : 0;
   static constexpr int kSoftmaxWarp0 = 1 + kMmaWarps + kIdleWarps;
-  static constexpr int kRegsLaunch = kFp4 ? RL : 128, kRegsLow = kFp4 ? RLOW : 56,
-                       kRegsHigh = kFp4 ? RS : 152, kRegsExpand = RE;
-  static_assert(!kWide || (kRegsLow * 128 + kRegsHigh * 128 * SWG <= kRegsLaunch * 512 &&
-                           32 * kSoftmaxWarp0 + 128 * SWG == 512),
-                "register split");
+  static constexpr int kRegsLaunch = !kFp4 ? 128 : NR == 16 ? 80 : 96;
+  static constexpr int kRegsLow = kFp4 ? 48 : 56;
+  static constexpr int kRegsHigh = !kFp4 ? 152 : NR == 16 ? 72 : kWide ? RHW : RHM;
+  static constexpr int kRegsExpand = NR == 16 ? 96 : kWide ? REW : REM;
+  static_assert(!kWide || kFp4 || 32 * kSoftmaxWarp0 + 128 * SWG == 512, "register split");
   // 4-bit cache: expander warps after the softmax warps.
-  static_assert(!kFp4 || !kWide, "the 4-bit cache has row groups of at most 48 rows");
-  static constexpr int kExpandWarps = !kFp4 ? 0 : NR == 16 ? kExpandWarps16 : 4;
+  static constexpr int kExpandWarps = !kFp4 ? 0 : NR == 16 ? 12 : kWide ? 4 : 8;
   static constexpr int kExpandWarp0 = kSoftmaxWarp0 + 4 * SWG;
   static constexpr int kThreads = 32 * (kExpandWarp0 + kExpandWarps);
   static constexpr int kRegsSplit =
@@ -414,13 +413,13 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       mbar_init(bar(BAR_FULL0 + k), 1);
       mbar_init(bar(BAR_EMPTY0 + k), 1);
     }
-    if constexpr (kFp4) {
+    if constexpr (kFp4 && !C::kBlockStages) {
       for (int k = 0; k < C::NST; ++k) mbar_init(sbase + C::expanded_bar(k), 8);
     }
     if constexpr (C::kBlockStages) {
       for (int k = 0; k < C::NST; ++k)
         for (int b = 0; b < 5; ++b) {
-          mbar_init(full_blk(k, b), 1);
+          mbar_init(full_blk(k, b), kFp4 && b < 4 ? 2 : 1);  // 4-bit cache: two chunks
           mbar_init(empty_blk(k, b), 1);
         }
     }
@@ -466,8 +465,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
   if (warp < C::kSoftmaxWarp0) {
     // Producer, MMA issuers (and the 96-row configuration's idle warp): one
     // warpgroup, whose registers go to the softmax warpgroups.
-    if constexpr (C::kSplitRegs)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsLow));
+    if constexpr (C::kSplitRegs) set_registers<C::kRegsLaunch, C::kRegsLow>();
     if (warp == 0) {
       // ================= TMA producer =================
       if (lane == 0) {
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         int window_next = load_window(1, window_next_nv);
         // 4-bit cache: pages go to L2 kPrefetch tiles ahead, so that the
         // expanders' loads, of which registers hold one tile, find them there.
-        constexpr int kPrefetch = kPrefetchTiles;
+        constexpr int kPrefetch = C::kWide ? PFW : PFT;
         auto prefetch_tile = [&](int j, int i) {
           if constexpr (kFp4) {
             const bool here = (j >> 3) == (i >> 3);
@@ -622,7 +620,31 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           const int nload = __popc(__ballot_sync(0xffffffffu, lane < 4 && my_load));
           const uint32_t kv = sbase + C::kKV + st * kTileBytes;
           const int row = my_page * MLA_PAGE_SIZE;
-          if constexpr (C::kBlockStages) {
+          if constexpr (C::kBlockStages && kFp4) {
+            // The rope block; the latent blocks are the expander warps' work.
+            if (round > 0) {
+              ok = mbar_wait_abort<kFp4>(empty_blk(st, 4), (round - 1) & 1, p.wait_cycles,
+                                         abort_flag);
+              ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+              if (!ok) {
+                if (lane == 0) {
+                  report(p.status, MLA_ERR_TIMEOUT);
+                  *abort_flag = 1;
+                }
+                break;
+              }
+            }
+            const uint32_t fb = full_blk(st, 4);
+            if (lane == 0) {
+              if (kGather) stage_info[st] = info;
+              mbar_arrive_expect_tx(fb, nload * kPageRopeBytes);
+            }
+            __syncwarp();
+            if (lane < 4 && my_load)
+              tma_load_3d_hint(kv + kRopeOffset + lane * kPageRopeBytes, &tm_kv_rope, 0, 0, my_page,
+                               fb, pol);
+            __syncwarp();
+          } else if constexpr (C::kBlockStages) {
             // Block by block as the previous tile of this stage releases them:
             // the rope block after its QK, latent block d after its PV block d.
             // The rows-loaded word goes out with the first block's barrier.
@@ -701,7 +723,8 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             // for tile k (their release needed it); that tile's own blocks
             // are one phase ahead, waited for after this loop.
             const int skip = (k + C::NST == issued) ? armed_part : 0;
-            for (int bi = skip; bi < 5; ++bi)
+            // (4-bit cache: the copies fill the rope blocks only.)
+            for (int bi = skip; bi < (kFp4 ? 1 : 5); ++bi)
               mbar_wait(full_blk(k % C::NST, bi == 0 ? 4 : bi - 1), (k / C::NST) & 1,
                         kWaitLimitCycles);
           } else {
@@ -740,10 +763,13 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           for (int ks = 0; ks < 4; ++ks) {
             const uint32_t acc = (j > 0 || ks > 0) ? 1u : 0u;
             if constexpr (kFp4) {
-              umma_f8_halves(tmem + C::kOCol + d * C::OW,
-                             a0 + ((d * kLatBlockBytes + ks * 4096) >> 4),
-                             smem_desc_hi(1024, kLayoutSW128), b0 + ((ks * 512) >> 4),
-                             smem_desc_hi(2048, kLayoutNone), kIdPV, acc);
+              const uint32_t a = a0 + ((d * kLatBlockBytes + ks * 4096) >> 4);
+              umma_f8_halves(tmem + C::kOCol + d * C::OW, a, smem_desc_hi(1024, kLayoutSW128),
+                             b0 + ((ks * 512) >> 4), smem_desc_hi(2048, kLayoutNone), kIdPV, acc);
+              if constexpr (C::kWide)
+                umma_f8_halves(tmem + C::kOCol + d * C::OW, a, smem_desc_hi(1024, kLayoutSW128),
+                               b0 + ((C::kPHalf + ks * 512) >> 4), smem_desc_hi(2048, kLayoutNone),
+                               kIdPV, 1u);
             } else {
               const uint64_t a = smem_desc(kv + d * kLatBlockBytes + ks * 4096, 16384, 1024,
                                            kLayoutSW128);
@@ -769,6 +795,15 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       // the latent blocks, 16-17 the rope block.
       auto qk_step = [&](int ist, int sb, int kk, bool acc) {
         const uint32_t kv = sbase + C::kKV + ist * kTileBytes;
+        if constexpr (kFp4) {
+          const int d = kk >> 2, sub = kk & 3;  // the rope block is block 4
+          const uint32_t hi = kk < 16 ? smem_desc_hi(1024, kLayoutSW128)
+                                      : smem_desc_hi(512, kLayoutSW64);
+          umma_f8_halves(tmem + sb * NR, smem_desc_lo(kv, 16) + ((d * kLatBlockBytes + sub * 32) >> 4),
+                         hi, smem_desc_lo(sbase + C::kQ, 16) + ((d * NR * 128 + sub * 32) >> 4), hi,
+                         kIdQK, acc ? 1u : 0u);
+          return;
+        }
         uint64_t a, bd;
         if (kk < 16) {
           const int d = kk >> 2, sub = kk & 3;
@@ -784,25 +819,8 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       // QK of tile i (KV in stage ist) into S buffer sb; lane 0 issues.
       auto issue_qk = [&](int ist, int sb) {
         tc_fence_after();
-        if constexpr (kFp4) {
-          const uint32_t kv = sbase + C::kKV + ist * kTileBytes;
-          const uint32_t a0 = smem_desc_lo(kv, 16), b0 = smem_desc_lo(sbase + C::kQ, 16);
-          const uint32_t d = tmem + sb * NR;
 #pragma unroll
-          for (int kk = 0; kk < 16; ++kk)
-            umma_f8_halves(d, a0 + (((kk >> 2) * kLatBlockBytes + (kk & 3) * 32) >> 4),
-                           smem_desc_hi(1024, kLayoutSW128),
-                           b0 + (((kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4),
-                           smem_desc_hi(1024, kLayoutSW128), kIdQK, kk > 0 ? 1u : 0u);
-#pragma unroll
-          for (int sub = 0; sub < 2; ++sub)
-            umma_f8_halves(d, a0 + ((kRopeOffset + sub * 32) >> 4),
-                           smem_desc_hi(512, kLayoutSW64), b0 + ((4 * NR * 128 + sub * 32) >> 4),
-                           smem_desc_hi(512, kLayoutSW64), kIdQK, 1u);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < 18; ++kk) qk_step(ist, sb, kk, kk > 0);
-        }
+        for (int kk = 0; kk < 18; ++kk) qk_step(ist, sb, kk, kk > 0);
         umma_commit(bar(BAR_SFULL0 + sb));
       };
       if (warp == 1) {
@@ -828,7 +846,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             w = !expired_here(p, WAIT_TILE_FULL, j) &&
                 mbar_wait_abort<kFp4>(C::kBlockStages ? full_blk(st, 4) : bar(BAR_FULL0 + st), round & 1,
                                 p.wait_cycles, abort_flag);
-            if constexpr (kFp4) {
+            if constexpr (kFp4 && !C::kBlockStages) {
               if (w)
                 w = mbar_wait_abort<kFp4>(sbase + C::expanded_bar(st), round & 1, p.wait_cycles,
                                     abort_flag);
@@ -869,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
                 }
                 zero_unloaded_rows<kGather>(base + C::kKV + st * kTileBytes, lane, info, valid);
               }
-              if (lane == 0) {
+              if (kFp4 ? elect_one() : lane == 0) {
                 tc_fence_after();
                 qk_step(st, sb, 16, false);
                 qk_step(st, sb, 17, true);
@@ -881,7 +899,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
                   w = __all_sync(0xffffffffu, w && !*abort_flag);
                   if (!w) break;
                 }
-                if (lane == 0) {
+                if (kFp4 ? elect_one() : lane == 0) {
                   tc_fence_after();
 #pragma unroll
                   for (int sub = 0; sub < 4; ++sub) qk_step(st, sb, blk * 4 + sub, true);
@@ -893,7 +911,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
                 break;
               }
               // S^T is complete, and the rope block free, once these MMAs are.
-              if (lane == 0) {
+              if (kFp4 ? elect_one() : lane == 0) {
                 umma_commit(bar(BAR_SFULL0 + sb));
                 umma_commit(empty_blk(st, 4));
               }
@@ -959,149 +977,289 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     }
   } else if (kFp4 && warp >= C::kExpandWarp0) {
     if constexpr (kFp4) {
-      if constexpr (C::kSplitRegs && C::kRegsExpand > C::kRegsLaunch)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsExpand));
+      set_registers<C::kRegsLaunch, C::kRegsExpand>();
       // ================= expanders (4-bit cache) =================
-      // They fill the four latent blocks of each stage: 16 tokens (half a
-      // page, a "chunk") at a time, each lane loads one 16-byte block of codes
-      // of 8 of them and those blocks' scales, expands them to E4M3 codes in
-      // registers and stores them where TMA's 128-byte swizzle would have put
-      // an E4M3 cache's bytes.  Going through registers instead of a staging buffer saves
-      // a write and a read of shared memory, whose bandwidth the two MMAs'
-      // operand reads already fill.
-      //
-      // Lane -> block (lane / 8) * 4 + lane % 4 (its latent block of the tile
-      // is lane / 8), token 2 k + (lane / 4) % 2: a warp's load covers two
-      // whole rows of codes (512 contiguous bytes), and the 8 lanes that store
-      // together hit the 8 chunks of two neighbouring swizzled rows, all
-      // banks once.
-      MLA_ITEM_NAMES(first);
-      constexpr int W = C::kExpandWarps;
-      const int ew = warp - C::kExpandWarp0;
-      const int blk = (lane >> 3) * 4 + (lane & 3), par = (lane >> 2) & 1;
-      const int n_chunks = n_tiles * 8;  // this warp takes chunks ew, ew + W, ...
-      const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-      const int page0 = t0 / MLA_PAGE_SIZE;
-      const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;  // exclusive
-      // Page of this warp's chunk number 32 w + lane (-1: not loaded; the QK warp
-      // zeroes those rows).  Bad ids are reported by the producer, which reads
-      // page 0 in their place, as here.
-      // key0 (restricted key sets): the first key position of the page.
-      auto chunk_window = [&](int w, int& key0) -> int {
-        key0 = 0;
-        const int ch = ew + W * (w * 32 + lane);
-        if (ch >= n_chunks) return -1;
-        const int pi = page0 + (ch >> 1);
-        if (pi >= page_end) return -1;
-        int lp = pi;
-        if constexpr (kGather) {
-          if (sparse) lp = (pi < p.topk) ? p.block_idx[static_cast<int64_t>(b) * p.topk + pi] : -1;
-          const int64_t first_pos = static_cast<int64_t>(lp) * MLA_PAGE_SIZE;
-          if (lp < 0 || first_pos >= (sparse ? win_hi : tok_end) ||
-              first_pos + MLA_PAGE_SIZE <= win_lo)
-            return -1;
-          key0 = lp * MLA_PAGE_SIZE;
-        }
-        const int pg = pt[lp];
-        return (pg < 0 || pg >= p.num_pages) ? 0 : pg;
-      };
-      int key0, key0_next;
-      int window = chunk_window(0, key0), window_next = chunk_window(1, key0_next);
-      // A chunk in registers: the codes of tokens 2 k + par, the block's 16
-      // scale codes and (restricted key sets) how many of its tokens, which
-      // come first, lie before the key window.
-      uint4 v[8], sc;
-      const uint8_t* src;  // the page whose codes are loaded next
-      int hidden = 0, hidden_next = 0;
-      const int half = (ew & 1) * 16;
-      static_assert(W % 2 == 0, "a warp's chunks are the same half of their pages");
-      // Page of this warp's chunk number n, in order (page 0 for one that is not loaded, so that
-      // its loads need no condition: a merge with the old values would wait
-      // for them).
-      auto locate = [&](int n) {
-        if ((n & 31) == 0 && n > 0) {
-          window = window_next;
-          key0 = key0_next;
-          window_next = chunk_window((n >> 5) + 1, key0_next);
-        }
-        const int pg = __shfl_sync(0xffffffffu, window, n & 31);
-        if constexpr (kGather)
-          hidden_next = win_lo - __shfl_sync(0xffffffffu, key0, n & 31) - half;
-        src = p.kv_fp4 + static_cast<int64_t>(max(pg, 0)) * MLA_FP4_PAGE_BYTES;
-      };
-      auto codes_of = [&](int k) {
-        return ldg_stream(src + (half + 2 * k + par) * kFp4RowCodes + blk * 16);
-      };
-      auto scales = [&]() { return ldg_stream(src + kFp4ScaleOffset + blk * MLA_PAGE_SIZE + half); };
-      locate(0);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = codes_of(k);
-      sc = scales();
-#pragma unroll 1
-      for (int ch = ew, n = 0; ch < n_chunks; ch += W, ++n) {
-        const int tile = ch >> 3, st = tile % C::NST, round = tile / C::NST;
-        hidden = hidden_next;
-        // This lane's scale codes: bytes 2 k + par, two to a word.
-        uint32_t scw[4] = {(sc.x >> (8 * par)) & 0x000F000Fu, (sc.y >> (8 * par)) & 0x000F000Fu,
-                           (sc.z >> (8 * par)) & 0x000F000Fu, (sc.w >> (8 * par)) & 0x000F000Fu};
-        locate(n + 1);
-        sc = scales();
-        if (round > 0) {
-          bool w = mbar_wait_abort<kFp4>(bar(BAR_EMPTY0 + st), (round - 1) & 1, p.wait_cycles,
-                                   abort_flag);
-          w = __all_sync(0xffffffffu, w && !*abort_flag);
-          if (!w) {
-            if (lane == 0) {
-              report(p.status, MLA_ERR_TIMEOUT);
-              *abort_flag = 1;
-            }
-            break;
+      if constexpr (C::kBlockStages) {
+        // They fill the four latent blocks of each stage, half a block (128 dims
+        // of 64 tokens, a "chunk") at a time in the order the QK warp takes them:
+        // each lane loads 8 16-byte blocks of codes and their scales, expands
+        // them to E4M3 codes in registers and stores them where TMA's 128-byte
+        // swizzle would have put an E4M3 cache's bytes.  Going through registers
+        // instead of a staging buffer saves a write and a read of shared memory,
+        // whose bandwidth the two MMAs' operand reads already fill.
+        //
+        // Lane -> block lane % 4 of the chunk's four, tokens par + 2 k + 8 (lane / 8)
+        // (k < 4) of each of the chunk's two pages, par = (lane / 4) % 2: the 8
+        // lanes that store together hit the 8 chunks of two neighbouring swizzled
+        // rows, all banks once, and a lane's four scale codes of a page lie within
+        // 8 aligned bytes.
+        MLA_ITEM_NAMES(first);
+        constexpr int W = C::kExpandWarps;
+        const int ew = warp - C::kExpandWarp0;
+        const int par = (lane >> 2) & 1, tok8 = (lane >> 3) * 8;
+        const int n_chunks = n_tiles * 8;  // this warp takes chunks ew, ew + W, ...
+        const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+        const int page0 = t0 / MLA_PAGE_SIZE;
+        const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;  // exclusive
+        // The two pages of this warp's chunk number 16 w + lane / 2, one a lane:
+        // page 0 in the place of one that is not loaded (the QK warp zeroes its
+        // rows) or has a bad id (the producer reports it and reads page 0, too).
+        // hide (restricted key sets): how many rows lie before the key window.
+        auto chunk_window = [&](int w, int& hide) -> int {
+          hide = 0;
+          const int ch = ew + W * (w * 16 + (lane >> 1));
+          if (ch >= n_chunks) return 0;
+          const int pi = page0 + (ch >> 3) * 4 + (ch & 1) * 2 + (lane & 1);
+          if (pi >= page_end) return 0;
+          int lp = pi;
+          if constexpr (kGather) {
+            if (sparse) lp = (pi < p.topk) ? p.block_idx[static_cast<int64_t>(b) * p.topk + pi] : -1;
+            const int64_t first_pos = static_cast<int64_t>(lp) * MLA_PAGE_SIZE;
+            if (lp < 0 || first_pos >= (sparse ? win_hi : tok_end) ||
+                first_pos + MLA_PAGE_SIZE <= win_lo)
+              return 0;
+            hide = max(0, static_cast<int>(win_lo - first_pos));
           }
-        }
-        uint8_t* row = base + C::kKV + st * kTileBytes + (lane >> 3) * kLatBlockBytes +
-                       ((ch & 7) * 16 + par) * 128;
-        const uint32_t c0 = (((lane & 3) * 2) ^ par) * 16;  // swizzled chunk of token par
-        // Scales below 2^-5 and NaN blocks, which the arithmetic table does
-        // not cover: rare, and decided once per chunk for the whole warp.
-        bool odd_scale = false;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          odd_scale |= (((scw[m] - 0x00030003u) | (scw[m] + 0x00010001u)) & 0x80108010u) != 0;
-        odd_scale = __any_sync(0xffffffffu, odd_scale || (kGather && hidden > 0));
-        // One block a step: expand, store, and load the next chunk's codes into
-        // the same registers, so that a whole chunk is always in flight.
-        auto step = [&](int k, uint2 t) {
-          const uint2 a = fp4_expand8(v[k].x, t), bb = fp4_expand8(v[k].y, t);
-          const uint2 cc = fp4_expand8(v[k].z, t), dd = fp4_expand8(v[k].w, t);
-          v[k] = codes_of(k);
-          uint8_t* dst = row + k * 256;
-          const uint32_t c = c0 ^ ((2 * k & 7) * 16);
-          *reinterpret_cast<uint4*>(dst + c) = make_uint4(a.x, a.y, bb.x, bb.y);
-          *reinterpret_cast<uint4*>(dst + (c ^ 16)) = make_uint4(cc.x, cc.y, dd.x, dd.y);
+          const int pg = pt[lp];
+          return (pg < 0 || pg >= p.num_pages) ? 0 : pg;
         };
-        if (!odd_scale) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            step(k, fp4_scale_table_normal((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu));
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint2 t = fp4_scale_table((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
-            // A key before the window has weight 0, and so must not be a NaN.
-            if (kGather && 2 * k + par < hidden) t = make_uint2(0u, 0u);
-            step(k, t);
+        int hide, hide_next;
+        int window = chunk_window(0, hide), window_next = chunk_window(1, hide_next);
+        // A chunk in registers: codes of tokens par + 2 (k % 4) + tok8 of page
+        // k / 4, and those tokens' scale codes.  Its loads have no condition: a
+        // merge with the old values would wait for them.
+        uint4 v[8];
+        uint2 sc[2];
+        const uint8_t* src[2];  // where the next chunk's codes are loaded from
+        const uint8_t* ssrc[2];
+        int hidden[2] = {0, 0}, hidden_next[2] = {0, 0};
+        auto locate = [&](int n) {
+          if ((n & 15) == 0 && n > 0) {
+            window = window_next;
+            hide = hide_next;
+            window_next = chunk_window((n >> 4) + 1, hide_next);
           }
+          const int d = ((ew + W * n) >> 1) & 3;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int pg = __shfl_sync(0xffffffffu, window, 2 * (n & 15) + i);
+            if constexpr (kGather)
+              hidden_next[i] = __shfl_sync(0xffffffffu, hide, 2 * (n & 15) + i);
+            const uint8_t* page = p.kv_fp4 + static_cast<int64_t>(pg) * MLA_FP4_PAGE_BYTES;
+            src[i] = page + (tok8 + par) * kFp4RowCodes + d * 64 + (lane & 3) * 16;
+            ssrc[i] = page + kFp4ScaleOffset + (d * 4 + (lane & 3)) * MLA_PAGE_SIZE + tok8;
+          }
+        };
+        auto codes_of = [&](int k) {
+          return ldg_stream(src[k >> 2] + (k & 3) * (2 * kFp4RowCodes));
+        };
+        locate(0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = codes_of(k);
+        sc[0] = ldg_stream8(ssrc[0]);
+        sc[1] = ldg_stream8(ssrc[1]);
+        const uint32_t c0 = (((lane & 3) * 2) ^ par) * 16;  // swizzled chunk of token par
+#pragma unroll 1
+        for (int ch = ew, n = 0; ch < n_chunks; ch += W, ++n) {
+          const int tile = ch >> 3, d = (ch >> 1) & 3, st = tile % C::NST, round = tile / C::NST;
+          // This lane's scale codes: bytes 2 k + par, two to a word.
+          const uint32_t scw[4] = {(sc[0].x >> (8 * par)) & 0x000F000Fu,
+                                   (sc[0].y >> (8 * par)) & 0x000F000Fu,
+                                   (sc[1].x >> (8 * par)) & 0x000F000Fu,
+                                   (sc[1].y >> (8 * par)) & 0x000F000Fu};
+          hidden[0] = hidden_next[0];
+          hidden[1] = hidden_next[1];
+          locate(n + 1);
+          sc[0] = ldg_stream8(ssrc[0]);
+          sc[1] = ldg_stream8(ssrc[1]);
+          if (round > 0) {
+            bool w = mbar_wait_abort<kFp4>(empty_blk(st, d), (round - 1) & 1, p.wait_cycles,
+                                           abort_flag);
+            w = __all_sync(0xffffffffu, w && !*abort_flag);
+            if (!w) {
+              if (lane == 0) {
+                report(p.status, MLA_ERR_TIMEOUT);
+                *abort_flag = 1;
+              }
+              break;
+            }
+          }
+          uint8_t* row = base + C::kKV + st * kTileBytes + d * kLatBlockBytes +
+                         ((ch & 1) * 64 + tok8 + par) * 128;
+          // Scales below 2^-5 and NaN blocks, which the arithmetic table does
+          // not cover: rare, and decided once per chunk for the whole warp.
+          bool odd_scale = false;
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            odd_scale |= (((scw[m] - 0x00030003u) | (scw[m] + 0x00010001u)) & 0x80108010u) != 0;
+          odd_scale = __any_sync(0xffffffffu, odd_scale || (kGather && (hidden[0] | hidden[1]) > 0));
+          // One block a step: expand, store, and load the next chunk's codes into
+          // the same registers, so that a whole chunk is always in flight.
+          auto step = [&](int k, uint2 t) {
+            const uint2 a = fp4_expand8(v[k].x, t), bb = fp4_expand8(v[k].y, t);
+            const uint2 cc = fp4_expand8(v[k].z, t), dd = fp4_expand8(v[k].w, t);
+            v[k] = codes_of(k);
+            uint8_t* dst = row + (k >> 2) * (32 * 128) + (k & 3) * 256;
+            const uint32_t c = c0 ^ ((2 * k & 7) * 16);
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(a.x, a.y, bb.x, bb.y);
+            *reinterpret_cast<uint4*>(dst + (c ^ 16)) = make_uint4(cc.x, cc.y, dd.x, dd.y);
+          };
+          if (!odd_scale) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              step(k, fp4_scale_table_normal((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint2 t = fp4_scale_table((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
+              // A key before the window has weight 0, and so must not be a NaN.
+              if (kGather && tok8 + par + 2 * (k & 3) < hidden[k >> 2]) t = make_uint2(0u, 0u);
+              step(k, t);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full_blk(st, d));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sbase + C::expanded_bar(st));
+      } else {
+        // They fill the four latent blocks of each stage: 16 tokens (half a
+        // page, a "chunk") at a time, each lane loads one 16-byte block of codes
+        // of 8 of them and those blocks' scales, expands them to E4M3 codes in
+        // registers and stores them where TMA's 128-byte swizzle would have put
+        // an E4M3 cache's bytes.  Going through registers instead of a staging buffer saves
+        // a write and a read of shared memory, whose bandwidth the two MMAs'
+        // operand reads already fill.
+        //
+        // Lane -> block (lane / 8) * 4 + lane % 4 (its latent block of the tile
+        // is lane / 8), token 2 k + (lane / 4) % 2: a warp's load covers two
+        // whole rows of codes (512 contiguous bytes), and the 8 lanes that store
+        // together hit the 8 chunks of two neighbouring swizzled rows, all
+        // banks once.
+        MLA_ITEM_NAMES(first);
+        constexpr int W = C::kExpandWarps;
+        const int ew = warp - C::kExpandWarp0;
+        const int blk = (lane >> 3) * 4 + (lane & 3), par = (lane >> 2) & 1;
+        const int n_chunks = n_tiles * 8;  // this warp takes chunks ew, ew + W, ...
+        const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+        const int page0 = t0 / MLA_PAGE_SIZE;
+        const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;  // exclusive
+        // Page of this warp's chunk number 32 w + lane (-1: not loaded; the QK warp
+        // zeroes those rows).  Bad ids are reported by the producer, which reads
+        // page 0 in their place, as here.
+        // key0 (restricted key sets): the first key position of the page.
+        auto chunk_window = [&](int w, int& key0) -> int {
+          key0 = 0;
+          const int ch = ew + W * (w * 32 + lane);
+          if (ch >= n_chunks) return -1;
+          const int pi = page0 + (ch >> 1);
+          if (pi >= page_end) return -1;
+          int lp = pi;
+          if constexpr (kGather) {
+            if (sparse) lp = (pi < p.topk) ? p.block_idx[static_cast<int64_t>(b) * p.topk + pi] : -1;
+            const int64_t first_pos = static_cast<int64_t>(lp) * MLA_PAGE_SIZE;
+            if (lp < 0 || first_pos >= (sparse ? win_hi : tok_end) ||
+                first_pos + MLA_PAGE_SIZE <= win_lo)
+              return -1;
+            key0 = lp * MLA_PAGE_SIZE;
+          }
+          const int pg = pt[lp];
+          return (pg < 0 || pg >= p.num_pages) ? 0 : pg;
+        };
+        int key0, key0_next;
+        int window = chunk_window(0, key0), window_next = chunk_window(1, key0_next);
+        // A chunk in registers: the codes of tokens 2 k + par, the block's 16
+        // scale codes and (restricted key sets) how many of its tokens, which
+        // come first, lie before the key window.
+        uint4 v[8], sc;
+        const uint8_t* src;  // the page whose codes are loaded next
+        int hidden = 0, hidden_next = 0;
+        const int half = (ew & 1) * 16;
+        static_assert(W % 2 == 0, "a warp's chunks are the same half of their pages");
+        // Page of this warp's chunk number n, in order (page 0 for one that is not loaded, so that
+        // its loads need no condition: a merge with the old values would wait
+        // for them).
+        auto locate = [&](int n) {
+          if ((n & 31) == 0 && n > 0) {
+            window = window_next;
+            key0 = key0_next;
+            window_next = chunk_window((n >> 5) + 1, key0_next);
+          }
+          const int pg = __shfl_sync(0xffffffffu, window, n & 31);
+          if constexpr (kGather)
+            hidden_next = win_lo - __shfl_sync(0xffffffffu, key0, n & 31) - half;
+          src = p.kv_fp4 + static_cast<int64_t>(max(pg, 0)) * MLA_FP4_PAGE_BYTES;
+        };
+        auto codes_of = [&](int k) {
+          return ldg_stream(src + (half + 2 * k + par) * kFp4RowCodes + blk * 16);
+        };
+        auto scales = [&]() { return ldg_stream(src + kFp4ScaleOffset + blk * MLA_PAGE_SIZE + half); };
+        locate(0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = codes_of(k);
+        sc = scales();
+#pragma unroll 1
+        for (int ch = ew, n = 0; ch < n_chunks; ch += W, ++n) {
+          const int tile = ch >> 3, st = tile % C::NST, round = tile / C::NST;
+          hidden = hidden_next;
+          // This lane's scale codes: bytes 2 k + par, two to a word.
+          uint32_t scw[4] = {(sc.x >> (8 * par)) & 0x000F000Fu, (sc.y >> (8 * par)) & 0x000F000Fu,
+                             (sc.z >> (8 * par)) & 0x000F000Fu, (sc.w >> (8 * par)) & 0x000F000Fu};
+          locate(n + 1);
+          sc = scales();
+          if (round > 0) {
+            bool w = mbar_wait_abort<kFp4>(bar(BAR_EMPTY0 + st), (round - 1) & 1, p.wait_cycles,
+                                     abort_flag);
+            w = __all_sync(0xffffffffu, w && !*abort_flag);
+            if (!w) {
+              if (lane == 0) {
+                report(p.status, MLA_ERR_TIMEOUT);
+                *abort_flag = 1;
+              }
+              break;
+            }
+          }
+          uint8_t* row = base + C::kKV + st * kTileBytes + (lane >> 3) * kLatBlockBytes +
+                         ((ch & 7) * 16 + par) * 128;
+          const uint32_t c0 = (((lane & 3) * 2) ^ par) * 16;  // swizzled chunk of token par
+          // Scales below 2^-5 and NaN blocks, which the arithmetic table does
+          // not cover: rare, and decided once per chunk for the whole warp.
+          bool odd_scale = false;
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            odd_scale |= (((scw[m] - 0x00030003u) | (scw[m] + 0x00010001u)) & 0x80108010u) != 0;
+          odd_scale = __any_sync(0xffffffffu, odd_scale || (kGather && hidden > 0));
+          // One block a step: expand, store, and load the next chunk's codes into
+          // the same registers, so that a whole chunk is always in flight.
+          auto step = [&](int k, uint2 t) {
+            const uint2 a = fp4_expand8(v[k].x, t), bb = fp4_expand8(v[k].y, t);
+            const uint2 cc = fp4_expand8(v[k].z, t), dd = fp4_expand8(v[k].w, t);
+            v[k] = codes_of(k);
+            uint8_t* dst = row + k * 256;
+            const uint32_t c = c0 ^ ((2 * k & 7) * 16);
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(a.x, a.y, bb.x, bb.y);
+            *reinterpret_cast<uint4*>(dst + (c ^ 16)) = make_uint4(cc.x, cc.y, dd.x, dd.y);
+          };
+          if (!odd_scale) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              step(k, fp4_scale_table_normal((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint2 t = fp4_scale_table((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
+              // A key before the window has weight 0, and so must not be a NaN.
+              if (kGather && 2 * k + par < hidden) t = make_uint2(0u, 0u);
+              step(k, t);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sbase + C::expanded_bar(st));
+        }
       }
     }
   } else {
-    if constexpr (C::kSplitRegs && C::kRegsHigh > C::kRegsLaunch)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsHigh));
-    else if constexpr (C::kSplitRegs && C::kRegsHigh < C::kRegsLaunch)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsHigh));
+    if constexpr (C::kSplitRegs) set_registers<C::kRegsLaunch, C::kRegsHigh>();
     // ===== softmax warpgroups (warps kSoftmaxWarp0 .. kSoftmaxWarp0 + 4*SWG - 1) =====
     // SWG warpgroups share each tile: warpgroup g owns rows [g*NRH, (g+1)*NRH)
     // of every token (two warps per SM sub-partition when SWG = 2, so one

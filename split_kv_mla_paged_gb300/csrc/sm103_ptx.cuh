@@ -147,6 +147,14 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
+__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
@@ -168,6 +176,19 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // ---------------------------------------------------------------- named barriers
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// ---------------------------------------------------------------- registers
+// A warpgroup goes from kFrom registers per thread to kTo.  Every warpgroup of
+// a CTA that splits its registers calls it with its share: an increase waits
+// until the others' decreases have freed enough, so the shares must not add up
+// to more than the launch's registers.
+template <int kFrom, int kTo>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (kTo < kFrom)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTo));
+  else if constexpr (kTo > kFrom)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTo));
 }
 
 // ---------------------------------------------------------------- tcgen05 / TMEM

@@ -183,7 +183,7 @@ def test_decode_fp4_refusals(lib):
     assert call(O(None, None, None, float("inf"))) == mla.MLA_ERR_INVALID_ARG
     assert call(O(None, None, None, 1.0, None, None, None, FAKE, 0)) == mla.MLA_ERR_INVALID_ARG
     assert call(O(None, None, None, 1.0, None, None, None, None, 0, 0, 3)) == mla.MLA_ERR_INVALID_ARG
-    # 96 rows are two row groups, so an item list may be twice as long as splits.
+    # At most batch * max_splits * row groups items.
     assert call(O(None, None, None, 1.0, None, None, None, FAKE, 5), a11=8) == mla.MLA_ERR_INVALID_ARG
     sp = args[:6] + [FAKE, 8] + args[6:]
     assert lib.mla_decode_fp4_sparse(*sp[:6], None, *sp[7:], None, None) == mla.MLA_ERR_INVALID_ARG
