@@ -26,18 +26,6 @@ constexpr uint32_t kPageRopeBytes = MLA_PAGE_SIZE * 64;      // 2048
 constexpr uint32_t kPageBytes = MLA_PAGE_SIZE * MLA_HEAD_DIM;
 
 
-#ifndef RHW
-#define RHW 120
-#define REW 72
-#define RHM 128
-#define REM 88
-#endif
-#ifndef PFT
-#define PFT 3
-#endif
-#ifndef PFW
-#define PFW 3
-#endif
 // kFp4: the 4-bit cache.  Everything downstream of the KV stages is the E4M3
 // kernel; only how a stage is filled differs (see the expander warps).
 template <int NR, bool kFp4 = false>
@@ -78,16 +66,19 @@ struct Cfg {
   // (which spilled): MTP q8 B16 128K 371.6 -> 361.2 us, B1 45.1 -> 41.4 us,
   // H96 q8 B1 1M 1332.7 -> 1305.7 us.
   // 4-bit cache: launched with 80 (16 rows, 768 threads) or 96 registers per
-  // thread (640 threads), warpgroup 0 drops to 48 and the rest goes to the
-  // softmax and expander warpgroups as each needs, the split using up the
-  // launch's registers.
+  // thread (640 threads), warpgroup 0 drops to 48 (32 for 96 rows) and the
+  // softmax and expander warpgroups share the rest as each needs.  Measured
+  // for 96 rows (softmax / expander / warpgroup 0): 128 / 64 / 32 against
+  // 128 / 56 / 40 and 120 / 72 / 48, H12 q8 B16 128K 449.5 against 460.5 and
+  // 458.0 us; for 32 and 48 rows 128 / 88 against 120 / 96 and 112 / 104, H24
+  // B4 128K 75.5 against 76-79 us.
   static constexpr bool kSplitRegs = kWide || kFp4;
   static constexpr int kIdleWarps = kSplitRegs ? 1 : 0;
   static constexpr int kSoftmaxWarp0 = 1 + kMmaWarps + kIdleWarps;
   static constexpr int kRegsLaunch = !kFp4 ? 128 : NR == 16 ? 80 : 96;
-  static constexpr int kRegsLow = kFp4 ? 48 : 56;
-  static constexpr int kRegsHigh = !kFp4 ? 152 : NR == 16 ? 72 : kWide ? RHW : RHM;
-  static constexpr int kRegsExpand = NR == 16 ? 96 : kWide ? REW : REM;
+  static constexpr int kRegsLow = !kFp4 ? 56 : kWide ? 32 : 48;
+  static constexpr int kRegsHigh = !kFp4 ? 152 : NR == 16 ? 72 : 128;
+  static constexpr int kRegsExpand = NR == 16 ? 96 : kWide ? 64 : 88;
   static_assert(!kWide || kFp4 || 32 * kSoftmaxWarp0 + 128 * SWG == 512, "register split");
   // 4-bit cache: expander warps after the softmax warps.
   static constexpr int kExpandWarps = !kFp4 ? 0 : NR == 16 ? 12 : kWide ? 4 : 8;
@@ -419,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     if constexpr (C::kBlockStages) {
       for (int k = 0; k < C::NST; ++k)
         for (int b = 0; b < 5; ++b) {
-          mbar_init(full_blk(k, b), kFp4 && b < 4 ? 2 : 1);  // 4-bit cache: two chunks
+          mbar_init(full_blk(k, b), kFp4 && b < 4 ? 4 : 1);  // 4-bit cache: four chunks
           mbar_init(empty_blk(k, b), 1);
         }
     }
@@ -563,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         int window_next = load_window(1, window_next_nv);
         // 4-bit cache: pages go to L2 kPrefetch tiles ahead, so that the
         // expanders' loads, of which registers hold one tile, find them there.
-        constexpr int kPrefetch = C::kWide ? PFW : PFT;
+        constexpr int kPrefetch = 3;
         auto prefetch_tile = [&](int j, int i) {
           if constexpr (kFp4) {
             const bool here = (j >> 3) == (i >> 3);
@@ -980,40 +971,38 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       set_registers<C::kRegsLaunch, C::kRegsExpand>();
       // ================= expanders (4-bit cache) =================
       if constexpr (C::kBlockStages) {
-        // They fill the four latent blocks of each stage, half a block (128 dims
-        // of 64 tokens, a "chunk") at a time in the order the QK warp takes them:
-        // each lane loads 8 16-byte blocks of codes and their scales, expands
-        // them to E4M3 codes in registers and stores them where TMA's 128-byte
-        // swizzle would have put an E4M3 cache's bytes.  Going through registers
-        // instead of a staging buffer saves a write and a read of shared memory,
-        // whose bandwidth the two MMAs' operand reads already fill.
+        // They fill the latent blocks of each stage, a page of one block (128
+        // dims of 32 tokens, a "chunk") at a time in the order the QK warp
+        // takes them: each lane loads 4 16-byte blocks of codes and their
+        // scales, expands them to E4M3 codes in registers and stores them where
+        // TMA's 128-byte swizzle would have put an E4M3 cache's bytes.
         //
-        // Lane -> block lane % 4 of the chunk's four, tokens par + 2 k + 8 (lane / 8)
-        // (k < 4) of each of the chunk's two pages, par = (lane / 4) % 2: the 8
-        // lanes that store together hit the 8 chunks of two neighbouring swizzled
-        // rows, all banks once, and a lane's four scale codes of a page lie within
-        // 8 aligned bytes.
+        // Lane -> block lane % 4 of the chunk's four, tokens par + 2 k +
+        // 8 (lane / 8) (k < 4), par = (lane / 4) % 2: the 8 lanes that store
+        // together hit the 8 chunks of two neighbouring swizzled rows, all banks
+        // once, and a lane's four scale codes lie within 8 aligned bytes.
         MLA_ITEM_NAMES(first);
         constexpr int W = C::kExpandWarps;
         const int ew = warp - C::kExpandWarp0;
         const int par = (lane >> 2) & 1, tok8 = (lane >> 3) * 8;
-        const int n_chunks = n_tiles * 8;  // this warp takes chunks ew, ew + W, ...
+        const int n_chunks = n_tiles * 16;  // this warp takes chunks ew, ew + W, ...
         const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
         const int page0 = t0 / MLA_PAGE_SIZE;
         const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;  // exclusive
-        // The two pages of this warp's chunk number 16 w + lane / 2, one a lane:
-        // page 0 in the place of one that is not loaded (the QK warp zeroes its
-        // rows) or has a bad id (the producer reports it and reads page 0, too).
-        // hide (restricted key sets): how many rows lie before the key window.
+        // Page of this warp's chunk number 32 w + lane: page 0 in the place of
+        // one that is not loaded (the QK warp zeroes its rows) or has a bad id
+        // (the producer reports it and reads page 0, too).  hide (restricted key
+        // sets): how many of its rows lie before the key window.
         auto chunk_window = [&](int w, int& hide) -> int {
           hide = 0;
-          const int ch = ew + W * (w * 16 + (lane >> 1));
+          const int ch = ew + W * (w * 32 + lane);
           if (ch >= n_chunks) return 0;
-          const int pi = page0 + (ch >> 3) * 4 + (ch & 1) * 2 + (lane & 1);
+          const int pi = page0 + (ch >> 4) * 4 + (ch & 3);
           if (pi >= page_end) return 0;
           int lp = pi;
           if constexpr (kGather) {
-            if (sparse) lp = (pi < p.topk) ? p.block_idx[static_cast<int64_t>(b) * p.topk + pi] : -1;
+            if (sparse)
+              lp = (pi < p.topk) ? p.block_idx[static_cast<int64_t>(b) * p.topk + pi] : -1;
             const int64_t first_pos = static_cast<int64_t>(lp) * MLA_PAGE_SIZE;
             if (lp < 0 || first_pos >= (sparse ? win_hi : tok_end) ||
                 first_pos + MLA_PAGE_SIZE <= win_lo)
@@ -1025,53 +1014,38 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         };
         int hide, hide_next;
         int window = chunk_window(0, hide), window_next = chunk_window(1, hide_next);
-        // A chunk in registers: codes of tokens par + 2 (k % 4) + tok8 of page
-        // k / 4, and those tokens' scale codes.  Its loads have no condition: a
-        // merge with the old values would wait for them.
-        uint4 v[8];
-        uint2 sc[2];
-        const uint8_t* src[2];  // where the next chunk's codes are loaded from
-        const uint8_t* ssrc[2];
-        int hidden[2] = {0, 0}, hidden_next[2] = {0, 0};
-        auto locate = [&](int n) {
-          if ((n & 15) == 0 && n > 0) {
+        // A chunk in registers: codes of tokens par + 2 k + tok8 and their scale
+        // codes.  Its loads have no condition: a merge with the old values would
+        // wait for them.
+        uint4 v[4];
+        uint2 sc;
+        const uint8_t* src;  // where the next chunk's codes are loaded from
+        int hidden = 0, hidden_next = 0;
+        auto locate = [&](int n) -> const uint8_t* {  // returns the address of its scales
+          if ((n & 31) == 0 && n > 0) {
             window = window_next;
             hide = hide_next;
-            window_next = chunk_window((n >> 4) + 1, hide_next);
+            window_next = chunk_window((n >> 5) + 1, hide_next);
           }
-          const int d = ((ew + W * n) >> 1) & 3;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int pg = __shfl_sync(0xffffffffu, window, 2 * (n & 15) + i);
-            if constexpr (kGather)
-              hidden_next[i] = __shfl_sync(0xffffffffu, hide, 2 * (n & 15) + i);
-            const uint8_t* page = p.kv_fp4 + static_cast<int64_t>(pg) * MLA_FP4_PAGE_BYTES;
-            src[i] = page + (tok8 + par) * kFp4RowCodes + d * 64 + (lane & 3) * 16;
-            ssrc[i] = page + kFp4ScaleOffset + (d * 4 + (lane & 3)) * MLA_PAGE_SIZE + tok8;
-          }
+          const int d = ((ew + W * n) >> 2) & 3;
+          const int pg = __shfl_sync(0xffffffffu, window, n & 31);
+          if constexpr (kGather) hidden_next = __shfl_sync(0xffffffffu, hide, n & 31);
+          const uint8_t* page = p.kv_fp4 + static_cast<int64_t>(pg) * MLA_FP4_PAGE_BYTES;
+          src = page + (tok8 + par) * kFp4RowCodes + d * 64 + (lane & 3) * 16;
+          return page + kFp4ScaleOffset + (d * 4 + (lane & 3)) * MLA_PAGE_SIZE + tok8;
         };
-        auto codes_of = [&](int k) {
-          return ldg_stream(src[k >> 2] + (k & 3) * (2 * kFp4RowCodes));
-        };
-        locate(0);
+        sc = ldg_stream8(locate(0));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = codes_of(k);
-        sc[0] = ldg_stream8(ssrc[0]);
-        sc[1] = ldg_stream8(ssrc[1]);
+        for (int k = 0; k < 4; ++k) v[k] = ldg_stream(src + k * (2 * kFp4RowCodes));
         const uint32_t c0 = (((lane & 3) * 2) ^ par) * 16;  // swizzled chunk of token par
 #pragma unroll 1
         for (int ch = ew, n = 0; ch < n_chunks; ch += W, ++n) {
-          const int tile = ch >> 3, d = (ch >> 1) & 3, st = tile % C::NST, round = tile / C::NST;
+          const int tile = ch >> 4, d = (ch >> 2) & 3, st = tile % C::NST, round = tile / C::NST;
           // This lane's scale codes: bytes 2 k + par, two to a word.
-          const uint32_t scw[4] = {(sc[0].x >> (8 * par)) & 0x000F000Fu,
-                                   (sc[0].y >> (8 * par)) & 0x000F000Fu,
-                                   (sc[1].x >> (8 * par)) & 0x000F000Fu,
-                                   (sc[1].y >> (8 * par)) & 0x000F000Fu};
-          hidden[0] = hidden_next[0];
-          hidden[1] = hidden_next[1];
-          locate(n + 1);
-          sc[0] = ldg_stream8(ssrc[0]);
-          sc[1] = ldg_stream8(ssrc[1]);
+          const uint32_t scw[2] = {(sc.x >> (8 * par)) & 0x000F000Fu,
+                                   (sc.y >> (8 * par)) & 0x000F000Fu};
+          hidden = hidden_next;
+          sc = ldg_stream8(locate(n + 1));
           if (round > 0) {
             bool w = mbar_wait_abort<kFp4>(empty_blk(st, d), (round - 1) & 1, p.wait_cycles,
                                            abort_flag);
@@ -1085,35 +1059,35 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             }
           }
           uint8_t* row = base + C::kKV + st * kTileBytes + d * kLatBlockBytes +
-                         ((ch & 1) * 64 + tok8 + par) * 128;
+                         ((ch & 3) * MLA_PAGE_SIZE + tok8 + par) * 128;
           // Scales below 2^-5 and NaN blocks, which the arithmetic table does
           // not cover: rare, and decided once per chunk for the whole warp.
           bool odd_scale = false;
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
+          for (int m = 0; m < 2; ++m)
             odd_scale |= (((scw[m] - 0x00030003u) | (scw[m] + 0x00010001u)) & 0x80108010u) != 0;
-          odd_scale = __any_sync(0xffffffffu, odd_scale || (kGather && (hidden[0] | hidden[1]) > 0));
+          odd_scale = __any_sync(0xffffffffu, odd_scale || (kGather && hidden > 0));
           // One block a step: expand, store, and load the next chunk's codes into
           // the same registers, so that a whole chunk is always in flight.
           auto step = [&](int k, uint2 t) {
             const uint2 a = fp4_expand8(v[k].x, t), bb = fp4_expand8(v[k].y, t);
             const uint2 cc = fp4_expand8(v[k].z, t), dd = fp4_expand8(v[k].w, t);
-            v[k] = codes_of(k);
-            uint8_t* dst = row + (k >> 2) * (32 * 128) + (k & 3) * 256;
-            const uint32_t c = c0 ^ ((2 * k & 7) * 16);
+            v[k] = ldg_stream(src + k * (2 * kFp4RowCodes));
+            uint8_t* dst = row + k * 256;
+            const uint32_t c = c0 ^ (2 * k * 16);
             *reinterpret_cast<uint4*>(dst + c) = make_uint4(a.x, a.y, bb.x, bb.y);
             *reinterpret_cast<uint4*>(dst + (c ^ 16)) = make_uint4(cc.x, cc.y, dd.x, dd.y);
           };
           if (!odd_scale) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < 4; ++k)
               step(k, fp4_scale_table_normal((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu));
           } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
               uint2 t = fp4_scale_table((scw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
               // A key before the window has weight 0, and so must not be a NaN.
-              if (kGather && tok8 + par + 2 * (k & 3) < hidden[k >> 2]) t = make_uint2(0u, 0u);
+              if (kGather && tok8 + par + 2 * k < hidden) t = make_uint2(0u, 0u);
               step(k, t);
             }
           }
