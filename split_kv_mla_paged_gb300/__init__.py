@@ -115,6 +115,8 @@ def library_path() -> str:
 def load_library() -> ctypes.CDLL:
     """Load libmla_decode.so (built by `build.build()`); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -558,16 +560,24 @@ def _call_on(tensor, fn, *args, stream=None) -> None:
     """fn(*args, stream) with the tensor's device current: on `stream`, or on
     that device's current stream."""
     import torch
-    dev = tensor.device
+    index = tensor.get_device()
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        handle = torch._C._cuda_getCurrentRawStream(index)
     else:
         handle = _stream_handle(stream)
-    if dev.index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         _check(fn(*args, handle))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             _check(fn(*args, handle))
+
+
+def _row_stride(t, dim: int, name: str) -> int:
+    """Stride of a dimension, which the C structure's 0 (contiguous) cannot carry."""
+    stride = t.stride(dim)
+    if stride == 0:
+        raise ValueError(f"{name} may not repeat one row (stride 0)")
+    return stride
 
 
 def mla_prologue(n_tokens: int, *, positions=None, cos_sin=None, rope_positions=None,
@@ -584,43 +594,48 @@ def mla_prologue(n_tokens: int, *, positions=None, cos_sin=None, rope_positions=
     be strided views whose last dimension is dense; either may be None.
     cos_sin is fp32 [rope_rows, 64] (32 cosines, then 32 sines)."""
     import torch
-    a = PrologueArgs()
-    a.n_tokens = int(n_tokens)
-    a.positions = _device_tensor(positions, "positions", torch.int32)
-    a.rope_halves = 1 if rope_halves else 0
-    if cos_sin is not None:
-        a.cos_sin = _device_tensor(cos_sin, "cos_sin", torch.float32)
-        a.rope_rows = int(cos_sin.shape[0] if rope_rows is None else rope_rows)
-        a.rope_positions = _device_tensor(rope_positions, "rope_positions", torch.int32)
-    a.req_idx = _device_tensor(req_idx, "req_idx", torch.int32)
-    a.status = _device_tensor(status, "status", torch.int32)
-    if kv_rows is not None:
-        a.kv_rows = _device_tensor(kv_rows, "kv_rows", torch.bfloat16, contiguous=False)
-        if kv_rows.dim() != 2 or kv_rows.shape[1] != HEAD_DIM or kv_rows.stride(1) != 1:
-            raise ValueError("kv_rows must be [n_tokens, 576] with dense rows")
-        a.kv_row_stride = kv_rows.stride(0) if kv_rows.shape[0] > 1 else HEAD_DIM
-        a.norm_weight = _device_tensor(norm_weight, "norm_weight", torch.float32)
-        a.norm_eps = float(norm_eps)
-        a.max_pages_per_req = int(max_pages_per_req)
-        a.page_table = _device_tensor(page_table, "page_table", torch.int32)
-        a.kv_pages = _device_tensor(kv_pages, "kv_pages")
-        a.num_pages = int(num_pages)
-        a.batch = int(batch)
-        a.cache_kind = int(cache_kind)
-        a.kv_scale = float(kv_scale)
-    if q_rows is not None:
-        a.q_rows = _device_tensor(q_rows, "q_rows", torch.bfloat16, contiguous=False)
-        if q_rows.dim() != 3 or q_rows.shape[2] != HEAD_DIM or q_rows.stride(2) != 1:
-            raise ValueError("q_rows must be [n_tokens, num_heads, 576] with dense rows")
-        a.q_token_stride = q_rows.stride(0) if q_rows.shape[0] > 1 else 0
-        a.q_head_stride = q_rows.stride(1) if q_rows.shape[1] > 1 else 0
-        a.q_out = _device_tensor(q_out, "q_out")
-        a.num_heads = int(num_heads)
-        a.q_kind = int(q_kind)
-        a.q_scale = float(q_scale)
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
     where = kv_rows if kv_rows is not None else q_rows
     if where is None:
         raise ValueError("mla_prologue needs kv_rows, q_rows or both")
+    rows = table = pages = weight = None
+    row_stride = token_stride = head_stride = 0
+    if kv_rows is not None:
+        rows = _device_tensor(kv_rows, "kv_rows", bf16, contiguous=False)
+        if kv_rows.dim() != 2 or kv_rows.shape[1] != HEAD_DIM or kv_rows.stride(1) != 1:
+            raise ValueError("kv_rows must be [n_tokens, 576] with dense rows")
+        if kv_rows.shape[0] < n_tokens:
+            raise ValueError("kv_rows has fewer than n_tokens rows")
+        if kv_rows.shape[0] > 1:
+            row_stride = _row_stride(kv_rows, 0, "kv_rows")
+        weight = _device_tensor(norm_weight, "norm_weight", f32)
+        table = _device_tensor(page_table, "page_table", i32)
+        pages = _device_tensor(kv_pages, "kv_pages")
+    queries = out = None
+    if q_rows is not None:
+        queries = _device_tensor(q_rows, "q_rows", bf16, contiguous=False)
+        if q_rows.dim() != 3 or q_rows.shape[2] != HEAD_DIM or q_rows.stride(2) != 1:
+            raise ValueError("q_rows must be [n_tokens, num_heads, 576] with dense rows")
+        if q_rows.shape[0] < n_tokens or q_rows.shape[1] < num_heads:
+            raise ValueError("q_rows has fewer than n_tokens tokens or num_heads heads")
+        if q_rows.shape[0] > 1:
+            token_stride = _row_stride(q_rows, 0, "q_rows")
+        if q_rows.shape[1] > 1:
+            head_stride = _row_stride(q_rows, 1, "q_rows")
+        out = _device_tensor(q_out, "q_out")
+        if out is not None and q_out.numel() < n_tokens * num_heads * HEAD_DIM:
+            raise ValueError("q_out is smaller than [n_tokens, num_heads, 576]")
+    if cos_sin is None:
+        rope_rows = 0
+    elif rope_rows is None:
+        rope_rows = cos_sin.shape[0]
+    a = PrologueArgs(n_tokens, _device_tensor(positions, "positions", i32),
+                     _device_tensor(cos_sin, "cos_sin", f32),
+                     _device_tensor(rope_positions, "rope_positions", i32), rope_rows,
+                     1 if rope_halves else 0, rows, row_stride, weight, norm_eps,
+                     max_pages_per_req, _device_tensor(req_idx, "req_idx", i32), table, pages,
+                     num_pages, batch, cache_kind, kv_scale, q_scale, queries, token_stride,
+                     head_stride, out, num_heads, q_kind, _device_tensor(status, "status", i32))
     _call_on(where, load_library().mla_prologue, ctypes.byref(a), stream=stream)
 
 

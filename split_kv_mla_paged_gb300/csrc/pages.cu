@@ -41,11 +41,21 @@ __device__ __forceinline__ bool pages_entry(const PagesParams& p, int64_t i, int
   return true;
 }
 
-// Copies `n` 16-byte vectors with the CTA's threads.
+// Copies `n` 16-byte vectors with the CTA's threads, kBatch loads in flight per
+// thread before their stores (a plain loop's next load would wait behind the
+// previous store, which the compiler must assume to overlap it).
+template <int kBatch>
 __device__ __forceinline__ void copy_vectors(const uint8_t* s, uint8_t* d, int n) {
   const uint4* sv = reinterpret_cast<const uint4*>(s);
   uint4* dv = reinterpret_cast<uint4*>(d);
-  for (int k = threadIdx.x; k < n; k += kCopyThreads) dv[k] = sv[k];
+  for (int k0 = threadIdx.x; k0 < n; k0 += kBatch * kCopyThreads) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) v[u] = sv[min(k0 + u * kCopyThreads, n - 1)];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (k0 + u * kCopyThreads < n) dv[k0 + u * kCopyThreads] = v[u];
+  }
 }
 
 // Same-kind copy: one CTA per entry.  A page of kRowBytes-byte rows is
@@ -56,7 +66,7 @@ __global__ void __launch_bounds__(kCopyThreads) mla_pages_copy_kernel(const Page
   int rows;
   if (!pages_entry(p, blockIdx.x, sp, dp, rows)) return;
   constexpr int64_t kPage = static_cast<int64_t>(kRowBytes) * MLA_PAGE_SIZE;
-  copy_vectors(p.src + sp * kPage, p.dst + dp * kPage, rows * (kRowBytes / 16));
+  copy_vectors<5>(p.src + sp * kPage, p.dst + dp * kPage, rows * (kRowBytes / 16));
 }
 
 __global__ void __launch_bounds__(kCopyThreads) mla_pages_copy_fp4_kernel(const PagesParams p) {
@@ -66,82 +76,135 @@ __global__ void __launch_bounds__(kCopyThreads) mla_pages_copy_fp4_kernel(const 
   const uint8_t* s = p.src + sp * MLA_FP4_PAGE_BYTES;
   uint8_t* d = p.dst + dp * MLA_FP4_PAGE_BYTES;
   if (rows == MLA_PAGE_SIZE) {
-    copy_vectors(s, d, MLA_FP4_PAGE_BYTES / 16);
+    copy_vectors<3>(s, d, MLA_FP4_PAGE_BYTES / 16);
     return;
   }
-  copy_vectors(s, d, rows * (kFp4RowCodes / 16));
-  copy_vectors(s + kFp4RopeOffset, d + kFp4RopeOffset, rows * (MLA_ROPE_DIM / 16));
+  copy_vectors<2>(s, d, rows * (kFp4RowCodes / 16));
+  copy_vectors<1>(s + kFp4RopeOffset, d + kFp4RopeOffset, rows * (MLA_ROPE_DIM / 16));
   for (int k = threadIdx.x; k < kFp4Blocks * MLA_PAGE_SIZE; k += kCopyThreads)
     if (k % MLA_PAGE_SIZE < rows) d[kFp4ScaleOffset + k] = s[kFp4ScaleOffset + k];
 }
 
-// Demotion: one CTA per entry, one warp per row at a time.  A row's latent
-// part is 32 16-byte vectors of 16 E4M3 values, one per lane: a block of the
-// 4-bit format is two lanes.
-__global__ void __launch_bounds__(kCopyThreads) mla_pages_demote_kernel(const PagesParams p) {
+// Demotion: one CTA per entry, one warp for each four rows, whose loads are in
+// flight together.  A row's latent part is 32 16-byte vectors of 16 E4M3
+// values, one per lane: a block of the 4-bit format is two lanes.  The scale
+// codes, which the page holds block by block, are turned around in shared
+// memory.
+#ifndef DLB
+#define DLB 5
+#endif
+#ifndef DLD
+#define DLD(p) (*(p))
+#endif
+__global__ void __launch_bounds__(kCopyThreads, DLB) mla_pages_demote_kernel(const PagesParams p) {
+  static_assert(kCopyThreads == 256, "eight warps of four rows");
+  __shared__ __align__(16) uint8_t scales[kFp4Blocks * MLA_PAGE_SIZE];
   int64_t sp, dp;
   int rows;
   if (!pages_entry(p, blockIdx.x, sp, dp, rows)) return;
   const uint8_t* s = p.src + sp * (MLA_PAGE_SIZE * MLA_HEAD_DIM);
   uint8_t* d = p.dst + dp * MLA_FP4_PAGE_BYTES;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int row = warp; row < rows; row += kCopyThreads / 32) {
-    const uint4* sv = reinterpret_cast<const uint4*>(s + row * MLA_HEAD_DIM);
-    const uint4 v = sv[lane];
-    uint4 r = make_uint4(0u, 0u, 0u, 0u);
-    if (lane < 4) r = sv[32 + lane];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float x[2][8];
-    uint32_t amax = 0;
+  const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * 4;
+  const int n = min(4, rows - row0);  // rows of this warp (none: <= 0)
+  if (n > 0) {
+    uint4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 a = unpack_e4m3x2(static_cast<uint16_t>(w[k] & 0xFFFFu));
-      const float2 b = unpack_e4m3x2(static_cast<uint16_t>(w[k] >> 16));
-      float* o = &x[k >> 1][4 * (k & 1)];
-      o[0] = a.x;
-      o[1] = a.y;
-      o[2] = b.x;
-      o[3] = b.y;
+    for (int r = 0; r < 4; ++r)
+      v[r] = DLD(reinterpret_cast<const uint4*>(s + (row0 + min(r, n - 1)) * MLA_HEAD_DIM) + lane);
+    const int rr = (lane >> 2) & 3;  // the rope parts: four lanes a row, half the warp
+    const bool rope = lane < 16 && rr < n;
+    uint4 rv = make_uint4(0u, 0u, 0u, 0u);
+    if (rope)
+      rv = reinterpret_cast<const uint4*>(s + (row0 + rr) * MLA_HEAD_DIM + MLA_LATENT_DIM)[lane & 3];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) amax = max(amax, __float_as_uint(o[m]) & 0x7FFFFFFFu);
+    for (int r = 0; r < 4; ++r) {
+      if (r >= n) break;
+      const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+      float x[2][8];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 a = unpack_e4m3x2(static_cast<uint16_t>(w[k] & 0xFFFFu));
+        const float2 b = unpack_e4m3x2(static_cast<uint16_t>(w[k] >> 16));
+        float* o = &x[k >> 1][4 * (k & 1)];
+        o[0] = a.x;
+        o[1] = a.y;
+        o[2] = b.x;
+        o[3] = b.y;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) amax = max(amax, __float_as_uint(o[m]) & 0x7FFFFFFFu);
+      }
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      const int e = fp4_scale_code(amax);
+      const float inv = fp4_inv_scale(e);
+      uint2 c = make_uint2(0u, 0u);
+      if (e != kFp4NanScale) c = make_uint2(fp4_encode8(x[0], inv), fp4_encode8(x[1], inv));
+      reinterpret_cast<uint2*>(d + (row0 + r) * kFp4RowCodes)[lane] = c;
+      if ((lane & 1) == 0)
+        scales[(lane >> 1) * MLA_PAGE_SIZE + row0 + r] = static_cast<uint8_t>(e);
     }
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    const int e = fp4_scale_code(amax);
-    const float inv = fp4_inv_scale(e);
-    uint2 c = make_uint2(0u, 0u);
-    if (e != kFp4NanScale) c = make_uint2(fp4_encode8(x[0], inv), fp4_encode8(x[1], inv));
-    reinterpret_cast<uint2*>(d + row * kFp4RowCodes)[lane] = c;
-    if ((lane & 1) == 0)
-      d[kFp4ScaleOffset + (lane >> 1) * MLA_PAGE_SIZE + row] = static_cast<uint8_t>(e);
-    if (lane < 4)
-      reinterpret_cast<uint4*>(d + kFp4RopeOffset + row * MLA_ROPE_DIM)[lane] = r;
+    if (rope)
+      reinterpret_cast<uint4*>(d + kFp4RopeOffset + (row0 + rr) * MLA_ROPE_DIM)[lane & 3] = rv;
+  }
+  __syncthreads();
+  if (rows == MLA_PAGE_SIZE) {
+    if (threadIdx.x < sizeof(scales) / 16)
+      reinterpret_cast<uint4*>(d + kFp4ScaleOffset)[threadIdx.x] =
+          reinterpret_cast<const uint4*>(scales)[threadIdx.x];
+  } else {
+    for (int k = threadIdx.x; k < kFp4Blocks * MLA_PAGE_SIZE; k += kCopyThreads)
+      if (k % MLA_PAGE_SIZE < rows) d[kFp4ScaleOffset + k] = scales[k];
   }
 }
 
-// Promotion: one CTA per entry.  A 16-byte vector of codes is one block: 32
-// E4M3 codes out.
+// Promotion: one CTA per entry.  A 16-byte vector of codes is one block, 32
+// E4M3 codes out; neighbouring lanes swap halves so that each store of a warp
+// covers whole sectors.
 __global__ void __launch_bounds__(kCopyThreads) mla_pages_promote_kernel(const PagesParams p) {
-  __shared__ uint2 table[16];
-  if (threadIdx.x < 16) table[threadIdx.x] = fp4_table_entry(threadIdx.x);
-  __syncthreads();
+  static_assert(kFp4Blocks * MLA_PAGE_SIZE == 2 * kCopyThreads, "two blocks a thread");
   int64_t sp, dp;
   int rows;
   if (!pages_entry(p, blockIdx.x, sp, dp, rows)) return;
   const uint8_t* s = p.src + sp * MLA_FP4_PAGE_BYTES;
   uint8_t* d = p.dst + dp * (MLA_PAGE_SIZE * MLA_HEAD_DIM);
-  for (int k = threadIdx.x; k < rows * kFp4Blocks; k += kCopyThreads) {
-    const int row = k / kFp4Blocks, blk = k % kFp4Blocks;
-    const uint4 v = reinterpret_cast<const uint4*>(s)[k];
-    const uint2 t = table[s[kFp4ScaleOffset + blk * MLA_PAGE_SIZE + row] & 15];
-    const uint2 a = fp4_expand8(v.x, t), b = fp4_expand8(v.y, t);
-    const uint2 c = fp4_expand8(v.z, t), e = fp4_expand8(v.w, t);
-    uint4* o = reinterpret_cast<uint4*>(d + row * MLA_HEAD_DIM) + 2 * blk;
-    o[0] = make_uint4(a.x, a.y, b.x, b.y);
-    o[1] = make_uint4(c.x, c.y, e.x, e.y);
+  const int blk = threadIdx.x % kFp4Blocks, row0 = threadIdx.x / kFp4Blocks;
+  constexpr int kStep = kCopyThreads / kFp4Blocks;  // rows between a thread's two blocks
+  uint4 v[2];
+  uint32_t e[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {  // (rows past the count: inside the page, not stored)
+    const int row = row0 + u * kStep;
+    v[u] = DLD(reinterpret_cast<const uint4*>(s + row * kFp4RowCodes) + blk);
+    e[u] = s[kFp4ScaleOffset + blk * MLA_PAGE_SIZE + row] & 15u;
   }
-  for (int k = threadIdx.x; k < rows * 4; k += kCopyThreads)
-    reinterpret_cast<uint4*>(d + (k / 4) * MLA_HEAD_DIM + MLA_LATENT_DIM)[k % 4] =
-        reinterpret_cast<const uint4*>(s + kFp4RopeOffset)[k];
+  const int rrow = threadIdx.x / 4;  // the rope part: half the threads
+  const bool rope = rrow < rows;
+  uint4 rv = make_uint4(0u, 0u, 0u, 0u);
+  if (rope) rv = reinterpret_cast<const uint4*>(s + kFp4RopeOffset)[threadIdx.x];
+  const bool odd = (threadIdx.x & 1) != 0;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int row = row0 + u * kStep;
+    const uint2 t = fp4_scale_table(e[u]);
+    const uint2 a = fp4_expand8(v[u].x, t), b = fp4_expand8(v[u].y, t);
+    const uint2 c = fp4_expand8(v[u].z, t), f = fp4_expand8(v[u].w, t);
+    uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, f.x, f.y);
+    // The even lane keeps its first half and takes the odd lane's first half;
+    // the odd lane takes the even lane's second half and keeps its second.
+    const uint4 send = odd ? lo : hi;
+    uint4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, send.x, 1);
+    got.y = __shfl_xor_sync(0xffffffffu, send.y, 1);
+    got.z = __shfl_xor_sync(0xffffffffu, send.z, 1);
+    got.w = __shfl_xor_sync(0xffffffffu, send.w, 1);
+    if (row < rows) {
+      uint4* o = reinterpret_cast<uint4*>(d + row * MLA_HEAD_DIM) + 2 * (blk & ~1) + (odd ? 1 : 0);
+      o[0] = odd ? got : lo;
+      o[2] = odd ? hi : got;
+    }
+  }
+  if (rope)
+    reinterpret_cast<uint4*>(d + rrow * MLA_HEAD_DIM + MLA_LATENT_DIM)[threadIdx.x & 3] = rv;
 }
 
 __global__ void __launch_bounds__(kCopyThreads)

@@ -300,3 +300,19 @@ def test_side_stream_and_graph_replay():
     graph.replay()
     want, qwant, _ = _run(j, "fp4")
     assert torch.equal(pool, want) and torch.equal(q_out, qwant)
+
+
+def test_binding_refuses_what_an_address_cannot_carry():
+    i = _inputs(1, 4, 2, seed=17)
+    d = {k: (v.cuda() if torch.is_tensor(v) else v) for k, v in i.items()}
+    pool, q_out = _pool("fp8", i["pages"]), torch.zeros(4, 2, 576, dtype=torch.uint8, device="cuda")
+    good = dict(positions=d["pos"], cos_sin=d["cos_sin"], kv_rows=d["rows"], req_idx=d["req"], page_table=d["table"],
+                max_pages_per_req=d["table"].shape[1], batch=1, kv_pages=pool, num_pages=i["pages"], q_rows=d["q"], num_heads=2, q_out=q_out)
+    for n, bad in ((5, {}), (4, dict(num_heads=3)), (4, dict(kv_rows=d["rows"][:1].expand(4, 576))), (4, dict(kv_rows=d["rows"].float())),
+                   (4, dict(q_rows=d["q"][:, :1].expand(4, 2, 576))), (4, dict(q_rows=d["q"].transpose(1, 2).contiguous().transpose(1, 2))),
+                   (4, dict(positions=d["pos"].long())), (4, dict(page_table=d["table"].cpu())), (4, dict(q_out=q_out[:2])),
+                   (4, dict(cos_sin=d["cos_sin"].double())), (4, dict(norm_weight=d["weight"].bfloat16()))):
+        with pytest.raises(ValueError):
+            mla.mla_prologue(n, **dict(good, **bad))
+    mla.mla_prologue(4, **good)
+    torch.cuda.synchronize()
