@@ -53,6 +53,14 @@ __device__ __forceinline__ int fp4_scale_code(uint32_t amax_bits) {
 // 2^(8 - e), exactly.
 __device__ __forceinline__ float fp4_inv_scale(int e) { return __int_as_float((135 - e) << 23); }
 
+// Signs of a word of plain E2M1 nibbles (bits 4j + 3) to the format's places.
+__device__ __forceinline__ uint32_t fp4_place_signs(uint32_t w) {
+  const uint32_t up = w << 4;  // even nibbles' signs at their bytes' top bits
+  const uint32_t lo = __byte_perm(up, w, 0x5140) & 0x80808080u;         // values 0-3
+  const uint32_t hi = (__byte_perm(up, w, 0x7362) & 0x80808080u) >> 4;  // values 4-7
+  return (w & 0x77777777u) | lo | hi;
+}
+
 // Eight values times 2^(8 - e) as one word of the format: nearest E2M1, ties
 // to even, saturating at 6.
 __device__ __forceinline__ uint32_t fp4_encode8(const float (&x)[8], float inv) {
@@ -66,28 +74,28 @@ __device__ __forceinline__ uint32_t fp4_encode8(const float (&x)[8], float inv) 
       : "=r"(w)
       : "f"(x[0] * inv), "f"(x[1] * inv), "f"(x[2] * inv), "f"(x[3] * inv), "f"(x[4] * inv),
         "f"(x[5] * inv), "f"(x[6] * inv), "f"(x[7] * inv));
-  // Signs from their own nibbles (bits 4j + 3) to the format's places.
-  const uint32_t up = w << 4;  // even nibbles' signs at their bytes' top bits
-  const uint32_t lo = __byte_perm(up, w, 0x5140) & 0x80808080u;         // values 0-3
-  const uint32_t hi = (__byte_perm(up, w, 0x7362) & 0x80808080u) >> 4;  // values 4-7
-  return (w & 0x77777777u) | lo | hi;
+  return fp4_place_signs(w);
 }
 
-// The eight E4M3 codes of scale code e's magnitudes, as two words (e = 15: NaN).
-__device__ __forceinline__ uint2 fp4_table_entry(int e) {
-  if (e == kFp4NanScale) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  const float s = __int_as_float((119 + e) << 23);  // 2^(e - 8)
-  uint16_t a, b, c, d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(0.5f * s), "f"(0.0f));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(1.5f * s), "f"(s));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(3.0f * s), "f"(2.0f * s));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(6.0f * s), "f"(4.0f * s));
-  return make_uint2(a | (static_cast<uint32_t>(b) << 16), c | (static_cast<uint32_t>(d) << 16));
+// The same from four pairs of halves already multiplied by 2^(8 - e) (low half:
+// the earlier value).
+__device__ __forceinline__ uint32_t fp4_encode8_halves(uint32_t x01, uint32_t x23, uint32_t x45,
+                                                       uint32_t x67) {
+  uint32_t w;
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+      " cvt.rn.satfinite.e2m1x2.f16x2 b0, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f16x2 b1, %2;\n"
+      " cvt.rn.satfinite.e2m1x2.f16x2 b2, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f16x2 b3, %4;\n"
+      " mov.b32 %0, {b0, b1, b2, b3};\n}"
+      : "=r"(w)
+      : "r"(x01), "r"(x23), "r"(x45), "r"(x67));
+  return fp4_place_signs(w);
 }
 
-// The same table by arithmetic, for kernels without room for one in shared
-// memory: from e = 3 to 14 all codes are normal E4M3 numbers, e - 2 exponents
-// above e = 2's pattern, so each word is one multiply-add.
+// The E4M3 codes of scale code e's eight magnitudes, as two words: from e = 3 to
+// 14 all are normal numbers, e - 2 exponents above e = 2's pattern, so each word
+// is one multiply-add.
 __device__ __forceinline__ uint2 fp4_scale_table_normal(uint32_t e) {
   return make_uint2(0x0C080000u - 2u * 0x08080800u + e * 0x08080800u,
                     0x1C181410u - 2u * 0x08080808u + e * 0x08080808u);

@@ -85,18 +85,18 @@ __global__ void __launch_bounds__(kCopyThreads) mla_pages_copy_fp4_kernel(const 
     if (k % MLA_PAGE_SIZE < rows) d[kFp4ScaleOffset + k] = s[kFp4ScaleOffset + k];
 }
 
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint16_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
+  return *reinterpret_cast<__half2*>(&h);
+}
+
 // Demotion: one CTA per entry, one warp for each four rows, whose loads are in
 // flight together.  A row's latent part is 32 16-byte vectors of 16 E4M3
 // values, one per lane: a block of the 4-bit format is two lanes.  The scale
 // codes, which the page holds block by block, are turned around in shared
 // memory.
-#ifndef DLB
-#define DLB 5
-#endif
-#ifndef DLD
-#define DLD(p) (*(p))
-#endif
-__global__ void __launch_bounds__(kCopyThreads, DLB) mla_pages_demote_kernel(const PagesParams p) {
+__global__ void __launch_bounds__(kCopyThreads) mla_pages_demote_kernel(const PagesParams p) {
   static_assert(kCopyThreads == 256, "eight warps of four rows");
   __shared__ __align__(16) uint8_t scales[kFp4Blocks * MLA_PAGE_SIZE];
   int64_t sp, dp;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kCopyThreads, DLB) mla_pages_demote_kernel(con
     uint4 v[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      v[r] = DLD(reinterpret_cast<const uint4*>(s + (row0 + min(r, n - 1)) * MLA_HEAD_DIM) + lane);
+      v[r] = reinterpret_cast<const uint4*>(s + (row0 + min(r, n - 1)) * MLA_HEAD_DIM)[lane];
     const int rr = (lane >> 2) & 3;  // the rope parts: four lanes a row, half the warp
     const bool rope = lane < 16 && rr < n;
     uint4 rv = make_uint4(0u, 0u, 0u, 0u);
@@ -120,25 +120,30 @@ __global__ void __launch_bounds__(kCopyThreads, DLB) mla_pages_demote_kernel(con
     for (int r = 0; r < 4; ++r) {
       if (r >= n) break;
       const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
-      float x[2][8];
-      uint32_t amax = 0;
+      __half2 x[8];
+      __half2 m = __half2half2(__ushort_as_half(0));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 a = unpack_e4m3x2(static_cast<uint16_t>(w[k] & 0xFFFFu));
-        const float2 b = unpack_e4m3x2(static_cast<uint16_t>(w[k] >> 16));
-        float* o = &x[k >> 1][4 * (k & 1)];
-        o[0] = a.x;
-        o[1] = a.y;
-        o[2] = b.x;
-        o[3] = b.y;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) amax = max(amax, __float_as_uint(o[m]) & 0x7FFFFFFFu);
+      for (int k = 0; k < 8; ++k) {
+        x[k] = e4m3x2_to_half2(static_cast<uint16_t>(k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu));
+        m = __hmax2_nan(m, __habs2(x[k]));
       }
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      const int e = fp4_scale_code(amax);
-      const float inv = fp4_inv_scale(e);
+      m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      const float amax = __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+      const int e = fp4_scale_code(__float_as_uint(amax) & 0x7FFFFFFFu);
       uint2 c = make_uint2(0u, 0u);
-      if (e != kFp4NanScale) c = make_uint2(fp4_encode8(x[0], inv), fp4_encode8(x[1], inv));
+      if (e != kFp4NanScale) {
+        // Exact in halves: an E4M3 value is at least 2^-9, and 2^(8 - e) at
+        // least 2^-6; the products are at most 448.
+        const __half2 inv = __float2half2_rn(fp4_inv_scale(e));
+        uint32_t u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const __half2 q = __hmul2(x[k], inv);
+          u[k] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        c = make_uint2(fp4_encode8_halves(u[0], u[1], u[2], u[3]),
+                       fp4_encode8_halves(u[4], u[5], u[6], u[7]));
+      }
       reinterpret_cast<uint2*>(d + (row0 + r) * kFp4RowCodes)[lane] = c;
       if ((lane & 1) == 0)
         scales[(lane >> 1) * MLA_PAGE_SIZE + row0 + r] = static_cast<uint8_t>(e);
@@ -157,54 +162,42 @@ __global__ void __launch_bounds__(kCopyThreads, DLB) mla_pages_demote_kernel(con
   }
 }
 
-// Promotion: one CTA per entry.  A 16-byte vector of codes is one block, 32
-// E4M3 codes out; neighbouring lanes swap halves so that each store of a warp
-// covers whole sectors.
+// Promotion: one CTA per entry, one warp for each four rows.  A lane expands 16
+// values (8 bytes of codes, half a block) a row, so that a warp's load covers a
+// row's 256 bytes and its store 512; its scale codes of the four rows are one
+// aligned word.
 __global__ void __launch_bounds__(kCopyThreads) mla_pages_promote_kernel(const PagesParams p) {
-  static_assert(kFp4Blocks * MLA_PAGE_SIZE == 2 * kCopyThreads, "two blocks a thread");
+  static_assert(kCopyThreads == 256, "eight warps of four rows");
   int64_t sp, dp;
   int rows;
   if (!pages_entry(p, blockIdx.x, sp, dp, rows)) return;
   const uint8_t* s = p.src + sp * MLA_FP4_PAGE_BYTES;
   uint8_t* d = p.dst + dp * (MLA_PAGE_SIZE * MLA_HEAD_DIM);
-  const int blk = threadIdx.x % kFp4Blocks, row0 = threadIdx.x / kFp4Blocks;
-  constexpr int kStep = kCopyThreads / kFp4Blocks;  // rows between a thread's two blocks
-  uint4 v[2];
-  uint32_t e[2];
+  const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * 4;
+  const int n = min(4, rows - row0);  // rows of this warp
+  if (n <= 0) return;
+  // (Rows past the count are loaded, inside the page, and not stored.)
+  uint2 v[4];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {  // (rows past the count: inside the page, not stored)
-    const int row = row0 + u * kStep;
-    v[u] = DLD(reinterpret_cast<const uint4*>(s + row * kFp4RowCodes) + blk);
-    e[u] = s[kFp4ScaleOffset + blk * MLA_PAGE_SIZE + row] & 15u;
-  }
-  const int rrow = threadIdx.x / 4;  // the rope part: half the threads
-  const bool rope = rrow < rows;
+  for (int r = 0; r < 4; ++r)
+    v[r] = reinterpret_cast<const uint2*>(s + (row0 + r) * kFp4RowCodes)[lane];
+  const uint32_t sc = *reinterpret_cast<const uint32_t*>(s + kFp4ScaleOffset +
+                                                         (lane >> 1) * MLA_PAGE_SIZE + row0);
+  const int rr = (lane >> 2) & 3;  // the rope parts: four lanes a row, half the warp
+  const bool rope = lane < 16 && rr < n;
   uint4 rv = make_uint4(0u, 0u, 0u, 0u);
-  if (rope) rv = reinterpret_cast<const uint4*>(s + kFp4RopeOffset)[threadIdx.x];
-  const bool odd = (threadIdx.x & 1) != 0;
+  if (rope)
+    rv = reinterpret_cast<const uint4*>(s + kFp4RopeOffset + (row0 + rr) * MLA_ROPE_DIM)[lane & 3];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int row = row0 + u * kStep;
-    const uint2 t = fp4_scale_table(e[u]);
-    const uint2 a = fp4_expand8(v[u].x, t), b = fp4_expand8(v[u].y, t);
-    const uint2 c = fp4_expand8(v[u].z, t), f = fp4_expand8(v[u].w, t);
-    uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, f.x, f.y);
-    // The even lane keeps its first half and takes the odd lane's first half;
-    // the odd lane takes the even lane's second half and keeps its second.
-    const uint4 send = odd ? lo : hi;
-    uint4 got;
-    got.x = __shfl_xor_sync(0xffffffffu, send.x, 1);
-    got.y = __shfl_xor_sync(0xffffffffu, send.y, 1);
-    got.z = __shfl_xor_sync(0xffffffffu, send.z, 1);
-    got.w = __shfl_xor_sync(0xffffffffu, send.w, 1);
-    if (row < rows) {
-      uint4* o = reinterpret_cast<uint4*>(d + row * MLA_HEAD_DIM) + 2 * (blk & ~1) + (odd ? 1 : 0);
-      o[0] = odd ? got : lo;
-      o[2] = odd ? hi : got;
-    }
+  for (int r = 0; r < 4; ++r) {
+    if (r >= n) break;
+    const uint2 t = fp4_scale_table((sc >> (8 * r)) & 15u);
+    const uint2 a = fp4_expand8(v[r].x, t), b = fp4_expand8(v[r].y, t);
+    reinterpret_cast<uint4*>(d + (row0 + r) * MLA_HEAD_DIM)[lane] =
+        make_uint4(a.x, a.y, b.x, b.y);
   }
   if (rope)
-    reinterpret_cast<uint4*>(d + rrow * MLA_HEAD_DIM + MLA_LATENT_DIM)[threadIdx.x & 3] = rv;
+    reinterpret_cast<uint4*>(d + (row0 + rr) * MLA_HEAD_DIM + MLA_LATENT_DIM)[lane & 3] = rv;
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
