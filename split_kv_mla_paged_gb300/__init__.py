@@ -57,6 +57,7 @@ EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_workspace_size", "mla_decode_
 
 HEAD_DIM = 576
 LATENT_DIM = 512
+ROPE_DIM = 64
 PAGE_SIZE = 32
 TILE_TOKENS = 128
 MAX_SPLITS = 256
@@ -432,11 +433,11 @@ def _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sin
         0 if cta_items is None else int(cta_items.numel()), 0, int(phases)))
 
 
-def _fp4_pages(pool) -> int:
+def _fp4_pages(pool, num_pages: int) -> int:
     import torch
-    if pool.dim() != 2 or pool.shape[1] != FP4_PAGE_BYTES:
+    if pool.dtype is not torch.uint8 or pool.dim() != 2 or pool.shape[1] != FP4_PAGE_BYTES:
         raise ValueError(f"a 4-bit page pool is uint8 [pages, {FP4_PAGE_BYTES}]")
-    return _device_tensor(pool, "kv_pages_fp4", torch.uint8)
+    return _device_pool(pool, "kv_pages_fp4", num_pages, CACHE_FP4)
 
 
 def mla_decode_fp4(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req, kv_lens, splits,
@@ -450,7 +451,7 @@ def mla_decode_fp4(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req
     mla_decode_ex (no persistent CTAs)."""
     opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
                         query_lens, kv_bounds, cta_items, phases)
-    _call_on(q_fp8, load_library().mla_decode_fp4, _ptr(q_fp8), _fp4_pages(kv_pages_fp4),
+    _call_on(q_fp8, load_library().mla_decode_fp4, _ptr(q_fp8), _fp4_pages(kv_pages_fp4, num_pages),
              num_pages, _ptr(page_table), max_pages_per_req, _ptr(kv_lens), _ptr(splits),
              _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads, 1 if causal else 0,
              q_scale, kv_scale, softmax_scale, _ptr(workspace), workspace_bytes, _ptr(out_bf16),
@@ -468,7 +469,7 @@ def mla_decode_fp4_sparse(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_
     cache (plan with the compact lengths 32 * topk)."""
     opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
                         query_lens, kv_bounds, cta_items, phases)
-    _call_on(q_fp8, load_library().mla_decode_fp4_sparse, _ptr(q_fp8), _fp4_pages(kv_pages_fp4),
+    _call_on(q_fp8, load_library().mla_decode_fp4_sparse, _ptr(q_fp8), _fp4_pages(kv_pages_fp4, num_pages),
              num_pages, _ptr(page_table), max_pages_per_req, _ptr(kv_lens), _ptr(block_idx), topk,
              _ptr(splits), _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads,
              1 if causal else 0, q_scale, kv_scale, softmax_scale, _ptr(workspace),
@@ -542,9 +543,9 @@ def mla_kv_append(rows_bf16, n_tokens: int, req_idx, positions, page_table,
         _ptr(status), _stream_handle(stream)))
 
 
-def _device_tensor(t, name: str, dtype=None, contiguous: bool = True):
+def _device_tensor(t, name: str, dtype=None, least: int = 0, contiguous: bool = True):
     """Address of a CUDA tensor (None for None), after the checks that a raw
-    address cannot carry: its device, type and contiguity."""
+    address cannot carry: its device, type, contiguity and number of elements."""
     if t is None:
         return None
     if not t.is_cuda:
@@ -553,7 +554,24 @@ def _device_tensor(t, name: str, dtype=None, contiguous: bool = True):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    if t.numel() < least:
+        raise ValueError(f"{name} has {t.numel()} elements, this call needs {least}")
     return t.data_ptr()
+
+
+_PAGE_BYTES = {CACHE_FP8: PAGE_SIZE * HEAD_DIM, CACHE_BF16: 2 * PAGE_SIZE * HEAD_DIM,
+               CACHE_FP4: FP4_PAGE_BYTES}
+
+
+def _device_pool(pool, name: str, pages: int, kind: int):
+    """Address of a page pool that holds at least `pages` pages of its kind (an
+    unknown kind is left to the library to refuse)."""
+    if pool is None:
+        return None
+    ptr = _device_tensor(pool, name)
+    if pool.numel() * pool.element_size() < pages * _PAGE_BYTES.get(kind, 0):
+        raise ValueError(f"{name} is smaller than {pages} pages of its kind")
+    return ptr
 
 
 def _call_on(tensor, fn, *args, stream=None) -> None:
@@ -601,19 +619,19 @@ def mla_prologue(n_tokens: int, *, positions=None, cos_sin=None, rope_positions=
     rows = table = pages = weight = None
     row_stride = token_stride = head_stride = 0
     if kv_rows is not None:
-        rows = _device_tensor(kv_rows, "kv_rows", bf16, contiguous=False)
+        rows = _device_tensor(kv_rows, "kv_rows", bf16, 0, False)
         if kv_rows.dim() != 2 or kv_rows.shape[1] != HEAD_DIM or kv_rows.stride(1) != 1:
             raise ValueError("kv_rows must be [n_tokens, 576] with dense rows")
         if kv_rows.shape[0] < n_tokens:
             raise ValueError("kv_rows has fewer than n_tokens rows")
         if kv_rows.shape[0] > 1:
             row_stride = _row_stride(kv_rows, 0, "kv_rows")
-        weight = _device_tensor(norm_weight, "norm_weight", f32)
-        table = _device_tensor(page_table, "page_table", i32)
-        pages = _device_tensor(kv_pages, "kv_pages")
+        weight = _device_tensor(norm_weight, "norm_weight", f32, LATENT_DIM)
+        table = _device_tensor(page_table, "page_table", i32, batch * max_pages_per_req)
+        pages = _device_pool(kv_pages, "kv_pages", num_pages, cache_kind)
     queries = out = None
     if q_rows is not None:
-        queries = _device_tensor(q_rows, "q_rows", bf16, contiguous=False)
+        queries = _device_tensor(q_rows, "q_rows", bf16, 0, False)
         if q_rows.dim() != 3 or q_rows.shape[2] != HEAD_DIM or q_rows.stride(2) != 1:
             raise ValueError("q_rows must be [n_tokens, num_heads, 576] with dense rows")
         if q_rows.shape[0] < n_tokens or q_rows.shape[1] < num_heads:
@@ -622,18 +640,19 @@ def mla_prologue(n_tokens: int, *, positions=None, cos_sin=None, rope_positions=
             token_stride = _row_stride(q_rows, 0, "q_rows")
         if q_rows.shape[1] > 1:
             head_stride = _row_stride(q_rows, 1, "q_rows")
-        out = _device_tensor(q_out, "q_out")
-        if out is not None and q_out.numel() < n_tokens * num_heads * HEAD_DIM:
-            raise ValueError("q_out is smaller than [n_tokens, num_heads, 576]")
+        out = _device_tensor(q_out, "q_out", None, n_tokens * num_heads * HEAD_DIM)
+        if out is not None and q_out.element_size() != (2 if q_kind == CACHE_BF16 else 1):
+            raise ValueError("q_out must have the element size of q_kind")
     if cos_sin is None:
         rope_rows = 0
     elif rope_rows is None:
         rope_rows = cos_sin.shape[0]
-    a = PrologueArgs(n_tokens, _device_tensor(positions, "positions", i32),
-                     _device_tensor(cos_sin, "cos_sin", f32),
-                     _device_tensor(rope_positions, "rope_positions", i32), rope_rows,
+    a = PrologueArgs(n_tokens, _device_tensor(positions, "positions", i32, n_tokens),
+                     _device_tensor(cos_sin, "cos_sin", f32, rope_rows * ROPE_DIM),
+                     _device_tensor(rope_positions, "rope_positions", i32, n_tokens), rope_rows,
                      1 if rope_halves else 0, rows, row_stride, weight, norm_eps,
-                     max_pages_per_req, _device_tensor(req_idx, "req_idx", i32), table, pages,
+                     max_pages_per_req, _device_tensor(req_idx, "req_idx", i32, n_tokens), table,
+                     pages,
                      num_pages, batch, cache_kind, kv_scale, q_scale, queries, token_stride,
                      head_stride, out, num_heads, q_kind, _device_tensor(status, "status", i32))
     _call_on(where, load_library().mla_prologue, ctypes.byref(a), stream=stream)
@@ -647,11 +666,12 @@ def mla_pages_copy(src_pool, src_pages: int, src_kind: int, dst_pool, dst_pages:
     tensors."""
     import torch
     i32 = torch.int32
-    _call_on(dst_pool, load_library().mla_pages_copy, _device_tensor(src_pool, "src_pool"),
-             int(src_pages), int(src_kind), _device_tensor(dst_pool, "dst_pool"), int(dst_pages),
-             int(dst_kind), _device_tensor(src_ids, "src_ids", i32),
-             _device_tensor(dst_ids, "dst_ids", i32), _device_tensor(rows, "rows", i32), int(n),
-             _device_tensor(status, "status", i32), stream=stream)
+    _call_on(dst_pool, load_library().mla_pages_copy,
+             _device_pool(src_pool, "src_pool", src_pages, src_kind), src_pages, src_kind,
+             _device_pool(dst_pool, "dst_pool", dst_pages, dst_kind), dst_pages, dst_kind,
+             _device_tensor(src_ids, "src_ids", i32, n), _device_tensor(dst_ids, "dst_ids", i32, n),
+             _device_tensor(rows, "rows", i32, n), n, _device_tensor(status, "status", i32),
+             stream=stream)
 
 
 def mla_pages_remap(page_table, n_entries: int, page_map, num_pages: int, status=None,
@@ -660,8 +680,8 @@ def mla_pages_remap(page_table, n_entries: int, page_map, num_pages: int, status
     import torch
     i32 = torch.int32
     _call_on(page_table, load_library().mla_pages_remap,
-             _device_tensor(page_table, "page_table", i32), int(n_entries),
-             _device_tensor(page_map, "page_map", i32), int(num_pages),
+             _device_tensor(page_table, "page_table", i32, n_entries), n_entries,
+             _device_tensor(page_map, "page_map", i32, num_pages), num_pages,
              _device_tensor(status, "status", i32), stream=stream)
 
 

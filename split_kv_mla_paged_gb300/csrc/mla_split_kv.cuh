@@ -45,7 +45,8 @@ struct Cfg {
   static_assert(kTmemUsed <= 512, "TMEM");
   // Softmax warpgroups: two (each owning half the rows) from 32 rows up,
   // three (32 rows each) for the 96-row configuration.
-  // (4-bit cache: two for 16 rows as well, whose tiles come 1.7 times as fast.)
+  // (4-bit cache: two for 16 rows as well, whose tiles come 1.7 times as fast:
+  // one warpgroup's chain from S^T to P^T alone took 2,800 cycles a tile.)
   static constexpr int SWG = kWide ? 3 : (NR >= 32 || kFp4) ? 2 : 1;
   static constexpr int NRH = NR / SWG;
   // Each softmax thread keeps its own row sums across tiles, and a warpgroup's
@@ -80,7 +81,10 @@ struct Cfg {
   static constexpr int kRegsHigh = !kFp4 ? 152 : NR == 16 ? 72 : 128;
   static constexpr int kRegsExpand = NR == 16 ? 96 : kWide ? 64 : 88;
   static_assert(!kWide || kFp4 || 32 * kSoftmaxWarp0 + 128 * SWG == 512, "register split");
-  // 4-bit cache: expander warps after the softmax warps.
+  // 4-bit cache: expander warps after the softmax warps.  16 rows: 12 of them
+  // (8 with 128 registers each: B1 1M 101.5 -> 102.2 us, B16 128K 188.9 ->
+  // 192.7 us; 16 with 80: 12 % slower); 96 rows: 4 (8 with 56 and the softmax
+  // at 112: H12 q8 B16 128K 449.8 -> 457.3 us).
   static constexpr int kExpandWarps = !kFp4 ? 0 : NR == 16 ? 12 : kWide ? 4 : 8;
   static constexpr int kExpandWarp0 = kSoftmaxWarp0 + 4 * SWG;
   static constexpr int kThreads = 32 * (kExpandWarp0 + kExpandWarps);
@@ -553,7 +557,9 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         int window = load_window(0, window_nv);
         int window_next = load_window(1, window_next_nv);
         // 4-bit cache: pages go to L2 kPrefetch tiles ahead, so that the
-        // expanders' loads, of which registers hold one tile, find them there.
+        // expanders' loads, of which registers hold one tile, find them there
+        // (16 rows, B1 1M: 111.6 us without, 109.4 with 3, 110.7 with 5 tiles; H12
+        // q8 B16 128K 519 -> 505 us).
         constexpr int kPrefetch = 3;
         auto prefetch_tile = [&](int j, int i) {
           if constexpr (kFp4) {
@@ -971,9 +977,10 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       set_registers<C::kRegsLaunch, C::kRegsExpand>();
       // ================= expanders (4-bit cache) =================
       if constexpr (C::kBlockStages) {
-        // They fill the latent blocks of each stage, a page of one block (128
-        // dims of 32 tokens, a "chunk") at a time in the order the QK warp
-        // takes them: each lane loads 4 16-byte blocks of codes and their
+        // 96 rows, whose stages are released block by block: they fill the latent
+        // blocks of each stage, a page of one block (128 dims of 32 tokens, a
+        // "chunk") at a time in the order the QK warp takes them (against pairs
+        // of pages, which need 16 registers more: H12 q8 B16 128K 505 -> 450 us): each lane loads 4 16-byte blocks of codes and their
         // scales, expands them to E4M3 codes in registers and stores them where
         // TMA's 128-byte swizzle would have put an E4M3 cache's bytes.
         //
@@ -1096,13 +1103,18 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           if (lane == 0) mbar_arrive(full_blk(st, d));
         }
       } else {
-        // They fill the four latent blocks of each stage: 16 tokens (half a
-        // page, a "chunk") at a time, each lane loads one 16-byte block of codes
-        // of 8 of them and those blocks' scales, expands them to E4M3 codes in
-        // registers and stores them where TMA's 128-byte swizzle would have put
-        // an E4M3 cache's bytes.  Going through registers instead of a staging buffer saves
-        // a write and a read of shared memory, whose bandwidth the two MMAs'
-        // operand reads already fill.
+        // Up to 48 rows: they fill the four latent blocks of each stage, 16 tokens
+        // (half a page, a "chunk") at a time.  Each lane loads one 16-byte block of
+        // codes of 8 of them and those blocks' scales, expands them to E4M3
+        // codes in registers and stores them where TMA's 128-byte swizzle would
+        // have put an E4M3 cache's bytes.  Going through registers instead of a
+        // staging buffer saves a write and a read of shared memory, whose
+        // pipe bounds the 16-row kernel: of the 3,780 cycles a tile took (under
+        // ncu) the MMAs' operands fill 1,288, the loads, stores and barriers of
+        // all warps 1,862, and their conflicts 402.  Tried and slower: blocks of
+        // 128 dims x 64 tokens handed to the QK warp one by one (101 -> 121 us
+        // at B1 1M: 64-byte pieces of rows), expanding 8-token chunks before the
+        // stage is free (109 us), the two shifts of fp4_expand8 as multiplies.
         //
         // Lane -> block (lane / 8) * 4 + lane % 4 (its latent block of the tile
         // is lane / 8), token 2 k + (lane / 4) % 2: a warp's load covers two

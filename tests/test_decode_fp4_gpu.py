@@ -2,12 +2,13 @@
 
 Every value of a 4-bit page times its block's scale is an E4M3 number, so the
 kernel's tensor-core operands are those of the E4M3 cache that the pages expand
-to: with the same plan and row groups its outputs equal mla_decode's, bit for
-bit from 17 to 48 rows.  Up to 16 rows only the row sums differ, which are added
+to: with the same plan its outputs equal mla_decode's, bit for bit from 17 rows
+on.  Up to 16 rows only the row sums differ, which are added
 in another order: at most 128 tiles of a split, one after the other, then a tree
 over 128 tokens, 136 roundings on either side, 2 * 136 * 2^-24 < 2^-15 relative
-(and as much, absolute, in the natural logarithm).  The oracle runs on that expanded cache (expanded by oracle.cache, not by
-the kernel under test), with the decode tests' tolerances.
+(and as much, absolute, in the natural logarithm).  The oracle runs on that
+expanded cache (expanded by oracle.cache, not by the kernel under test), with the
+decode tests' tolerances.
 """
 import numpy as np
 import pytest
@@ -17,7 +18,8 @@ import oracle
 import split_kv_mla_paged_gb300 as mla
 from oracle import cache
 from split_kv_mla_paged_gb300 import build as mla_build
-from synth import SOFTMAX_SCALE, decode_inputs
+from synth import SOFTMAX_SCALE
+from fp4_testutil import equal_outputs as _equal, fp4_case as _case, same_outputs as _same
 from mla_testutil import assert_parity
 
 pytestmark = pytest.mark.gpu
@@ -29,48 +31,11 @@ def _lib():
     mla.load_library()
 
 
-def _case(batch, heads, q_len, lens, seed, extra_pages=2):
-    """decode_inputs with its cache re-encoded in 4 bits: (inputs with the
-    expanded E4M3 cache, 4-bit pool).  Rows behind a sequence's end stay NaN in
-    the 4-bit pool (scale bytes 0xFF, rope 0x7F)."""
-    inp = decode_inputs(batch, heads, q_len, lens, seed, extra_pages=extra_pages)
-    host = inp.kv.numpy()
-    vals = cache.e4m3_values()[host].reshape(-1, 576)
-    rng = np.random.default_rng(seed)
-    spread = np.exp2(rng.integers(-9, 6, (vals.shape[0], 18)).repeat(32, 1) * (rng.random((vals.shape[0], 1)) < 0.1))
-    stale = np.isnan(vals).any(1)
-    vals = np.where(stale[:, None], np.nan, np.nan_to_num(vals) * spread)
-    codes, sc, rope = cache.fp4_encode_rows(vals)
-    sc[stale], codes[stale] = 255, 255
-    pool = np.zeros((host.shape[0], mla.FP4_PAGE_BYTES), np.uint8)
-    n = host.shape[0]
-    pool[:, :8192] = codes.reshape(n, 8192)
-    pool[:, 8192:8704] = sc.reshape(n, 32, 16).transpose(0, 2, 1).reshape(n, 512)
-    pool[:, 8704:] = rope.reshape(n, 2048)
-    inp.kv = torch.from_numpy(cache.e4m3_codes(cache.fp4_decode(pool)))
-    return inp, torch.from_numpy(pool)
-
-
 def _decode(inp, kv, causal, **kw):
     out = mla.decode(inp.q.cuda(), kv.cuda(), inp.page_table.cuda(), inp.kv_lens, num_heads=inp.num_heads, q_len=inp.q_len,
                      causal=causal, softmax_scale=SOFTMAX_SCALE, want_f32=True, **kw)
     torch.cuda.synchronize()
     return out
-
-
-def _same(a, b):
-    for x, y in zip(a, b):
-        assert torch.equal(x, y)
-
-
-def _equal(a, b, rows):
-    """Outputs (bf16, lse, fp32) of the 4-bit and the E4M3 decode of `rows` rows a request."""
-    if rows > 16:
-        return _same(a, b)
-    (o, l, f), (ob, lb, fb) = a, b
-    assert ((f - fb).abs() <= 2.0 ** -15 * fb.abs()).all()
-    assert ((l - lb).abs() <= 2.0 ** -15).all()
-    assert ((o.float() - ob.float()).abs() <= 2.0 ** -7 * ob.float().abs()).all()  # one BF16 step
 
 
 SHAPES = [
@@ -193,7 +158,7 @@ def test_bad_page_id_and_bad_plan_are_reported():
     assert e.value.status == mla.MLA_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("q_len", [1, 4])
+@pytest.mark.parametrize("q_len", [1, 2, 4, 8])  # 16, 32, 48 and 96-row CTAs
 @pytest.mark.parametrize("role", range(6))
 def test_expired_waits_end_the_call_with_a_status(role, q_len):
     # The hook makes one wait read as expired without any stall; the kernel

@@ -311,7 +311,10 @@ def test_binding_refuses_what_an_address_cannot_carry():
     for n, bad in ((5, {}), (4, dict(num_heads=3)), (4, dict(kv_rows=d["rows"][:1].expand(4, 576))), (4, dict(kv_rows=d["rows"].float())),
                    (4, dict(q_rows=d["q"][:, :1].expand(4, 2, 576))), (4, dict(q_rows=d["q"].transpose(1, 2).contiguous().transpose(1, 2))),
                    (4, dict(positions=d["pos"].long())), (4, dict(page_table=d["table"].cpu())), (4, dict(q_out=q_out[:2])),
-                   (4, dict(cos_sin=d["cos_sin"].double())), (4, dict(norm_weight=d["weight"].bfloat16()))):
+                   (4, dict(cos_sin=d["cos_sin"].double())), (4, dict(norm_weight=d["weight"].bfloat16())),
+                   (4, dict(norm_weight=d["weight"][:511].contiguous())), (4, dict(positions=d["pos"][:3].contiguous())),
+                   (4, dict(num_pages=i["pages"] + 1)), (4, dict(cache_kind=mla.CACHE_BF16)), (4, dict(rope_rows=d["cos_sin"].shape[0] + 1)),
+                   (4, dict(batch=2)), (4, dict(q_kind=mla.CACHE_BF16))):
         with pytest.raises(ValueError):
             mla.mla_prologue(n, **dict(good, **bad))
     mla.mla_prologue(4, **good)
