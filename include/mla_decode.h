@@ -478,6 +478,7 @@ MLA_API int mla_kv_append(const void* rows_bf16, int64_t n_tokens, const int32_t
  * (mla_kv_append divides; for scales that are powers of two these are the same
  * numbers) and saturates (E4M3 at 448, FP4 at 384).  A NaN stays one.
  *
+ * n_tokens      0: nothing is done or checked.
  * positions     device int32 [n_tokens]: each token's index within its request.
  * cos_sin       device fp32 [rope_rows][64], 16-byte aligned: 32 cosines, then
  *               32 sines per position; NULL (with rope_rows 0): no rotation.

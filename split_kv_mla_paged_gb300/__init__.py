@@ -666,6 +666,8 @@ def mla_pages_copy(src_pool, src_pages: int, src_kind: int, dst_pool, dst_pages:
     tensors."""
     import torch
     i32 = torch.int32
+    if src_pool is not None and src_pool.get_device() != dst_pool.get_device():
+        raise ValueError("the pools must be on one device")
     _call_on(dst_pool, load_library().mla_pages_copy,
              _device_pool(src_pool, "src_pool", src_pages, src_kind), src_pages, src_kind,
              _device_pool(dst_pool, "dst_pool", dst_pages, dst_kind), dst_pages, dst_kind,

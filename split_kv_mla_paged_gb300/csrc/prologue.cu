@@ -310,12 +310,13 @@ extern "C" int mla_prologue(const mla_prologue_args_t* args, void* stream) {
   };
   const bool keys = a.kv_rows != nullptr, queries = a.q_rows != nullptr;
   if (a.n_tokens < 0) return bad("n_tokens must be >= 0");
+  if (a.n_tokens == 0) return MLA_OK;  // (an empty batch's row pointers are null)
   if (!keys && !queries) return bad("neither kv_rows nor q_rows");
   if (a.rope_halves != 0 && a.rope_halves != 1) return bad("rope_halves must be 0 or 1");
   if (a.cos_sin ? a.rope_rows < 1 : a.rope_rows != 0)
     return bad("rope_rows must be >= 1 with cos_sin and 0 without");
   if (a.cos_sin && !aligned(a.cos_sin, 16)) return bad("cos_sin needs 16-byte alignment");
-  if (a.n_tokens > 0 && !a.positions && (keys || (a.cos_sin && !a.rope_positions)))
+  if (!a.positions && (keys || (a.cos_sin && !a.rope_positions)))
     return bad("null positions");
   if (keys) {
     if (a.kv_row_stride == 0) a.kv_row_stride = MLA_HEAD_DIM;
@@ -356,7 +357,6 @@ extern "C" int mla_prologue(const mla_prologue_args_t* args, void* stream) {
     if (!std::isnormal(a.q_scale) || !std::isnormal(1.0f / a.q_scale))
       return bad("q_scale and its reciprocal must be normal numbers");
   }
-  if (a.n_tokens == 0) return MLA_OK;
   p.inv_kv_scale = keys ? 1.0f / a.kv_scale : 1.0f;
   p.inv_q_scale = queries ? 1.0f / a.q_scale : 1.0f;
   p.head_groups = queries ? (a.num_heads - 1) / 4 + 1 : 0;

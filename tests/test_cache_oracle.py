@@ -161,6 +161,8 @@ def test_prologue_other_refusals(lib):
     assert lib.mla_prologue(_args(q_kind=mla.CACHE_FP4), None) == mla.MLA_ERR_UNSUPPORTED
     assert lib.mla_prologue(_args(n_tokens=1 << 40), None) == mla.MLA_ERR_UNSUPPORTED
     assert lib.mla_prologue(_args(n_tokens=0, positions=None), None) == mla.MLA_OK  # touches nothing
+    # An empty batch's tensors have null addresses.
+    assert lib.mla_prologue(_args(n_tokens=0, positions=None, kv_rows=None, q_rows=None, q_out=None), None) == mla.MLA_OK
 
 
 def test_decode_fp4_refusals(lib):

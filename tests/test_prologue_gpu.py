@@ -272,6 +272,13 @@ def test_queries_alone_and_keys_alone():
     assert none is None and torch.equal(got, ref)
 
 
+def test_empty_batch():
+    i = _inputs(1, 3, 2, seed=18)
+    empty = {k: (v[:0] if k in ("rows", "q", "pos", "req") else v) for k, v in i.items()}
+    pool, q_out, st = _run(empty, "fp4")
+    assert st == 0 and q_out.numel() == 0 and torch.equal(pool, _pool("fp4", i["pages"]))
+
+
 def test_side_stream_and_graph_replay():
     i = _inputs(2, 8, 4, seed=15, start=100)
     ref, qref, _ = _run(i, "fp4")
