@@ -687,6 +687,17 @@ def mla_pages_remap(page_table, n_entries: int, page_map, num_pages: int, status
              _device_tensor(status, "status", i32), stream=stream)
 
 
+def _host_ids(ids, name: str) -> np.ndarray:
+    """A host list of page ids or counts as int32; ValueError where that would
+    change a value."""
+    a = np.asarray(ids).reshape(-1)
+    if a.size and a.dtype.kind not in "iu":
+        raise ValueError(f"{name} must be integers, got {a.dtype}")
+    if a.size and (int(a.min()) < -(1 << 31) or int(a.max()) >= 1 << 31):
+        raise ValueError(f"{name} does not fit in 32 bits")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
 class PagePool:
     """Reference-counted pages of one cache (mla_pool_*): which are free, forks
     and compactions.  Host only; page ids are int32 numpy arrays.  The copies
@@ -698,6 +709,9 @@ class PagePool:
         handle = ctypes.c_void_p()
         _check(self._lib.mla_pool_create(self.num_pages, ctypes.byref(handle)))
         self._handle = handle
+
+    def __reduce__(self):
+        raise TypeError("a PagePool cannot be copied or pickled")
 
     def __del__(self):
         if getattr(self, "_handle", None):
@@ -719,13 +733,13 @@ class PagePool:
 
     def release(self, ids) -> None:
         """Give back one reference of each listed page."""
-        ids = np.ascontiguousarray(ids, dtype=np.int32).reshape(-1)
+        ids = _host_ids(ids, "ids")
         _check(self._lib.mla_pool_release(self._handle, ids.ctypes.data, ids.shape[0]))
 
     def fork(self, ids, kv_len: int, n_forks: int):
         """Fork a request of kv_len tokens: (page lists [n_forks, pages], src,
         dst, rows), the last three the copies to make."""
-        ids = np.ascontiguousarray(ids, dtype=np.int32).reshape(-1)
+        ids = _host_ids(ids, "ids")
         pages = (int(kv_len) + PAGE_SIZE - 1) // PAGE_SIZE
         if ids.shape[0] < pages:
             raise ValueError(f"kv_len {kv_len} needs {pages} pages, got {ids.shape[0]}")
@@ -920,7 +934,7 @@ def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> 
     Lists in which a page would be written twice, or both read and written,
     are refused (ValueError): the copies of one call run in no order."""
     import torch
-    src, dst = (np.ascontiguousarray(x, dtype=np.int32).reshape(-1) for x in (src_ids, dst_ids))
+    src, dst = _host_ids(src_ids, "src_ids"), _host_ids(dst_ids, "dst_ids")
     if src.shape != dst.shape:
         raise ValueError("src_ids and dst_ids must have the same length")
     n = int(src.shape[0])
@@ -935,7 +949,7 @@ def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> 
         raise ValueError("a page is both a source and a destination")
     lists = [src, dst]
     if rows is not None:
-        lists.append(np.broadcast_to(np.asarray(rows, dtype=np.int32), (n,)))
+        lists.append(np.broadcast_to(_host_ids(rows, "rows"), (n,)))
         if lists[2].min() < 0 or lists[2].max() > PAGE_SIZE:
             raise ValueError("rows must be in 0..32")
     # One upload for the lists, on the stream that the copy runs on (the lists

@@ -237,4 +237,8 @@ def test_copy_pages_refuses_clashing_lists():
         mla.copy_pages(pool, other, [0], [1, 2])
     with pytest.raises(ValueError, match="0..32"):
         mla.copy_pages(pool, other, [0], [1], rows=33)
+    with pytest.raises(ValueError, match="32 bits"):
+        mla.copy_pages(pool, other, [1 << 32], [1])
+    with pytest.raises(ValueError, match="integers"):
+        mla.copy_pages(pool, other, [0], [1], rows=2.5)
     mla.copy_pages(pool, other, [], [])

@@ -159,3 +159,20 @@ def test_threads_do_not_share_pages():
     for t in threads:
         t.join()
     assert np.array_equal(np.sort(np.concatenate(got)), np.arange(4000))
+
+
+def test_ids_are_not_truncated_and_pools_not_copied():
+    import copy
+    import pickle
+    p = mla.PagePool(4)
+    p.alloc(2)
+    for bad in ([1 << 32], [0.0], [-(1 << 40)]):
+        with pytest.raises(ValueError):
+            p.release(bad)
+        with pytest.raises(ValueError):
+            p.fork(bad, 32, 1)
+    assert p.free_pages == 2
+    for f in (copy.copy, copy.deepcopy, pickle.dumps):
+        with pytest.raises(TypeError):
+            f(p)
+    assert p.alloc(1).tolist() == [2]
