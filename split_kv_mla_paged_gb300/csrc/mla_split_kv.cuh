@@ -288,6 +288,29 @@ __device__ __forceinline__ bool item_info(const DecodeParams& p, int b, int spli
   return true;
 }
 
+// 4-bit cache: pool page of the item's compact page pi (counted like positions,
+// or like the selection's entries); -1 where it is not loaded.  Bad ids are
+// reported by the producer, which reads page 0 in their place, as here.  key0
+// (restricted key sets): the first key position of the page.
+template <bool kGather>
+__device__ __forceinline__ int fp4_page(const DecodeParams& p, const ItemInfo& it, int pi,
+                                        int& key0) {
+  key0 = 0;
+  if (pi >= (it.tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE) return -1;
+  int lp = pi;
+  if constexpr (kGather) {
+    if (it.sparse)
+      lp = (pi < p.topk) ? p.block_idx[static_cast<int64_t>(it.b) * p.topk + pi] : -1;
+    const int64_t first_pos = static_cast<int64_t>(lp) * MLA_PAGE_SIZE;
+    if (lp < 0 || first_pos >= (it.sparse ? it.win_hi : it.tok_end) ||
+        first_pos + MLA_PAGE_SIZE <= it.win_lo)
+      return -1;
+    key0 = lp * MLA_PAGE_SIZE;
+  }
+  const int pg = p.page_table[static_cast<int64_t>(it.b) * p.max_pages + lp];
+  return (pg < 0 || pg >= p.num_pages) ? 0 : pg;
+}
+
 // Decodes a CTA item-list entry; false (reported) for an item outside the
 // batch or the row groups.
 __device__ __forceinline__ bool decode_item(const DecodeParams& p, int it, int ngroups, int& b,
@@ -337,6 +360,12 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       grp = blockIdx.y - split * ngroups;
       b = blockIdx.x;
     }
+    if constexpr (kFp4) {
+      // The plan's three words in one round trip: item_info reads the other two
+      // from L1.
+      const int len = p.kv_lens[b], chunk = p.chunks[b];
+      asm volatile("" ::"r"(len), "r"(chunk));
+    }
     if (split >= p.splits[b]) return;  // empty split slot of a shorter request
     if (!item_info<kGather>(p, b, split, grp, first)) return;
   }
@@ -379,6 +408,16 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     }
   }
   (void)pre_window;
+  // 4-bit cache: the expanders' first page ids likewise.
+  int pre_page = -1, pre_key0 = 0;
+  if constexpr (kFp4 && !C::kBlockStages) {
+    const int ew = static_cast<int>(threadIdx.x >> 5) - C::kExpandWarp0;
+    const int ch = ew + C::kExpandWarps * static_cast<int>(threadIdx.x & 31);
+    if (ew >= 0 && ch < first.n_tiles * 8)
+      pre_page = fp4_page<kGather>(p, first, first.t0 / MLA_PAGE_SIZE + (ch >> 1), pre_key0);
+  }
+  (void)pre_page;
+  (void)pre_key0;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
@@ -993,31 +1032,19 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         const int ew = warp - C::kExpandWarp0;
         const int par = (lane >> 2) & 1, tok8 = (lane >> 3) * 8;
         const int n_chunks = n_tiles * 16;  // this warp takes chunks ew, ew + W, ...
-        const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-        const int page0 = t0 / MLA_PAGE_SIZE;
-        const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;  // exclusive
         // Page of this warp's chunk number 32 w + lane: page 0 in the place of
-        // one that is not loaded (the QK warp zeroes its rows) or has a bad id
-        // (the producer reports it and reads page 0, too).  hide (restricted key
-        // sets): how many of its rows lie before the key window.
+        // one that is not loaded (the QK warp zeroes its rows).  hide (restricted
+        // key sets): how many of its rows lie before the key window.
         auto chunk_window = [&](int w, int& hide) -> int {
           hide = 0;
           const int ch = ew + W * (w * 32 + lane);
           if (ch >= n_chunks) return 0;
-          const int pi = page0 + (ch >> 4) * 4 + (ch & 3);
-          if (pi >= page_end) return 0;
-          int lp = pi;
-          if constexpr (kGather) {
-            if (sparse)
-              lp = (pi < p.topk) ? p.block_idx[static_cast<int64_t>(b) * p.topk + pi] : -1;
-            const int64_t first_pos = static_cast<int64_t>(lp) * MLA_PAGE_SIZE;
-            if (lp < 0 || first_pos >= (sparse ? win_hi : tok_end) ||
-                first_pos + MLA_PAGE_SIZE <= win_lo)
-              return 0;
-            hide = max(0, static_cast<int>(win_lo - first_pos));
-          }
-          const int pg = pt[lp];
-          return (pg < 0 || pg >= p.num_pages) ? 0 : pg;
+          int key0;
+          const int pg =
+              fp4_page<kGather>(p, first, t0 / MLA_PAGE_SIZE + (ch >> 4) * 4 + (ch & 3), key0);
+          if (pg < 0) return 0;
+          if constexpr (kGather) hide = max(0, win_lo - key0);
+          return pg;
         };
         int hide, hide_next;
         int window = chunk_window(0, hide), window_next = chunk_window(1, hide_next);
@@ -1126,33 +1153,16 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         const int ew = warp - C::kExpandWarp0;
         const int blk = (lane >> 3) * 4 + (lane & 3), par = (lane >> 2) & 1;
         const int n_chunks = n_tiles * 8;  // this warp takes chunks ew, ew + W, ...
-        const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-        const int page0 = t0 / MLA_PAGE_SIZE;
-        const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;  // exclusive
         // Page of this warp's chunk number 32 w + lane (-1: not loaded; the QK warp
-        // zeroes those rows).  Bad ids are reported by the producer, which reads
-        // page 0 in their place, as here.
-        // key0 (restricted key sets): the first key position of the page.
+        // zeroes those rows).
         auto chunk_window = [&](int w, int& key0) -> int {
           key0 = 0;
           const int ch = ew + W * (w * 32 + lane);
           if (ch >= n_chunks) return -1;
-          const int pi = page0 + (ch >> 1);
-          if (pi >= page_end) return -1;
-          int lp = pi;
-          if constexpr (kGather) {
-            if (sparse) lp = (pi < p.topk) ? p.block_idx[static_cast<int64_t>(b) * p.topk + pi] : -1;
-            const int64_t first_pos = static_cast<int64_t>(lp) * MLA_PAGE_SIZE;
-            if (lp < 0 || first_pos >= (sparse ? win_hi : tok_end) ||
-                first_pos + MLA_PAGE_SIZE <= win_lo)
-              return -1;
-            key0 = lp * MLA_PAGE_SIZE;
-          }
-          const int pg = pt[lp];
-          return (pg < 0 || pg >= p.num_pages) ? 0 : pg;
+          return fp4_page<kGather>(p, first, t0 / MLA_PAGE_SIZE + (ch >> 1), key0);
         };
-        int key0, key0_next;
-        int window = chunk_window(0, key0), window_next = chunk_window(1, key0_next);
+        int key0 = pre_key0, key0_next;  // (window 0 was read before the set-up)
+        int window = pre_page, window_next = chunk_window(1, key0_next);
         // A chunk in registers: the codes of tokens 2 k + par, the block's 16
         // scale codes and (restricted key sets) how many of its tokens, which
         // come first, lie before the key window.
