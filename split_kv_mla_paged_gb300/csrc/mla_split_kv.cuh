@@ -1874,9 +1874,10 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         // warp turns its 32 dims x 8 rows at a time around through 1 KB of it,
         // so that a lane stores 4 contiguous dims of a row (16 B of a partial,
         // 8 B of BF16 output) instead of one dim of each of four rows.
-        float* const scr = reinterpret_cast<float*>(base + C::kP) +
+        // (4-bit cache, 16 rows: through the KV stages, which are free as well.)
+        constexpr bool transpose = !C::kPInStage || kFp4;
+        float* const scr = reinterpret_cast<float*>(base + (C::kPInStage ? C::kKV : C::kP)) +
                            (warp - C::kSoftmaxWarp0) * 256;
-        constexpr bool transpose = !C::kPInStage;
         // The rows' scales in registers: read from shared memory inside the
         // store loops, each would wait behind the previous row's stores (the
         // compiler cannot tell the two shared-memory pointers apart).
