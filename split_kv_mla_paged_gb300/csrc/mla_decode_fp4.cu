@@ -6,10 +6,10 @@
 // it, bit for bit for the same plan and row groups.
 //
 // What it must move per key row: 336 bytes (256 codes, 16 scales, 64 rope)
-// instead of 576.  Measured (calls in a CUDA graph): H12 q1 B1 x 1M keys 101 us
-// (the E4M3 decode on the same values 103), B16 x 128K 189 us (197), 256 selected pages of 16
-// requests 27.3 us (29.3), H24 q1 B4 x 128K 75.5 us (73.8), H12 q8 B16 x 128K 450
-// us (346).  The bytes alone would take 52.7 and 105 us in the first two: what
+// instead of 576.  Measured (calls in a CUDA graph; in brackets the E4M3 decode on
+// values of the same distribution): H12 q1 B1 x 1M keys 98.6 us (103.8), B16 x
+// 128K 185 us (199), 256 selected pages of 16 requests 27.0 us (29.3), H24 q1 B4
+// x 128K 74.6 us (73.8), H12 q8 B16 x 128K 450 us (347).  The bytes alone would take 52.7 and 105 us in the first two: what
 // bounds them is shared memory's pipe, which the expansion's stores share with
 // the MMAs' operands (see the expander warps); from 48 rows on the softmax has
 // fewer registers than in the E4M3 kernel besides.

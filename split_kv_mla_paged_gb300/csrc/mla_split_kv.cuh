@@ -597,9 +597,10 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         int window_next = load_window(1, window_next_nv);
         // 4-bit cache: pages go to L2 kPrefetch tiles ahead, so that the
         // expanders' loads, of which registers hold one tile, find them there
-        // (16 rows, B1 1M: 111.6 us without, 109.4 with 3, 110.7 with 5 tiles; H12
-        // q8 B16 128K 519 -> 505 us).
-        constexpr int kPrefetch = 3;
+        // (16 rows, B1 1M: 98.9 us with 2, 99.9 with 3, 101.0 with 4, and 2 % more
+        // without; 96 rows, H12 q8 B16 128K: 505 us with 3, 517 with 1, 519
+        // without).
+        constexpr int kPrefetch = C::kWide ? 3 : 2;
         auto prefetch_tile = [&](int j, int i) {
           if constexpr (kFp4) {
             const bool here = (j >> 3) == (i >> 3);
