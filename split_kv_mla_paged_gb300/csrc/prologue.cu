@@ -27,7 +27,7 @@
 
 namespace mla {
 
-constexpr int kPrologueWarps = 8;
+constexpr int kPrologueWarps = 4;
 
 struct PrologueParams {
   mla_prologue_args_t a;
@@ -274,11 +274,12 @@ __device__ __forceinline__ void query_rows(const PrologueParams& p, int64_t t, i
   }
 }
 
-// Bound by the bytes read and written.  At least three CTAs per SM (80
-// registers): 32,767 tokens of 12 heads into a BF16 cache 168 -> 148 us (6.64
-// TB/s), 8,192 tokens into an E4M3 cache 35.5 -> 32.0 us; with one row per warp
-// it was 265 and 51 us, the rows' index and table loads one after the other.
-__global__ void __launch_bounds__(32 * kPrologueWarps, 3)
+// Bound by the bytes read and written.  Six CTAs of four warps per SM (80
+// registers): 32,767 tokens of 12 heads into a BF16 cache 146.0 us (6.72 TB/s),
+// 8,192 tokens into an E4M3 cache 31.4 us; three of eight warps 147.8 and 32.0,
+// two of eight 168 and 35.5, four of eight (64 registers) 153.7 and 33.2 us.  One
+// row per warp took 265 and 51 us, its index and table loads one after the other.
+__global__ void __launch_bounds__(32 * kPrologueWarps, 6)
     mla_prologue_kernel(const __grid_constant__ PrologueParams p) {
   const int lane = threadIdx.x & 31;
   int64_t u = static_cast<int64_t>(blockIdx.x) * kPrologueWarps + (threadIdx.x >> 5);
