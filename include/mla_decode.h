@@ -21,6 +21,9 @@
  *   the MTP-verify block, query token i sees keys [0, L - q_len + i]),
  *   O = sum_j softmax(s)_j v_j  (BF16, round to nearest even),
  *   LSE = ln sum_j exp(s_j)     (natural log, fp32).
+ * Scores are held in fp32, in log2 units; what is computed is this definition
+ * while |s_j| log2(e) stays below 2^24 (fp32 then holds a score to one unit).
+ * BF16 caches with more than 16 rows per request: below 2^21.
  *
  * Conventions for every function:
  *   - Return value is an mla_status_t.  Nothing throws, exits or aborts.

@@ -117,8 +117,7 @@ __device__ __forceinline__ float pow2i(int i) { return __int_as_float((i + 127) 
 // t far below k to 0 through the exponent clamp (-inf by a select), which
 // keeps the many independent weights of a 24-row thread in flight; the other
 // form takes an exact fallback branch for |t| >= 2^21 or -inf, which is
-// faster for the 16-row kernel.  Scores above 2^21 in log2 units are outside
-// the branch-free form's range.
+// faster for the 16-row kernel.  The branch-free form wants |k| <= kFarReference.
 template <bool kBranchFree>
 __device__ __forceinline__ float softmax_weight(float t, float k) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
@@ -213,6 +212,7 @@ __device__ __forceinline__ void split_e4m3x2_h(float w0, float w1, uint32_t& hi,
 // without a reference (kc = kKcNone) give an exponent below 0, i.e. 0.
 // Requires t <= k + 0.75 (the vote guarantees it), so the exponent stays
 // below 255.
+constexpr int kKcZero = 135 - 0x4B400000;  // k = 0
 constexpr int kKcNone = -2130706432;  // -2^31 + 2^24: bits + kc < 0 for every t
 __device__ __forceinline__ float softmax_weight_kc(float t, int kc) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
@@ -222,6 +222,31 @@ __device__ __forceinline__ float softmax_weight_kc(float t, int kc) {
   const float f = tc - r;       // exact, |f| <= 0.5
   const int e = max(__float_as_int(tr) + kc, 0);
   return ex2_approx(f) * __int_as_float(e << 23);
+}
+
+// Rows whose reference k is further from 0 than this are outside the range of
+// softmax_weight<true> and softmax_weight_kc (scores are rounded by an addition
+// that is exact below 2^21, and clamped at -2^21, where a row's weights must be
+// 0).  Such a row's scores are rebased: t - k takes t's place and 0 that of k.
+// The difference is exact where the weight is not 0 (t and k are then within a
+// factor of 2 of each other), so this holds while fp32 resolves the scores.
+constexpr float kFarReference = 2096896.0f;  // 2^21 - 256
+__device__ __forceinline__ float far_base(float k) {
+  return (fabsf(k) > kFarReference && k != -INFINITY) ? k : 0.0f;
+}
+
+// softmax_weight<true> for rebased rows: the same value from three operations
+// fewer, as t <= k + 1 and |k| <= 2^21 need neither the clamp from above nor that
+// of the exponent (r - k + 8 is above -2^22, where the addition of 1.5 * 2^23 is
+// still exact), and 8 goes into the constant.
+__device__ __forceinline__ float softmax_weight_near(float t, float k) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+  const float tc = fmaxf(t, -2097152.0f);
+  const float r = (tc + kMagic) - kMagic;  // rint(tc)
+  const float f = tc - r;                  // exact, |f| <= 0.5
+  const int e = max(__float_as_int((r - k) + (kMagic + 8.0f)) - 0x4B400000 + 127, 0);
+  const float w = ex2_approx(f) * __int_as_float(e << 23);
+  return t == -INFINITY ? 0.0f : w;  // masked (the row's k may still be -inf)
 }
 
 // Warp reduce-scatter over N per-lane values (one per row): afterwards lane
