@@ -1854,7 +1854,9 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
       // ---- epilogue ----
       if constexpr (C::kThreadSums) {
         // The per-thread sums, reduced over the 32 tokens of each warp; the
-        // owners add the four lane quadrants below.
+        // owners add the four lane quadrants below.  96 rows: they go where the
+        // last tile's alphas were, which every warp of the group must have read.
+        if constexpr (C::kWide) named_bar_sync(smx_bar, 128);
         warp_reduce_rows<NRH, false>(lsum, lane, red_sum + quad * NR + rbase);
       }
       named_bar_sync(kSoftmaxBarrier, NT);
