@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import operator
 import os
 import threading
 from typing import Optional, Sequence
@@ -698,6 +699,18 @@ def _host_ids(ids, name: str) -> np.ndarray:
     return np.ascontiguousarray(a, dtype=np.int32)
 
 
+def _host_int(value, name: str, bits: int) -> int:
+    """A host integer that the library takes in `bits` bits; ValueError where that
+    would change it."""
+    try:
+        n = operator.index(value)
+    except TypeError:
+        raise ValueError(f"{name} must be an integer, got {value!r}") from None
+    if not -(1 << (bits - 1)) <= n < 1 << (bits - 1):
+        raise ValueError(f"{name} does not fit in {bits} bits")
+    return n
+
+
 class PagePool:
     """Reference-counted pages of one cache (mla_pool_*): which are free, forks
     and compactions.  Host only; page ids are int32 numpy arrays.  The copies
@@ -705,7 +718,7 @@ class PagePool:
 
     def __init__(self, num_pages: int):
         self._lib = load_library()
-        self.num_pages = int(num_pages)
+        self.num_pages = _host_int(num_pages, "num_pages", 64)
         handle = ctypes.c_void_p()
         _check(self._lib.mla_pool_create(self.num_pages, ctypes.byref(handle)))
         self._handle = handle
@@ -723,7 +736,7 @@ class PagePool:
         return int(self._lib.mla_pool_free_pages(self._handle))
 
     def references(self, page: int) -> int:
-        return int(self._lib.mla_pool_references(self._handle, int(page)))
+        return int(self._lib.mla_pool_references(self._handle, _host_int(page, "page", 32)))
 
     def alloc(self, n: int) -> np.ndarray:
         """The n lowest free pages; MlaError (MLA_ERR_NO_PAGES) if fewer are free."""

@@ -176,3 +176,15 @@ def test_ids_are_not_truncated_and_pools_not_copied():
         with pytest.raises(TypeError):
             f(p)
     assert p.alloc(1).tolist() == [2]
+
+
+def test_single_ids_are_not_truncated():
+    p = mla.PagePool(4)
+    p.alloc(2)
+    for bad in (1 << 32, (1 << 32) + 1, -(1 << 32), 1 << 70, 0.0, 1.5):
+        with pytest.raises(ValueError):
+            p.references(bad)
+    assert [p.references(k) for k in (0, 1, 2, np.int64(3), 4, -1)] == [1, 1, 0, 0, -1, -1]
+    for bad in (1 << 64, (1 << 64) + 3, 2.5):
+        with pytest.raises(ValueError):
+            mla.PagePool(bad)
