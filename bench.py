@@ -33,15 +33,14 @@ DEFAULT_WORKLOAD = "long_h12_q1_l1m_b16"
 # kernel before #19338, on an unspecified Blackwell SM10x GPU): context only.
 PUBLISHED_US = {"long_h12_q1_l1m_b16": 1095.5}
 L2_ROTATE_BYTES = 2 * 126 * 1024 * 1024  # rotate inputs below 2x the 126 MB L2
-# Sources of the split-KV kernel a workload runs (recorded ncu traffic is
-# valid only for the source it was taken on).
-_COMMON_SOURCES = ["split_kv_mla_paged_gb300/csrc/mla_device.cuh",
-                   "split_kv_mla_paged_gb300/csrc/mla_internal.h",
-                   "split_kv_mla_paged_gb300/csrc/sm103_ptx.cuh"]
+# Sources of the split-KV kernel a workload runs, with what they include
+# (recorded ncu traffic is valid only for the source it was taken on).
+_CSRC = "split_kv_mla_paged_gb300/csrc/"
+_COMMON_SOURCES = [_CSRC + "mla_device.cuh", _CSRC + "mla_internal.h", _CSRC + "sm103_ptx.cuh"]
 KERNEL_SOURCES = {
-    "e4m3": ["split_kv_mla_paged_gb300/csrc/mla_decode.cu"] + _COMMON_SOURCES,
-    "bf16": ["split_kv_mla_paged_gb300/csrc/mla_decode_bf16.cu",
-             "split_kv_mla_paged_gb300/csrc/mla_decode.cu"] + _COMMON_SOURCES,
+    "e4m3": [_CSRC + "mla_decode.cu", _CSRC + "mla_split_kv.cuh",
+             _CSRC + "fp4_format.cuh"] + _COMMON_SOURCES,
+    "bf16": [_CSRC + "mla_decode_bf16.cu"] + _COMMON_SOURCES,
 }
 
 
