@@ -434,9 +434,13 @@ def _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sin
         0 if cta_items is None else int(cta_items.numel()), 0, int(phases)))
 
 
-def _fp4_pages(pool, num_pages: int) -> int:
+def _is_fp4_pool(pool) -> bool:
     import torch
-    if pool.dtype is not torch.uint8 or pool.dim() != 2 or pool.shape[1] != FP4_PAGE_BYTES:
+    return pool.dtype is torch.uint8 and tuple(pool.shape[1:]) == (FP4_PAGE_BYTES,)
+
+
+def _fp4_pages(pool, num_pages: int) -> int:
+    if not _is_fp4_pool(pool):
         raise ValueError(f"a 4-bit page pool is uint8 [pages, {FP4_PAGE_BYTES}]")
     return _device_pool(pool, "kv_pages_fp4", num_pages, CACHE_FP4)
 
@@ -850,7 +854,7 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
     if use_items is None:
         use_items = bool(np.any(plan.splits < plan.max_splits)) or persistent_ctas > 0
     is_bf16 = q_fp8.dtype == torch.bfloat16
-    is_fp4 = not is_bf16 and kv_pages_fp8.dim() == 2
+    is_fp4 = not is_bf16 and _is_fp4_pool(kv_pages_fp8)
     if is_fp4 and persistent_ctas > 0:
         raise ValueError("the 4-bit cache has no persistent CTAs")
     items_d = None
@@ -929,7 +933,7 @@ def fp4_pool(num_pages: int, device="cuda"):
 def _cache_kind(pool) -> int:
     """The kind of a page pool, from its type and shape."""
     import torch
-    if pool.dtype is torch.uint8 and tuple(pool.shape[1:]) == (FP4_PAGE_BYTES,):
+    if _is_fp4_pool(pool):
         return CACHE_FP4
     if tuple(pool.shape[1:]) == (PAGE_SIZE, HEAD_DIM):
         if pool.dtype in (torch.uint8, torch.float8_e4m3fn):
