@@ -439,10 +439,10 @@ def _is_fp4_pool(pool) -> bool:
     return pool.dtype is torch.uint8 and tuple(pool.shape[1:]) == (FP4_PAGE_BYTES,)
 
 
-def _fp4_pages(pool, num_pages: int) -> int:
+def _fp4_pages(pool, num_pages: int, q) -> int:
     if not _is_fp4_pool(pool):
         raise ValueError(f"a 4-bit page pool is uint8 [pages, {FP4_PAGE_BYTES}]")
-    return _device_pool(pool, "kv_pages_fp4", num_pages, CACHE_FP4)
+    return _device_pool(pool, "kv_pages_fp4", _device_of(q, "q_fp8"), num_pages, CACHE_FP4)
 
 
 def mla_decode_fp4(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req, kv_lens, splits,
@@ -456,9 +456,9 @@ def mla_decode_fp4(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req
     mla_decode_ex (no persistent CTAs)."""
     opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
                         query_lens, kv_bounds, cta_items, phases)
-    _call_on(q_fp8, load_library().mla_decode_fp4, _ptr(q_fp8), _fp4_pages(kv_pages_fp4, num_pages),
-             num_pages, _ptr(page_table), max_pages_per_req, _ptr(kv_lens), _ptr(splits),
-             _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads, 1 if causal else 0,
+    _call_on(q_fp8, load_library().mla_decode_fp4, _ptr(q_fp8),
+             _fp4_pages(kv_pages_fp4, num_pages, q_fp8), num_pages, _ptr(page_table),
+             max_pages_per_req, _ptr(kv_lens), _ptr(splits), _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads, 1 if causal else 0,
              q_scale, kv_scale, softmax_scale, _ptr(workspace), workspace_bytes, _ptr(out_bf16),
              _ptr(lse_f32), _ptr(out_f32_debug), opts, stream=stream)
 
@@ -474,9 +474,9 @@ def mla_decode_fp4_sparse(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_
     cache (plan with the compact lengths 32 * topk)."""
     opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
                         query_lens, kv_bounds, cta_items, phases)
-    _call_on(q_fp8, load_library().mla_decode_fp4_sparse, _ptr(q_fp8), _fp4_pages(kv_pages_fp4, num_pages),
-             num_pages, _ptr(page_table), max_pages_per_req, _ptr(kv_lens), _ptr(block_idx), topk,
-             _ptr(splits), _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads,
+    _call_on(q_fp8, load_library().mla_decode_fp4_sparse, _ptr(q_fp8),
+             _fp4_pages(kv_pages_fp4, num_pages, q_fp8), num_pages, _ptr(page_table),
+             max_pages_per_req, _ptr(kv_lens), _ptr(block_idx), topk, _ptr(splits), _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads,
              1 if causal else 0, q_scale, kv_scale, softmax_scale, _ptr(workspace),
              workspace_bytes, _ptr(out_bf16), _ptr(lse_f32), _ptr(out_f32_debug), opts,
              stream=stream)
@@ -548,13 +548,21 @@ def mla_kv_append(rows_bf16, n_tokens: int, req_idx, positions, page_table,
         _ptr(status), _stream_handle(stream)))
 
 
-def _device_tensor(t, name: str, dtype=None, least: int = 0, contiguous: bool = True):
-    """Address of a CUDA tensor (None for None), after the checks that a raw
-    address cannot carry: its device, type, contiguity and number of elements."""
-    if t is None:
-        return None
+def _device_of(t, name: str) -> int:
+    """Index of the CUDA device that a call's tensors are on: its first one's."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _device_tensor(t, name: str, device: int, dtype=None, least: int = 0, contiguous: bool = True):
+    """Address of a tensor on CUDA device `device` (None for None), after the
+    checks that a raw address cannot carry: its device, type, contiguity and
+    number of elements."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on device {device}, like the call's others")
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if contiguous and not t.is_contiguous():
@@ -568,12 +576,12 @@ _PAGE_BYTES = {CACHE_FP8: PAGE_SIZE * HEAD_DIM, CACHE_BF16: 2 * PAGE_SIZE * HEAD
                CACHE_FP4: FP4_PAGE_BYTES}
 
 
-def _device_pool(pool, name: str, pages: int, kind: int):
+def _device_pool(pool, name: str, device: int, pages: int, kind: int):
     """Address of a page pool that holds at least `pages` pages of its kind (an
     unknown kind is left to the library to refuse)."""
     if pool is None:
         return None
-    ptr = _device_tensor(pool, name)
+    ptr = _device_tensor(pool, name, device)
     if pool.numel() * pool.element_size() < pages * _PAGE_BYTES.get(kind, 0):
         raise ValueError(f"{name} is smaller than {pages} pages of its kind")
     return ptr
@@ -621,22 +629,23 @@ def mla_prologue(n_tokens: int, *, positions=None, cos_sin=None, rope_positions=
     where = kv_rows if kv_rows is not None else q_rows
     if where is None:
         raise ValueError("mla_prologue needs kv_rows, q_rows or both")
+    dev = _device_of(where, "kv_rows" if kv_rows is not None else "q_rows")
     rows = table = pages = weight = None
     row_stride = token_stride = head_stride = 0
     if kv_rows is not None:
-        rows = _device_tensor(kv_rows, "kv_rows", bf16, 0, False)
+        rows = _device_tensor(kv_rows, "kv_rows", dev, bf16, 0, False)
         if kv_rows.dim() != 2 or kv_rows.shape[1] != HEAD_DIM or kv_rows.stride(1) != 1:
             raise ValueError("kv_rows must be [n_tokens, 576] with dense rows")
         if kv_rows.shape[0] < n_tokens:
             raise ValueError("kv_rows has fewer than n_tokens rows")
         if kv_rows.shape[0] > 1:
             row_stride = _row_stride(kv_rows, 0, "kv_rows")
-        weight = _device_tensor(norm_weight, "norm_weight", f32, LATENT_DIM)
-        table = _device_tensor(page_table, "page_table", i32, batch * max_pages_per_req)
-        pages = _device_pool(kv_pages, "kv_pages", num_pages, cache_kind)
+        weight = _device_tensor(norm_weight, "norm_weight", dev, f32, LATENT_DIM)
+        table = _device_tensor(page_table, "page_table", dev, i32, batch * max_pages_per_req)
+        pages = _device_pool(kv_pages, "kv_pages", dev, num_pages, cache_kind)
     queries = out = None
     if q_rows is not None:
-        queries = _device_tensor(q_rows, "q_rows", bf16, 0, False)
+        queries = _device_tensor(q_rows, "q_rows", dev, bf16, 0, False)
         if q_rows.dim() != 3 or q_rows.shape[2] != HEAD_DIM or q_rows.stride(2) != 1:
             raise ValueError("q_rows must be [n_tokens, num_heads, 576] with dense rows")
         if q_rows.shape[0] < n_tokens or q_rows.shape[1] < num_heads:
@@ -645,21 +654,21 @@ def mla_prologue(n_tokens: int, *, positions=None, cos_sin=None, rope_positions=
             token_stride = _row_stride(q_rows, 0, "q_rows")
         if q_rows.shape[1] > 1:
             head_stride = _row_stride(q_rows, 1, "q_rows")
-        out = _device_tensor(q_out, "q_out", None, n_tokens * num_heads * HEAD_DIM)
+        out = _device_tensor(q_out, "q_out", dev, None, n_tokens * num_heads * HEAD_DIM)
         if out is not None and q_out.element_size() != (2 if q_kind == CACHE_BF16 else 1):
             raise ValueError("q_out must have the element size of q_kind")
     if cos_sin is None:
         rope_rows = 0
     elif rope_rows is None:
         rope_rows = cos_sin.shape[0]
-    a = PrologueArgs(n_tokens, _device_tensor(positions, "positions", i32, n_tokens),
-                     _device_tensor(cos_sin, "cos_sin", f32, rope_rows * ROPE_DIM),
-                     _device_tensor(rope_positions, "rope_positions", i32, n_tokens), rope_rows,
+    a = PrologueArgs(n_tokens, _device_tensor(positions, "positions", dev, i32, n_tokens),
+                     _device_tensor(cos_sin, "cos_sin", dev, f32, rope_rows * ROPE_DIM),
+                     _device_tensor(rope_positions, "rope_positions", dev, i32, n_tokens), rope_rows,
                      1 if rope_halves else 0, rows, row_stride, weight, norm_eps,
-                     max_pages_per_req, _device_tensor(req_idx, "req_idx", i32, n_tokens), table,
+                     max_pages_per_req, _device_tensor(req_idx, "req_idx", dev, i32, n_tokens), table,
                      pages,
                      num_pages, batch, cache_kind, kv_scale, q_scale, queries, token_stride,
-                     head_stride, out, num_heads, q_kind, _device_tensor(status, "status", i32))
+                     head_stride, out, num_heads, q_kind, _device_tensor(status, "status", dev, i32))
     _call_on(where, load_library().mla_prologue, ctypes.byref(a), stream=stream)
 
 
@@ -671,13 +680,12 @@ def mla_pages_copy(src_pool, src_pages: int, src_kind: int, dst_pool, dst_pages:
     tensors."""
     import torch
     i32 = torch.int32
-    if src_pool is not None and src_pool.get_device() != dst_pool.get_device():
-        raise ValueError("the pools must be on one device")
+    dev = _device_of(dst_pool, "dst_pool")
     _call_on(dst_pool, load_library().mla_pages_copy,
-             _device_pool(src_pool, "src_pool", src_pages, src_kind), src_pages, src_kind,
-             _device_pool(dst_pool, "dst_pool", dst_pages, dst_kind), dst_pages, dst_kind,
-             _device_tensor(src_ids, "src_ids", i32, n), _device_tensor(dst_ids, "dst_ids", i32, n),
-             _device_tensor(rows, "rows", i32, n), n, _device_tensor(status, "status", i32),
+             _device_pool(src_pool, "src_pool", dev, src_pages, src_kind), src_pages, src_kind,
+             _device_pool(dst_pool, "dst_pool", dev, dst_pages, dst_kind), dst_pages, dst_kind,
+             _device_tensor(src_ids, "src_ids", dev, i32, n), _device_tensor(dst_ids, "dst_ids", dev, i32, n),
+             _device_tensor(rows, "rows", dev, i32, n), n, _device_tensor(status, "status", dev, i32),
              stream=stream)
 
 
@@ -686,10 +694,11 @@ def mla_pages_remap(page_table, n_entries: int, page_map, num_pages: int, status
     """Replace every page id p >= 0 of a page table by page_map[p], in place."""
     import torch
     i32 = torch.int32
+    dev = _device_of(page_table, "page_table")
     _call_on(page_table, load_library().mla_pages_remap,
-             _device_tensor(page_table, "page_table", i32, n_entries), n_entries,
-             _device_tensor(page_map, "page_map", i32, num_pages), num_pages,
-             _device_tensor(status, "status", i32), stream=stream)
+             _device_tensor(page_table, "page_table", dev, i32, n_entries), n_entries,
+             _device_tensor(page_map, "page_map", dev, i32, num_pages), num_pages,
+             _device_tensor(status, "status", dev, i32), stream=stream)
 
 
 def _host_ids(ids, name: str) -> np.ndarray:
