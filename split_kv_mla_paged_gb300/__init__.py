@@ -458,9 +458,10 @@ def mla_decode_fp4(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req
                         query_lens, kv_bounds, cta_items, phases)
     _call_on(q_fp8, load_library().mla_decode_fp4, _ptr(q_fp8),
              _fp4_pages(kv_pages_fp4, num_pages, q_fp8), num_pages, _ptr(page_table),
-             max_pages_per_req, _ptr(kv_lens), _ptr(splits), _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads, 1 if causal else 0,
-             q_scale, kv_scale, softmax_scale, _ptr(workspace), workspace_bytes, _ptr(out_bf16),
-             _ptr(lse_f32), _ptr(out_f32_debug), opts, stream=stream)
+             max_pages_per_req, _ptr(kv_lens), _ptr(splits), _ptr(chunks), max_splits, kv_split,
+             batch, q_len, num_heads, 1 if causal else 0, q_scale, kv_scale, softmax_scale,
+             _ptr(workspace), workspace_bytes, _ptr(out_bf16), _ptr(lse_f32), _ptr(out_f32_debug),
+             opts, stream=stream)
 
 
 def mla_decode_fp4_sparse(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req, kv_lens,
@@ -476,10 +477,10 @@ def mla_decode_fp4_sparse(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_
                         query_lens, kv_bounds, cta_items, phases)
     _call_on(q_fp8, load_library().mla_decode_fp4_sparse, _ptr(q_fp8),
              _fp4_pages(kv_pages_fp4, num_pages, q_fp8), num_pages, _ptr(page_table),
-             max_pages_per_req, _ptr(kv_lens), _ptr(block_idx), topk, _ptr(splits), _ptr(chunks), max_splits, kv_split, batch, q_len, num_heads,
-             1 if causal else 0, q_scale, kv_scale, softmax_scale, _ptr(workspace),
-             workspace_bytes, _ptr(out_bf16), _ptr(lse_f32), _ptr(out_f32_debug), opts,
-             stream=stream)
+             max_pages_per_req, _ptr(kv_lens), _ptr(block_idx), topk, _ptr(splits), _ptr(chunks),
+             max_splits, kv_split, batch, q_len, num_heads, 1 if causal else 0, q_scale,
+             kv_scale, softmax_scale, _ptr(workspace), workspace_bytes, _ptr(out_bf16),
+             _ptr(lse_f32), _ptr(out_f32_debug), opts, stream=stream)
 
 
 def mla_decode_splitkv(*args, **kw) -> None:
@@ -971,7 +972,15 @@ def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> 
         raise ValueError("page id outside its pool")
     if np.unique(dst).shape[0] != n:
         raise ValueError("a page is the destination of two copies")
-    if src_pool.data_ptr() == dst_pool.data_ptr() and np.intersect1d(src, dst).size:
+    src_kind, dst_kind = _cache_kind(src_pool), _cache_kind(dst_pool)
+    # By address, as the pools may be views of one allocation: the destinations,
+    # which do not overlap each other, in order, and for each source the first
+    # that ends behind its start.
+    src_at = src_pool.data_ptr() + src.astype(np.int64) * _PAGE_BYTES[src_kind]
+    dst_at = np.sort(dst_pool.data_ptr() + dst.astype(np.int64) * _PAGE_BYTES[dst_kind])
+    first = np.searchsorted(dst_at + _PAGE_BYTES[dst_kind], src_at, side="right")
+    reach = first < n
+    if (dst_at[first[reach]] < src_at[reach] + _PAGE_BYTES[src_kind]).any():
         raise ValueError("a page is both a source and a destination")
     lists = [src, dst]
     if rows is not None:
@@ -985,8 +994,8 @@ def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> 
         stream = torch.cuda.ExternalStream(stream, device=dev)
     with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
         lists_d = torch.from_numpy(np.stack(lists)).to(dev)
-        mla_pages_copy(src_pool, src_pool.shape[0], _cache_kind(src_pool), dst_pool,
-                       dst_pool.shape[0], _cache_kind(dst_pool), lists_d[0], lists_d[1], n,
+        mla_pages_copy(src_pool, src_pool.shape[0], src_kind, dst_pool, dst_pool.shape[0],
+                       dst_kind, lists_d[0], lists_d[1], n,
                        rows=lists_d[2] if rows is not None else None)
 
 

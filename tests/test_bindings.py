@@ -3,6 +3,8 @@ they hand addresses to the library.
 
 Stand-ins of CUDA tensors: CPU tensors that report a device.  Every call here
 is refused, so no address of theirs is used."""
+import contextlib
+
 import pytest
 import torch
 
@@ -111,3 +113,46 @@ def test_the_four_bit_pool_is_on_the_queries_device(sparse):
     for other in (On(pool, 1), pool):
         with pytest.raises(ValueError):
             call(other)
+
+
+def _views():
+    big = torch.zeros(200, 32, 576, dtype=torch.uint8)
+    return big, On(big[:100], 0), On(big[50:150], 0)
+
+
+@pytest.mark.parametrize("src, dst", [([50], [0]), ([0, 99], [7, 49]), ([60, 70], [20, 5])])
+def test_page_copies_see_through_views_of_one_pool(src, dst):
+    # Page 50 + k of the first view is page k of the second.
+    _, a, b = _views()
+    with pytest.raises(ValueError, match="both a source"):
+        mla.copy_pages(a, b, src, dst)
+    with pytest.raises(ValueError, match="both a source"):
+        mla.copy_pages(b, a, dst, src)
+
+
+def test_page_copies_see_through_views_of_other_kinds():
+    # E4M3 pages are 18,432 bytes and 4-bit pages 10,752: page 7 of one
+    # buffer's 4-bit view lies in E4M3 pages 4 (73,728 .. 92,160) and no other.
+    buf = torch.zeros(20 * 18432 + 16, dtype=torch.uint8)
+    wide = On(buf[:20 * 18432].view(20, 32, 576), 0)
+    slim = On(buf[:20 * 10752].view(20, mla.FP4_PAGE_BYTES), 0)
+    with pytest.raises(ValueError, match="both a source"):
+        mla.copy_pages(wide, slim, [0, 4], [0, 7])
+    with pytest.raises(ValueError, match="both a source"):
+        mla.copy_pages(slim, wide, [7], [4])
+    shifted = On(buf[16:16 + 19 * 18432].view(19, 32, 576), 0)  # 16 bytes on: page 3 ends in page 4
+    with pytest.raises(ValueError, match="both a source"):
+        mla.copy_pages(shifted, wide, [3], [4])
+
+
+def test_page_copies_between_disjoint_parts_go_on(monkeypatch):
+    went = []
+    monkeypatch.setattr(mla, "mla_pages_copy", lambda *a, **k: went.append(a))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: None)
+    big, a, b = _views()
+    mla.copy_pages(a, b, [0, 49], [50, 99])      # pages 0 and 49 of the pool to 100 and 149
+    mla.copy_pages(a, b, [50, 51], [2, 3])       # 50 and 51 to 52 and 53
+    mla.copy_pages(a, a, [1, 2], [3, 4])
+    mla.copy_pages(a, On(big[100:], 0), [0, 99], [0, 99])
+    assert len(went) == 4
