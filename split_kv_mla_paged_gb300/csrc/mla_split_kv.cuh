@@ -1605,13 +1605,20 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             // B2: references ready.
             far = bar_sync_or(smx_bar, 128, far_base(k_row) != 0.0f);
             bool corr = false;
+            static_assert(C::kKref % 16 == 0 && C::kAlpha % 16 == 0, "16-byte loads");
 #pragma unroll
-            for (int k = 0; k < NRH; ++k) {
-              const float kr = kref[rbase + k], al = alpha_s[rbase + k];
-              thr[k] = kr + 0.75f;
-              kci[k] = (kr == -INFINITY) ? kKcNone : kKcZero - static_cast<int>(kr);
-              lsum[k] *= al;
-              corr |= al != 1.0f;
+            for (int q = 0; q < NRH / 4; ++q) {
+              const float4 k4 = *reinterpret_cast<const float4*>(kref + rbase + 4 * q);
+              const float4 a4 = *reinterpret_cast<const float4*>(alpha_s + rbase + 4 * q);
+              const float kr[4] = {k4.x, k4.y, k4.z, k4.w}, al[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const int k = 4 * q + m;
+                thr[k] = kr[m] + 0.75f;
+                kci[k] = (kr[m] == -INFINITY) ? kKcNone : kKcZero - static_cast<int>(kr[m]);
+                lsum[k] *= al[m];
+                corr |= al[m] != 1.0f;
+              }
             }
             if (far) {
 #pragma unroll

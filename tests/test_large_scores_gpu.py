@@ -86,7 +86,9 @@ def test_far_scores_match_oracle(heads, q_len, m, kind):
         vmax[b] = np.abs(values[table[b, :(n + 31) // 32].numpy()].reshape(-1, 576)[:n, :512]).max(0)
     tol = np.repeat(vmax, q_len * heads, 0) * 2.0 ** -7
     # One and several splits, and the variants with windows and with device scales.
-    for kw in (dict(target_ctas=1), dict(target_ctas=9), dict(kv_bounds=[[0, n] for n in LENS]), dict(device_scales=True)):
+    # (E4M3: and CTAs that go from one item to the next).
+    for kw in (dict(target_ctas=1), dict(target_ctas=9), dict(kv_bounds=[[0, n] for n in LENS]), dict(device_scales=True),
+               dict(target_ctas=9, persistent_ctas=2 if kind == "fp8" else 0)):
         _, lse, out = mla.decode(q.cuda(), (pool if kind == "fp4" else wide).cuda(), table.cuda(), LENS, num_heads=heads,
                                  q_len=q_len, causal=q_len > 1, softmax_scale=LN2, q_scale=2.0 ** m, want_f32=True, **kw)
         torch.cuda.synchronize()
