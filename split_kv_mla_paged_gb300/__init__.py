@@ -439,10 +439,10 @@ def _is_fp4_pool(pool) -> bool:
     return pool.dtype is torch.uint8 and tuple(pool.shape[1:]) == (FP4_PAGE_BYTES,)
 
 
-def _fp4_pages(pool, num_pages: int, q) -> int:
+def _fp4_pages(pool, num_pages: int, device: int) -> int:
     if not _is_fp4_pool(pool):
         raise ValueError(f"a 4-bit page pool is uint8 [pages, {FP4_PAGE_BYTES}]")
-    return _device_pool(pool, "kv_pages_fp4", _device_of(q, "q_fp8"), num_pages, CACHE_FP4)
+    return _device_pool(pool, "kv_pages_fp4", device, num_pages, CACHE_FP4)
 
 
 def mla_decode_fp4(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req, kv_lens, splits,
@@ -456,8 +456,9 @@ def mla_decode_fp4(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_per_req
     mla_decode_ex (no persistent CTAs)."""
     opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
                         query_lens, kv_bounds, cta_items, phases)
-    _call_on(q_fp8, load_library().mla_decode_fp4, _ptr(q_fp8),
-             _fp4_pages(kv_pages_fp4, num_pages, q_fp8), num_pages, _ptr(page_table),
+    dev = _device_of(q_fp8, "q_fp8")
+    _call_on(dev, load_library().mla_decode_fp4, _ptr(q_fp8),
+             _fp4_pages(kv_pages_fp4, num_pages, dev), num_pages, _ptr(page_table),
              max_pages_per_req, _ptr(kv_lens), _ptr(splits), _ptr(chunks), max_splits, kv_split,
              batch, q_len, num_heads, 1 if causal else 0, q_scale, kv_scale, softmax_scale,
              _ptr(workspace), workspace_bytes, _ptr(out_bf16), _ptr(lse_f32), _ptr(out_f32_debug),
@@ -475,8 +476,9 @@ def mla_decode_fp4_sparse(q_fp8, kv_pages_fp4, num_pages, page_table, max_pages_
     cache (plan with the compact lengths 32 * topk)."""
     opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
                         query_lens, kv_bounds, cta_items, phases)
-    _call_on(q_fp8, load_library().mla_decode_fp4_sparse, _ptr(q_fp8),
-             _fp4_pages(kv_pages_fp4, num_pages, q_fp8), num_pages, _ptr(page_table),
+    dev = _device_of(q_fp8, "q_fp8")
+    _call_on(dev, load_library().mla_decode_fp4_sparse, _ptr(q_fp8),
+             _fp4_pages(kv_pages_fp4, num_pages, dev), num_pages, _ptr(page_table),
              max_pages_per_req, _ptr(kv_lens), _ptr(block_idx), topk, _ptr(splits), _ptr(chunks),
              max_splits, kv_split, batch, q_len, num_heads, 1 if causal else 0, q_scale,
              kv_scale, softmax_scale, _ptr(workspace), workspace_bytes, _ptr(out_bf16),
@@ -588,11 +590,10 @@ def _device_pool(pool, name: str, device: int, pages: int, kind: int):
     return ptr
 
 
-def _call_on(tensor, fn, *args, stream=None) -> None:
-    """fn(*args, stream) with the tensor's device current: on `stream`, or on
-    that device's current stream."""
+def _call_on(index: int, fn, *args, stream=None) -> None:
+    """fn(*args, stream) with CUDA device `index` current: on `stream`, or on that
+    device's current stream."""
     import torch
-    index = tensor.get_device()
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     else:
@@ -670,7 +671,7 @@ def mla_prologue(n_tokens: int, *, positions=None, cos_sin=None, rope_positions=
                      pages,
                      num_pages, batch, cache_kind, kv_scale, q_scale, queries, token_stride,
                      head_stride, out, num_heads, q_kind, _device_tensor(status, "status", dev, i32))
-    _call_on(where, load_library().mla_prologue, ctypes.byref(a), stream=stream)
+    _call_on(dev, load_library().mla_prologue, ctypes.byref(a), stream=stream)
 
 
 def mla_pages_copy(src_pool, src_pages: int, src_kind: int, dst_pool, dst_pages: int,
@@ -682,7 +683,7 @@ def mla_pages_copy(src_pool, src_pages: int, src_kind: int, dst_pool, dst_pages:
     import torch
     i32 = torch.int32
     dev = _device_of(dst_pool, "dst_pool")
-    _call_on(dst_pool, load_library().mla_pages_copy,
+    _call_on(dev, load_library().mla_pages_copy,
              _device_pool(src_pool, "src_pool", dev, src_pages, src_kind), src_pages, src_kind,
              _device_pool(dst_pool, "dst_pool", dev, dst_pages, dst_kind), dst_pages, dst_kind,
              _device_tensor(src_ids, "src_ids", dev, i32, n), _device_tensor(dst_ids, "dst_ids", dev, i32, n),
@@ -696,7 +697,7 @@ def mla_pages_remap(page_table, n_entries: int, page_map, num_pages: int, status
     import torch
     i32 = torch.int32
     dev = _device_of(page_table, "page_table")
-    _call_on(page_table, load_library().mla_pages_remap,
+    _call_on(dev, load_library().mla_pages_remap,
              _device_tensor(page_table, "page_table", dev, i32, n_entries), n_entries,
              _device_tensor(page_map, "page_map", dev, i32, num_pages), num_pages,
              _device_tensor(status, "status", dev, i32), stream=stream)
@@ -954,6 +955,24 @@ def _cache_kind(pool) -> int:
                      "or uint8 [pages, 10752] (4 bits)")
 
 
+def _pages_clash(src_at: int, src_kind: int, src, dst_at: int, dst_kind: int, dst) -> bool:
+    """Whether a page of src, in a pool at address src_at, shares a byte with one
+    of dst (distinct ids) in a pool at dst_at: pools may be views of one allocation."""
+    src_bytes, dst_bytes = _PAGE_BYTES[src_kind], _PAGE_BYTES[dst_kind]
+    if (src_at + (int(src.max()) + 1) * src_bytes <= dst_at
+            or dst_at + (int(dst.max()) + 1) * dst_bytes <= src_at):
+        return False
+    if src_at == dst_at and src_bytes == dst_bytes:
+        return np.intersect1d(src, dst).size > 0
+    # The destinations, which do not overlap each other, in order, and for each
+    # source the first that ends behind its start.
+    src_at = src_at + src.astype(np.int64) * src_bytes
+    dst_at = np.sort(dst_at + dst.astype(np.int64) * dst_bytes)
+    first = np.searchsorted(dst_at + dst_bytes, src_at, side="right")
+    reach = first < dst.shape[0]
+    return bool((dst_at[first[reach]] < src_at[reach] + src_bytes).any())
+
+
 def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> None:
     """Copy pages (the lists of PagePool.fork or compact, or any host lists)
     within a pool or between pools, converting between E4M3 and 4-bit pools.
@@ -973,14 +992,7 @@ def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> 
     if np.unique(dst).shape[0] != n:
         raise ValueError("a page is the destination of two copies")
     src_kind, dst_kind = _cache_kind(src_pool), _cache_kind(dst_pool)
-    # By address, as the pools may be views of one allocation: the destinations,
-    # which do not overlap each other, in order, and for each source the first
-    # that ends behind its start.
-    src_at = src_pool.data_ptr() + src.astype(np.int64) * _PAGE_BYTES[src_kind]
-    dst_at = np.sort(dst_pool.data_ptr() + dst.astype(np.int64) * _PAGE_BYTES[dst_kind])
-    first = np.searchsorted(dst_at + _PAGE_BYTES[dst_kind], src_at, side="right")
-    reach = first < n
-    if (dst_at[first[reach]] < src_at[reach] + _PAGE_BYTES[src_kind]).any():
+    if _pages_clash(src_pool.data_ptr(), src_kind, src, dst_pool.data_ptr(), dst_kind, dst):
         raise ValueError("a page is both a source and a destination")
     lists = [src, dst]
     if rows is not None:

@@ -4,7 +4,9 @@ they hand addresses to the library.
 Stand-ins of CUDA tensors: CPU tensors that report a device.  Every call here
 is refused, so no address of theirs is used."""
 import contextlib
+import random
 
+import numpy as np
 import pytest
 import torch
 
@@ -156,3 +158,19 @@ def test_page_copies_between_disjoint_parts_go_on(monkeypatch):
     mla.copy_pages(a, a, [1, 2], [3, 4])
     mla.copy_pages(a, On(big[100:], 0), [0, 99], [0, 99])
     assert len(went) == 4
+
+
+def test_clashes_against_a_plain_search():
+    rng = random.Random(3)
+    sizes = {mla.CACHE_FP8: 18432, mla.CACHE_FP4: 10752, mla.CACHE_BF16: 36864}
+    seen = set()
+    for _ in range(2000):
+        sk, dk = rng.choice(list(sizes)), rng.choice(list(sizes))
+        sa, da = (rng.choice([0, 16, 18432, 10752 * 3, 1 << 20, 16 * rng.randrange(30000)]) for _ in range(2))
+        src = np.array([rng.randrange(12) for _ in range(rng.randint(1, 5))], np.int32)
+        dst = np.array(rng.sample(range(12), len(src)), np.int32)
+        want = any(max(sa + int(i) * sizes[sk], da + int(j) * sizes[dk]) < min(sa + (int(i) + 1) * sizes[sk], da + (int(j) + 1) * sizes[dk])
+                   for i in src for j in dst)
+        assert mla._pages_clash(sa, sk, src, da, dk, dst) == want
+        seen.add(want)
+    assert seen == {True, False}
