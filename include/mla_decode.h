@@ -385,7 +385,8 @@ MLA_API int mla_decode_bf16_sparse(const void* q_bf16, const void* kv_pages_bf16
 /*
  * Decode over a 4-bit cache (MLA_CACHE_FP4), dense and over selected pages:
  * mla_decode_ex and mla_decode_sparse with kv_pages_fp4 uint8 [num_pages,
- * MLA_FP4_PAGE_BYTES], 16-byte aligned.  Q is E4M3; a key's values are kv_scale
+ * MLA_FP4_PAGE_BYTES], 16-byte aligned, num_pages below 2^26 (as for the E4M3
+ * pool; such a pool would be 721 GB).  Q is E4M3; a key's values are kv_scale
  * times those of its codes.  Plans, item lists, workspace, status, outputs and
  * options are as there, but persistent_ctas is MLA_ERR_UNSUPPORTED.  options
  * may be NULL.  Outputs are those of mla_decode over the E4M3 cache that the

@@ -13,8 +13,9 @@
 //
 // 2^(e - 8) * v is an E4M3 number for every e in 0..14 (the smallest step,
 // 2^-9, is E4M3's, and 6 * 2^6 = 384 <= 448), so a block expands to E4M3 codes
-// without any rounding: the decode's tensor-core path and every result over an
-// FP4 cache equal those over the E4M3 cache that it expands to.
+// without any rounding: the decode's operands, scores and weights over an FP4
+// cache are those over the E4M3 cache that it expands to (up to 16 rows the
+// row sums are added in another order, and differ by rounding).
 //
 // Bit layout of a 32-bit word (8 consecutive values, little endian): the low
 // three bits of nibble j are value j's magnitude code; the top bits of nibbles

@@ -2,17 +2,21 @@
 // mla_split_kv.cuh with expander warps in the place of the latent blocks' TMA
 // copies.  Every E2M1 value times its block's scale is an E4M3 number, so the
 // stages hold exactly the codes of the E4M3 cache that the 4-bit one stands
-// for, and scores, weights, partials and outputs are those of mla_decode over
-// it, bit for bit for the same plan and row groups.
+// for, and scores and weights are those of mla_decode over it for the same plan
+// and row groups.  From 17 rows on so are sums, partials and outputs, bit for
+// bit; up to 16 rows the row sums are added in another order (per thread, then
+// over the tokens), and they and what is divided by them differ by rounding.
 //
 // What it must move per key row: 336 bytes (256 codes, 16 scales, 64 rope)
 // instead of 576.  Measured (calls in a CUDA graph; in brackets the E4M3 decode on
-// values of the same distribution): H12 q1 B1 x 1M keys 98.6 us (103.8), B16 x
-// 128K 185 us (199), 256 selected pages of 16 requests 27.0 us (29.3), H24 q1 B4
-// x 128K 74.6 us (73.8), H12 q8 B16 x 128K 450 us (347).  The bytes alone would take 52.7 and 105 us in the first two: what
-// bounds them is shared memory's pipe, which the expansion's stores share with
-// the MMAs' operands (see the expander warps); from 48 rows on the softmax has
-// fewer registers than in the E4M3 kernel besides.
+// values of the same distribution): H12 q1 B1 x 1M keys 99.9 us (103.2), B16 x
+// 128K 186 us (198), 256 selected pages of 16 requests 27.2 us (29.3), H24 q1 B4
+// x 128K 74.1 us (73.1), H12 q8 B16 x 128K 451 us (347).  The bytes alone would
+// take 52.7 and 105 us in the first two: what bounds them is the data pipe of L1
+// and shared memory (see the expander warps), of which the codes' loads take
+// three times what their bytes need, because 8 lanes load 64 bytes of two rows
+// and not 128 of one; from 48 rows on the softmax has fewer registers than in
+// the E4M3 kernel besides.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -1137,9 +1137,11 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         // codes in registers and stores them where TMA's 128-byte swizzle would
         // have put an E4M3 cache's bytes.  Going through registers instead of a
         // staging buffer saves a write and a read of shared memory, whose
-        // pipe bounds the 16-row kernel: of the 3,780 cycles a tile took (under
+        // pipe bounds the 16-row kernel: of the 3,617 cycles a tile takes (under
         // ncu) the MMAs' operands fill 1,288, the loads, stores and barriers of
-        // all warps 1,862, and their conflicts 402.  Tried and slower: blocks of
+        // all warps 1,855, and their conflicts 397.  797 of the 1,855 are global
+        // loads, whose bytes need 272 (see the lanes' blocks below), 512 the
+        // expansion's stores.  Tried and slower: blocks of
         // 128 dims x 64 tokens handed to the QK warp one by one (101 -> 121 us
         // at B1 1M: 64-byte pieces of rows), expanding 8-token chunks before the
         // stage is free (109 us), the two shifts of fp4_expand8 as multiplies.

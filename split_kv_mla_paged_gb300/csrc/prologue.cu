@@ -275,8 +275,9 @@ __device__ __forceinline__ void query_rows(const PrologueParams& p, int64_t t, i
 }
 
 // Bound by the bytes read and written.  Six CTAs of four warps per SM (80
-// registers): 32,767 tokens of 12 heads into a BF16 cache 146.0 us (6.72 TB/s),
-// 8,192 tokens into an E4M3 cache 31.4 us; three of eight warps 147.8 and 32.0,
+// registers): 32,767 tokens of 12 heads into a BF16 cache 146.0 us (6.72 TB/s;
+// 146.6 on another GPU), 8,192 tokens into an E4M3 cache 31.4 us (32.1); on the
+// first GPU, three CTAs of eight warps took 147.8 and 32.0,
 // two of eight 168 and 35.5, four of eight (64 registers) 153.7 and 33.2 us.  One
 // row per warp took 265 and 51 us, its index and table loads one after the other.
 __global__ void __launch_bounds__(32 * kPrologueWarps, 6)
