@@ -733,7 +733,7 @@ class PagePool:
 
     def __init__(self, num_pages: int):
         self._lib = load_library()
-        self.num_pages = _host_int(num_pages, "num_pages", 64)
+        self.num_pages = _host_int(int(num_pages), "num_pages", 64)
         handle = ctypes.c_void_p()
         _check(self._lib.mla_pool_create(self.num_pages, ctypes.byref(handle)))
         self._handle = handle
