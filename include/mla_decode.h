@@ -415,6 +415,65 @@ MLA_API int mla_decode_fp4_sparse(const void* q_fp8, const void* kv_pages_fp4,
                                   void* out_bf16, float* lse_f32, float* out_f32_debug,
                                   const mla_decode_options_t* options, void* stream);
 
+/*
+ * Decode of requests that share prefixes (forks of mla_pool_fork, samples of one
+ * prompt, prompts behind one system text): the batch is divided into groups of
+ * consecutive requests, and the first prefix_lens[g] keys of group g's requests
+ * lie in the same pages (the first prefix_lens[g] / 32 entries of their page
+ * tables are equal; those of the group's first request are read).  They are read
+ * and attended once for all rows of the group; each request's remaining keys are
+ * attended by its own rows, and the merge joins both.  The result is mla_decode's
+ * on the same arguments, up to the order of its fp32 sums.
+ *
+ * Planner (host only):
+ * kv_lens        host int32[batch]: whole lengths, prefix included.
+ * group_offsets  host int32[groups + 1]: group g is requests [group_offsets[g],
+ *                group_offsets[g + 1]); starts at 0, ends at batch, ascends.
+ * prefix_lens    host int32[groups]: multiples of 32, 0 for a group that shares
+ *                nothing; kv_lens[b] - prefix_lens[g] >= q_len under causal (the
+ *                query block is the request's own), >= 0 otherwise.
+ * cache_kind     MLA_CACHE_FP8, MLA_CACHE_BF16 or MLA_CACHE_FP4.
+ * sm_count       SMs of the target GPU, >= 1.
+ * data_out       host int32[capacity] or NULL (then only *plan_out is set): the
+ *                plan's arrays, plan_out->data_len values, to be copied to the
+ *                device.
+ * The plan stays valid while each request's kv_len stays within its suffix's
+ * splits ((splits - 1) * chunk < kv_len - prefix <= splits * chunk, which the
+ * device checks): at least until the next multiple of 128 keys past the prefix.
+ */
+typedef struct {
+  int32_t cache_kind, batch, groups, q_len, num_heads, causal;
+  int32_t num_segments;
+  int32_t prefix_nr, suffix_nr;      /* rows of a CTA (MMA N) */
+  int32_t prefix_ctas, suffix_ctas;
+  int32_t prefix_slots, suffix_slots; /* partials per row */
+  int32_t kv_split;
+  int64_t data_len;
+  uint64_t workspace_bytes;
+} mla_shared_plan_t;
+
+MLA_API int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offsets,
+                            const int32_t* prefix_lens, int32_t batch, int32_t groups,
+                            int32_t num_heads, int32_t q_len, int32_t causal, int32_t cache_kind,
+                            int32_t sm_count, int32_t* data_out, int64_t capacity,
+                            mla_shared_plan_t* plan_out);
+
+/* The decode.  q and kv_pages in the plan's cache kind (E4M3 queries for the E4M3
+ * and 4-bit caches, BF16 for BF16, where q_scale and kv_scale are 1); plan_data the
+ * device copy of the plan's arrays, 16-byte aligned; workspace of at least
+ * plan->workspace_bytes; the other arguments, the options and the status word as
+ * for mla_decode_ex, but kv_bounds, cta_items, persistent_ctas and phases are
+ * MLA_ERR_UNSUPPORTED.  That the shared entries of the page tables are equal is
+ * the caller's promise: only the first request's are read. */
+MLA_API int mla_decode_shared(const void* q, const void* kv_pages, int64_t num_pages,
+                              const int32_t* page_table, int32_t max_pages_per_req,
+                              const int32_t* kv_lens, const mla_shared_plan_t* plan,
+                              const int32_t* plan_data, int32_t batch, int32_t q_len,
+                              int32_t num_heads, int32_t causal, float q_scale, float kv_scale,
+                              float softmax_scale, void* workspace, size_t workspace_bytes,
+                              void* out_bf16, float* lse_f32, float* out_f32_debug,
+                              const mla_decode_options_t* options, void* stream);
+
 /* Zero the 256-byte status header of a new workspace (async on `stream`).
  * Call once per workspace before its first mla_decode; after that the
  * header only changes when the device reports a condition, and

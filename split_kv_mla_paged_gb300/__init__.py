@@ -28,7 +28,8 @@ __all__ = [
     "mla_decode_bf16_sparse", "mla_decode_plan_items_bf16", "DecodeOptions",
     "decode", "merge", "MLA_ERR_NO_PAGES", "CACHE_FP8", "CACHE_BF16", "CACHE_FP4",
     "FP4_PAGE_BYTES", "mla_decode_fp4", "mla_decode_fp4_sparse", "PrologueArgs", "mla_prologue", "mla_pages_copy", "mla_pages_remap",
-    "PagePool", "copy_pages", "fp4_pool",
+    "PagePool", "copy_pages", "fp4_pool", "SharedPlan", "mla_shared_plan", "mla_decode_shared",
+    "shared_groups",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -54,7 +55,8 @@ EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_workspace_size", "mla_decode_
                     "mla_decode_fp4", "mla_decode_fp4_sparse",
                     "mla_pages_copy", "mla_pages_remap", "mla_pool_create", "mla_pool_destroy",
                     "mla_pool_free_pages", "mla_pool_references", "mla_pool_alloc",
-                    "mla_pool_release", "mla_pool_fork", "mla_pool_compact")
+                    "mla_pool_release", "mla_pool_fork", "mla_pool_compact", "mla_shared_plan",
+                    "mla_decode_shared")
 
 HEAD_DIM = 576
 LATENT_DIM = 512
@@ -94,6 +96,15 @@ class PrologueArgs(ctypes.Structure):
                 ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
                 ("q_out", ctypes.c_void_p), ("num_heads", ctypes.c_int32),
                 ("q_kind", ctypes.c_int32), ("status", ctypes.c_void_p)]
+
+
+class _SharedPlanInfo(ctypes.Structure):
+    """mla_shared_plan_t (include/mla_decode.h)."""
+    _fields_ = ([(name, ctypes.c_int32) for name in
+                 ("cache_kind", "batch", "groups", "q_len", "num_heads", "causal", "num_segments",
+                  "prefix_nr", "suffix_nr", "prefix_ctas", "suffix_ctas", "prefix_slots",
+                  "suffix_slots", "kv_split")]
+                + [("data_len", ctypes.c_int64), ("workspace_bytes", ctypes.c_uint64)])
 
 
 # mla_decode_options_t.phases: both phases, the split-KV kernel only, the merge only.
@@ -195,6 +206,13 @@ def load_library() -> ctypes.CDLL:
         lib.mla_pool_fork.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp]
         lib.mla_pool_compact.restype = ctypes.c_int
         lib.mla_pool_compact.argtypes = [vp, i64, vp, vp, vp, vp]
+        lib.mla_shared_plan.restype = ctypes.c_int
+        lib.mla_shared_plan.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, i64,
+                                        ctypes.POINTER(_SharedPlanInfo)]
+        lib.mla_decode_shared.restype = ctypes.c_int
+        lib.mla_decode_shared.argtypes = [vp, vp, i64, vp, i32, vp, ctypes.POINTER(_SharedPlanInfo),
+                                          vp, i32, i32, i32, i32, f32, f32, f32, vp, sz, vp, vp,
+                                          vp, ctypes.POINTER(DecodeOptions), vp]
         lib.mla_debug_set_wait_limit.restype = None
         lib.mla_debug_set_wait_limit.argtypes = [ctypes.c_longlong]
         lib.mla_debug_set_expire.restype = None
@@ -220,6 +238,8 @@ def _ptr(t) -> Optional[int]:
         return None
     if isinstance(t, np.ndarray):
         return t.ctypes.data
+    if isinstance(t, int):
+        return t
     return t.data_ptr()
 
 
@@ -605,6 +625,106 @@ def _call_on(index: int, fn, *args, stream=None) -> None:
             _check(fn(*args, handle))
 
 
+@dataclasses.dataclass
+class SharedPlan:
+    """A plan of mla_shared_plan: `data` goes to the device, `info` to the call."""
+    data: np.ndarray
+    info: _SharedPlanInfo
+
+    @property
+    def workspace_bytes(self) -> int:
+        return int(self.info.workspace_bytes)
+
+
+def mla_shared_plan(kv_lens, group_offsets, prefix_lens, num_heads: int, q_len: int, *,
+                    causal: bool = False, cache_kind: int = CACHE_FP8,
+                    sm_count: int = 152) -> SharedPlan:
+    """Plan a decode of requests in groups that share prefixes: group g is the
+    requests group_offsets[g] .. group_offsets[g + 1] - 1 and shares its first
+    prefix_lens[g] keys (a multiple of 32).  kv_lens are whole lengths."""
+    lens, offsets = _host_ids(kv_lens, "kv_lens"), _host_ids(group_offsets, "group_offsets")
+    prefixes = _host_ids(prefix_lens, "prefix_lens")
+    if offsets.shape[0] != prefixes.shape[0] + 1:
+        raise ValueError("group_offsets needs one entry more than prefix_lens")
+    lib = load_library()
+    info = _SharedPlanInfo()
+    args = (lens.ctypes.data, offsets.ctypes.data, prefixes.ctypes.data, lens.shape[0],
+            prefixes.shape[0], num_heads, q_len, 1 if causal else 0, cache_kind, sm_count)
+    _check(lib.mla_shared_plan(*args, None, 0, ctypes.byref(info)))
+    data = np.zeros(int(info.data_len), dtype=np.int32)
+    _check(lib.mla_shared_plan(*args, data.ctypes.data, data.shape[0], ctypes.byref(info)))
+    return SharedPlan(data=data, info=info)
+
+
+def mla_decode_shared(q, kv_pages, num_pages: int, page_table, max_pages_per_req: int, kv_lens,
+                      plan: SharedPlan, plan_data, batch: int, q_len: int, num_heads: int,
+                      causal: bool, q_scale: float, kv_scale: float, softmax_scale: float,
+                      workspace, workspace_bytes: int, out_bf16, lse_f32=None, out_f32_debug=None,
+                      *, q_scale_dev=None, kv_scale_dev=None, softmax_scale_dev=None,
+                      output_scale: float = 1.0, sinks=None, query_lens=None, stream=None) -> None:
+    """Decode requests that share prefixes, each prefix attended once for all rows
+    of its group; plan_data is the device copy of plan.data."""
+    import torch
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    kind = plan.info.cache_kind
+    dev = _device_of(q, "q")
+    rows = batch * q_len * num_heads
+    q_at = _device_tensor(q, "q", dev, None, rows * HEAD_DIM)
+    if q.element_size() != (2 if kind == CACHE_BF16 else 1):
+        raise ValueError("q must be BF16 for a BF16 cache, E4M3 otherwise")
+    if _cache_kind(kv_pages) != kind:
+        raise ValueError("kv_pages is not a pool of the plan's cache kind")
+    opts = _fp4_options(
+        _device_tensor(q_scale_dev, "q_scale_dev", dev, f32, 1),
+        _device_tensor(kv_scale_dev, "kv_scale_dev", dev, f32, 1),
+        _device_tensor(softmax_scale_dev, "softmax_scale_dev", dev, f32, 1), output_scale,
+        _device_tensor(sinks, "sinks", dev, f32, num_heads),
+        _device_tensor(query_lens, "query_lens", dev, i32, batch), None, None, PHASE_ALL)
+    _call_on(dev, load_library().mla_decode_shared, q_at,
+             _device_pool(kv_pages, "kv_pages", dev, num_pages, kind), num_pages,
+             _device_tensor(page_table, "page_table", dev, i32, batch * max_pages_per_req),
+             max_pages_per_req, _device_tensor(kv_lens, "kv_lens", dev, i32, batch),
+             ctypes.byref(plan.info),
+             _device_tensor(plan_data, "plan_data", dev, i32, plan.info.data_len), batch, q_len,
+             num_heads, 1 if causal else 0, q_scale, kv_scale, softmax_scale,
+             _device_tensor(workspace, "workspace", dev, torch.uint8, workspace_bytes),
+             workspace_bytes, _device_tensor(out_bf16, "out_bf16", dev, bf16, rows * LATENT_DIM),
+             _device_tensor(lse_f32, "lse_f32", dev, f32, rows),
+             _device_tensor(out_f32_debug, "out_f32_debug", dev, f32, rows * LATENT_DIM), opts,
+             stream=stream)
+
+
+def shared_groups(page_lists, kv_lens, q_len: int = 1, least: int = PAGE_SIZE):
+    """Groups of consecutive requests whose page lists begin with the same pages,
+    for mla_shared_plan: (group_offsets, prefix_lens).  A request joins the group
+    before it while at least `least` keys stay shared; the keys of the last q_len
+    positions are never shared."""
+    lens = _host_ids(kv_lens, "kv_lens")
+    lists = [_host_ids(p, "page_lists") for p in page_lists]
+    if len(lists) != lens.shape[0]:
+        raise ValueError("page_lists and kv_lens must have the same length")
+    offsets, prefixes = [0], []
+    for b in range(1, lens.shape[0] + 1):
+        start = offsets[-1]
+        if b < lens.shape[0]:
+            room = max(0, int(min(lens[start:b + 1].min(), lens[b])) - q_len) // PAGE_SIZE
+            if b - start > 1:
+                room = min(room, prefixes[-1] // PAGE_SIZE)
+            room = min(room, lists[start].shape[0], lists[b].shape[0])
+            same = lists[start][:room] == lists[b][:room]
+            pages = room if bool(same.all()) else int(np.argmin(same))
+            if pages * PAGE_SIZE >= max(least, PAGE_SIZE):
+                if b - start > 1:
+                    prefixes[-1] = pages * PAGE_SIZE
+                else:
+                    prefixes.append(pages * PAGE_SIZE)
+                continue
+        if b - start == 1:
+            prefixes.append(0)
+        offsets.append(b)
+    return np.asarray(offsets, dtype=np.int32), np.asarray(prefixes, dtype=np.int32)
+
+
 def _row_stride(t, dim: int, name: str) -> int:
     """Stride of a dimension, which the C structure's 0 (contiguous) cannot carry."""
     stride = t.stride(dim)
@@ -823,7 +943,8 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
            kv_split: Optional[int] = None, want_f32: bool = False, stream=None,
            check_status: bool = True, sinks=None, output_scale: float = 1.0,
            device_scales: bool = False, query_lens=None, kv_bounds=None, block_idx=None,
-           use_items: Optional[bool] = None, persistent_ctas: int = 0):
+           use_items: Optional[bool] = None, persistent_ctas: int = 0, group_offsets=None,
+           prefix_lens=None):
     """Plan, allocate outputs and a workspace with torch, and run mla_decode.
 
     q_fp8 uint8 [B, q, H, 576] and kv_pages_fp8 uint8 [P, 32, 576] (E4M3 codes)
@@ -835,13 +956,25 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
     planned on the compact lengths) restrict the visible keys.  use_items
     (default: when the plan has empty split slots) launches the split kernel
     over the plan's CTA item list; persistent_ctas > 0 (FP8) runs that list
-    with that many persistent CTAs.  Returns (out_bf16, lse, out_f32 or None).
+    with that many persistent CTAs.  group_offsets and prefix_lens (shared_groups)
+    run mla_decode_shared, every group's prefix attended once.  Returns (out_bf16, lse, out_f32 or None).
     """
     import torch
     dev = q_fp8.device
     lens = np.asarray(kv_lens.cpu() if hasattr(kv_lens, "cpu") else kv_lens, dtype=np.int32)
     batch = int(lens.shape[0])
     topk = 0 if block_idx is None else int(block_idx.shape[1])
+    if (group_offsets is None) != (prefix_lens is None):
+        raise ValueError("group_offsets and prefix_lens go together")
+    if group_offsets is not None:
+        if (plan is not None or target_ctas or kv_split is not None or kv_bounds is not None
+                or block_idx is not None or use_items or persistent_ctas):
+            raise ValueError("a decode over shared prefixes has its own plan, and no key windows, "
+                             "page selections, item lists or persistent CTAs")
+        return _decode_shared(q_fp8, kv_pages_fp8, page_table, lens, group_offsets, prefix_lens,
+                              num_heads, q_len, causal, softmax_scale, q_scale, kv_scale, sm_count,
+                              want_f32, stream, check_status, sinks, output_scale, device_scales,
+                              query_lens)
     if plan is None:
         if sm_count is None:
             sm_count = torch.cuda.get_device_properties(dev).multi_processor_count
@@ -930,6 +1063,42 @@ def decode(q_fp8, kv_pages_fp8, page_table, kv_lens, *, num_heads: int, q_len: i
         else:
             mla_decode_sparse(*common[:6], bi_d, topk, *common[6:], *host, ws, ws_bytes, out,
                               lse, out_f32, **extra)
+    if check_status:
+        mla_decode_status(ws, stream)
+    return out, lse, out_f32
+
+
+def _decode_shared(q, kv_pages, page_table, lens, group_offsets, prefix_lens, num_heads, q_len,
+                   causal, softmax_scale, q_scale, kv_scale, sm_count, want_f32, stream,
+                   check_status, sinks, output_scale, device_scales, query_lens):
+    """decode() over shared prefixes."""
+    import torch
+    dev, batch = q.device, lens.shape[0]
+    kind = _cache_kind(kv_pages)
+    if sm_count is None:
+        sm_count = torch.cuda.get_device_properties(dev).multi_processor_count
+    plan = mla_shared_plan(lens, group_offsets, prefix_lens, num_heads, q_len, causal=causal,
+                           cache_kind=kind, sm_count=sm_count)
+    lens_d, plan_d = torch.from_numpy(lens).to(dev), torch.from_numpy(plan.data).to(dev)
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dev)
+    mla_decode_workspace_init(ws, plan.workspace_bytes, stream)
+    out = torch.empty((batch, q_len, num_heads, LATENT_DIM), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((batch, q_len, num_heads), dtype=torch.float32, device=dev)
+    out_f32 = torch.empty(out.shape, dtype=torch.float32, device=dev) if want_f32 else None
+    scales, host = [None] * 3, (q_scale, kv_scale, softmax_scale)
+    if device_scales:
+        one = torch.tensor(host, dtype=torch.float32, device=dev)
+        scales = [None if kind == CACHE_BF16 and i < 2 else one[i:i + 1] for i in range(3)]
+        if kind != CACHE_BF16:
+            host = (99.0,) * 3
+    extra = dict(zip(("q_scale_dev", "kv_scale_dev", "softmax_scale_dev"), scales))
+    if sinks is not None:
+        extra["sinks"] = torch.as_tensor(sinks, dtype=torch.float32).to(dev)
+    if query_lens is not None:
+        extra["query_lens"] = torch.as_tensor(query_lens, dtype=torch.int32).to(dev).contiguous()
+    mla_decode_shared(q, kv_pages, kv_pages.shape[0], page_table, page_table.shape[1], lens_d, plan,
+                      plan_d, batch, q_len, num_heads, causal, *host, ws, plan.workspace_bytes, out,
+                      lse, out_f32, output_scale=output_scale, stream=stream, **extra)
     if check_status:
         mla_decode_status(ws, stream)
     return out, lse, out_f32

@@ -11,6 +11,7 @@ LIB_NAME = "libmla_decode.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = [os.path.join(CSRC, "mla_decode.cu"), os.path.join(CSRC, "mla_decode_bf16.cu"),
            os.path.join(CSRC, "mla_decode_fp4.cu"),
+           os.path.join(CSRC, "mla_shared.cu"), os.path.join(CSRC, "mla_shared_fp4.cu"),
            os.path.join(CSRC, "mla_merge.cu"), os.path.join(CSRC, "kv_append.cu"),
            os.path.join(CSRC, "prologue.cu"), os.path.join(CSRC, "pages.cu"),
            os.path.join(CSRC, "page_pool.cpp"), os.path.join(CSRC, "plan.cpp")]

@@ -190,6 +190,10 @@ int prepare_decode(const void* q_fp8, const void* kv_pages_fp8, int64_t num_page
   prm.lse = lse_f32;
   prm.out_f32 = out_f32_debug;
   prm.kv_fp4 = nullptr;
+  prm.segs = nullptr;
+  prm.num_segs = 0;
+  prm.suffix_slot = 0;
+  prm.chain = 0;
   MergeParams& mp = dl->mp;
   mp.po = prm.ws_o;
   mp.pml = prm.ws_ml;
@@ -204,6 +208,9 @@ int prepare_decode(const void* q_fp8, const void* kv_pages_fp8, int64_t num_page
   mp.out = prm.out;
   mp.lse = lse_f32;
   mp.out_f32 = out_f32_debug;
+  mp.shared_slots = nullptr;
+  mp.suffix_slot = 0;
+  mp.query_lens = nullptr;
   return MLA_OK;
 }
 
@@ -567,7 +574,7 @@ extern "C" int mla_merge(const float* partial_o, const float* partial_ml, int32_
     set_error("mla_merge: partial_o/out_f32 need 16-byte, partial_ml/out 8-byte alignment");
     return MLA_ERR_INVALID_ARG;
   }
-  MergeParams mp;
+  MergeParams mp = {};
   mp.po = partial_o;
   mp.pml = partial_ml;
   mp.rows = rows;

@@ -152,7 +152,55 @@ __device__ __forceinline__ bool cta_coords(const DecodeParams& p, int ngroups, i
 struct SplitRange {
   int L, nsplit, q_b, tok_begin, tok_end, t0, win_lo, win_hi;
   bool sparse;
+  // The rows' place in the batch and in their request, the page table from the
+  // range's key 0 on, the partials' slot.
+  int row_at, row0, rows_here, rows_valid, slot;
+  const int32_t* table;
 };
+
+// A split of a segment of a decode over shared prefixes, as item_segment of the
+// E4M3 kernel: keys count from the segment's first one.
+__device__ __forceinline__ bool segment_range(const DecodeParams& p, SplitRange& r) {
+  const int entry = p.cta_items[blockIdx.x];
+  const int seg = entry >> MLA_ITEM_B_SHIFT;
+  const int split =
+      (entry >> MLA_ITEM_S_SHIFT) & ((1 << (MLA_ITEM_B_SHIFT - MLA_ITEM_S_SHIFT)) - 1);
+  if (entry < 0 || seg >= p.num_segs) {
+    if (threadIdx.x == 0) report(p.status, MLA_ERR_INVALID_ARG);
+    return false;
+  }
+  const int4 a = reinterpret_cast<const int4*>(p.segs + seg)[0];
+  const int4 c = reinterpret_cast<const int4*>(p.segs + seg)[1];
+  const Segment s{a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  const bool suffix = s.len < 0;
+  r.q_b = suffix && p.query_lens ? p.query_lens[s.request] : p.q_len;
+  const int len = suffix ? p.kv_lens[s.request] - s.key0 : s.len;
+  const bool bad = len < 0 || r.q_b < 1 || r.q_b > p.q_len ||
+                   (suffix && p.causal && len < r.q_b) || split >= s.splits ||
+                   s.chunk < MLA_TILE_TOKENS || (s.chunk % MLA_TILE_TOKENS) != 0 ||
+                   static_cast<int64_t>(s.splits) * s.chunk < len ||
+                   (s.splits > 1 && static_cast<int64_t>(s.splits - 1) * s.chunk >= len) ||
+                   static_cast<int64_t>(s.key0) + len >
+                       static_cast<int64_t>(p.max_pages) * MLA_PAGE_SIZE;
+  if (bad) {
+    if (threadIdx.x == 0) report(p.status, MLA_ERR_INVALID_ARG);
+    return false;
+  }
+  r.nsplit = s.splits;
+  r.L = suffix ? len : len + r.q_b;
+  r.t0 = r.tok_begin = split * s.chunk;
+  r.tok_end = min(len, r.tok_begin + s.chunk);
+  r.win_lo = 0;
+  r.win_hi = r.L;
+  r.sparse = false;
+  r.row0 = s.row_in_req;
+  r.row_at = s.first_row - s.row_in_req;
+  r.rows_here = s.n_rows;
+  r.rows_valid = suffix ? max(0, min(s.n_rows, r.q_b * p.num_heads - s.row_in_req)) : s.n_rows;
+  r.slot = split + (suffix ? p.suffix_slot : 0);
+  r.table = p.page_table + static_cast<int64_t>(s.request) * p.max_pages + s.key0 / MLA_PAGE_SIZE;
+  return true;
+}
 
 template <bool kGather, int kTile = kTokB>
 __device__ __forceinline__ bool split_range(const DecodeParams& p, int b, int split,
@@ -286,26 +334,39 @@ constexpr int BAR_ODONE_0 = BAR_ODONE;
 constexpr int BAR_ODONE_1 = BAR_PFREE1;
 }  // namespace q16
 
-template <bool kGather, bool kItems>
+template <bool kGather, bool kItems, bool kShared = false>
 __global__ void __launch_bounds__(q16::kThreads, 1)
     mla_split_kv_bf16_q16_kernel(const __grid_constant__ CUtensorMap tm_kv,
                                  const __grid_constant__ CUtensorMap tm_q, const DecodeParams p) {
   using namespace q16;
-  const int ngroups = (p.rows_per_req + p.rows_per_group - 1) / p.rows_per_group;
-  int b, split, grp;
-  if (!cta_coords<kItems>(p, ngroups, b, split, grp)) return;
-  if (split >= p.splits[b]) return;  // empty split slot of a shorter request
   SplitRange sr;
-  if (!split_range<kGather>(p, b, split, sr)) return;
+  int b = 0;
+  if constexpr (kShared) {
+    if (p.chain & SHARED_RELEASE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!segment_range(p, sr)) {
+      if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
+      return;
+    }
+  } else {
+    const int ngroups = (p.rows_per_req + p.rows_per_group - 1) / p.rows_per_group;
+    int split, grp;
+    if (!cta_coords<kItems>(p, ngroups, b, split, grp)) return;
+    if (split >= p.splits[b]) return;  // empty split slot of a shorter request
+    if (!split_range<kGather>(p, b, split, sr)) return;
+    sr.row_at = b * p.rows_per_req;
+    sr.row0 = grp * p.rows_per_group;
+    sr.rows_here = min(p.rows_per_group, p.rows_per_req - sr.row0);
+    // Rows of real query tokens (the others are padding slots of a shorter
+    // query block: no key is visible to them).
+    sr.rows_valid = max(0, min(sr.rows_here, sr.q_b * p.num_heads - sr.row0));
+    sr.slot = split;
+    sr.table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+  }
   const int L = sr.L, nsplit = sr.nsplit, q_b = sr.q_b, tok_end = sr.tok_end, t0 = sr.t0;
   const bool sparse = sr.sparse;
   const float c_log2 =
       p.sm_scale_dev ? *p.sm_scale_dev * 1.4426950408889634f : p.c_log2;
-  const int row0 = grp * p.rows_per_group;
-  const int rows_here = min(p.rows_per_group, p.rows_per_req - row0);
-  // Rows of real query tokens (the others are padding slots of a shorter
-  // query block: no key is visible to them).
-  const int rows_valid = max(0, min(rows_here, q_b * p.num_heads - row0));
+  const int row0 = sr.row0, rows_here = sr.rows_here, rows_valid = sr.rows_valid;
   const int n_tiles =
       (rows_valid > 0 && tok_end > t0) ? (tok_end - t0 + kTokB - 1) / kTokB : 0;
 
@@ -359,14 +420,14 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tm_kv);
       tma_prefetch_desc(&tm_q);
-      const int qrow = b * p.rows_per_req + row0;
+      const int qrow = sr.row_at + row0;
       mbar_arrive_expect_tx(bar(BAR_QFULL), NR * kRowBytesB);
 #pragma unroll
       for (int d = 0; d < 9; ++d)
         tma_load_2d(sbase + kQStage + d * NR * 128, &tm_q, d * 64, qrow, bar(BAR_QFULL));
     }
     const uint64_t pol = l2_policy_evict_first();
-    const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+    const int32_t* pt = sr.table;
     const int page0 = t0 / MLA_PAGE_SIZE;
     const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;
     int last_lp = -1;
@@ -717,7 +778,7 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
     }
     // ---- epilogue ----
     named_bar_sync(kSoftmaxBarrier, 128);
-    const bool single = (nsplit == 1);
+    const bool single = !kShared && nsplit == 1;
     float* scale_s = alpha_s;
     if (sid < NR) {
       if (n_tiles > 0) {
@@ -725,7 +786,7 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
         l_row += (rs[sid] + rs[16 + sid]) + (rs[32 + sid] + rs[48 + sid]);
       }
       const float m_s = (k_row == -INFINITY) ? -INFINITY : k_row - 8.0f;
-      const int64_t grow = static_cast<int64_t>(b) * p.rows_per_req + row0 + sid;
+      const int64_t grow = static_cast<int64_t>(sr.row_at) + row0 + sid;
       float sc = 0.0f;
       if (sid < rows_here) {
         if (single) {
@@ -740,7 +801,7 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
             p.lse[grow] = (den > 0.0f) ? 0.6931471805599453f * (mm + log2f(den)) : -INFINITY;
           sc = (den > 0.0f) ? p.output_scale * a / den : 0.0f;
         } else {
-          float* ml = p.ws_ml + (grow * p.max_splits + split) * 2;
+          float* ml = p.ws_ml + (grow * p.max_splits + sr.slot) * 2;
           ml[0] = m_s;
           ml[1] = l_row;
           sc = 1.0f;
@@ -768,12 +829,12 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
         for (int k = 0; k < 16; ++k) {
           if (k < rows_here) {
             const float v = __uint_as_float(r[k]) * sc_r[k];
-            const int64_t grow = static_cast<int64_t>(b) * p.rows_per_req + row0 + k;
+            const int64_t grow = static_cast<int64_t>(sr.row_at) + row0 + k;
             if (single) {
               p.out[grow * MLA_LATENT_DIM + dim] = __float2bfloat16_rn(v);
               if (p.out_f32) p.out_f32[grow * MLA_LATENT_DIM + dim] = v;
             } else {
-              p.ws_o[(grow * p.max_splits + split) * MLA_LATENT_DIM + dim] = v;
+              p.ws_o[(grow * p.max_splits + sr.slot) * MLA_LATENT_DIM + dim] = v;
             }
           }
         }
@@ -783,7 +844,7 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
       for (int d = 0; d < 4; ++d) {
         const int dim = d * 128 + lidx;
         for (int k = 0; k < rows_here; ++k) {
-          const int64_t grow = static_cast<int64_t>(b) * p.rows_per_req + row0 + k;
+          const int64_t grow = static_cast<int64_t>(sr.row_at) + row0 + k;
           p.out[grow * MLA_LATENT_DIM + dim] = __float2bfloat16_rn(0.0f);
           if (p.out_f32) p.out_f32[grow * MLA_LATENT_DIM + dim] = 0.0f;
         }
@@ -796,7 +857,12 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Shared prefixes: as in the E4M3 kernel.
+  if (!kShared || !(p.chain & SHARED_RELEASE))
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (kShared) {
+    if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -892,27 +958,40 @@ __device__ __forceinline__ void zero_unloaded_rows_w(uint8_t* kvp, int lane, uin
   }
 }
 
-template <int NR, bool kGather, bool kItems>
+template <int NR, bool kGather, bool kItems, bool kShared = false>
 __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
     mla_split_kv_bf16_wide_kernel(const __grid_constant__ CUtensorMap tm_kv,
                                   const __grid_constant__ CUtensorMap tm_q, const DecodeParams p) {
   using C = CfgW<NR>;
   using bw::kTok;
-  const int ngroups = (p.rows_per_req + p.rows_per_group - 1) / p.rows_per_group;
-  int b, split, grp;
-  if (!cta_coords<kItems>(p, ngroups, b, split, grp)) return;
-  if (split >= p.splits[b]) return;  // empty split slot of a shorter request
   SplitRange sr;
-  if (!split_range<kGather, kTok>(p, b, split, sr)) return;
+  int b = 0;
+  if constexpr (kShared) {
+    if (p.chain & SHARED_RELEASE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!segment_range(p, sr)) {
+      if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
+      return;
+    }
+  } else {
+    const int ngroups = (p.rows_per_req + p.rows_per_group - 1) / p.rows_per_group;
+    int split, grp;
+    if (!cta_coords<kItems>(p, ngroups, b, split, grp)) return;
+    if (split >= p.splits[b]) return;  // empty split slot of a shorter request
+    if (!split_range<kGather, kTok>(p, b, split, sr)) return;
+    sr.row_at = b * p.rows_per_req;
+    sr.row0 = grp * p.rows_per_group;
+    sr.rows_here = min(p.rows_per_group, p.rows_per_req - sr.row0);
+    // Rows of real query tokens (the others are padding slots of a shorter
+    // query block: no key is visible to them).
+    sr.rows_valid = max(0, min(sr.rows_here, sr.q_b * p.num_heads - sr.row0));
+    sr.slot = split;
+    sr.table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+  }
   const int L = sr.L, nsplit = sr.nsplit, q_b = sr.q_b, tok_end = sr.tok_end, t0 = sr.t0;
   const bool sparse = sr.sparse;
   const float c_log2 =
       p.sm_scale_dev ? *p.sm_scale_dev * 1.4426950408889634f : p.c_log2;
-  const int row0 = grp * p.rows_per_group;
-  const int rows_here = min(p.rows_per_group, p.rows_per_req - row0);
-  // Rows of real query tokens (the others are padding slots of a shorter
-  // query block: no key is visible to them).
-  const int rows_valid = max(0, min(rows_here, q_b * p.num_heads - row0));
+  const int row0 = sr.row0, rows_here = sr.rows_here, rows_valid = sr.rows_valid;
   const int n_tiles =
       (rows_valid > 0 && tok_end > t0) ? (tok_end - t0 + kTok - 1) / kTok : 0;
 
@@ -970,14 +1049,14 @@ __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tm_kv);
       tma_prefetch_desc(&tm_q);
-      const int qrow = b * p.rows_per_req + row0;
+      const int qrow = sr.row_at + row0;
       mbar_arrive_expect_tx(bar(BAR_QFULL), C::kQBytes);
 #pragma unroll
       for (int d = 0; d < 9; ++d)
         tma_load_2d(sbase + C::kQ + d * NR * 128, &tm_q, d * 64, qrow, bar(BAR_QFULL));
     }
     const uint64_t pol = l2_policy_evict_first();
-    const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+    const int32_t* pt = sr.table;
     const int page0 = t0 / MLA_PAGE_SIZE;
     const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;  // exclusive
     // Page ids of 8 tiles (32 pages) per window, one per lane, fetched a
@@ -1389,7 +1468,7 @@ __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
     }
     // ---- epilogue (as in the FP8 kernel; O^T has NR columns per group) ----
     named_bar_sync(kSoftmaxBarrier, NT);
-    const bool single = (nsplit == 1);
+    const bool single = !kShared && nsplit == 1;
     float* scale_s = alpha_s;
     if (sid < NR) {
       if (n_tiles > 0) {
@@ -1397,7 +1476,7 @@ __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
         l_row += (rs[sid] + rs[NR + sid]) + (rs[2 * NR + sid] + rs[3 * NR + sid]);
       }
       const float m_s = (k_row == -INFINITY) ? -INFINITY : k_row - 8.0f;
-      const int64_t grow = static_cast<int64_t>(b) * p.rows_per_req + row0 + sid;
+      const int64_t grow = static_cast<int64_t>(sr.row_at) + row0 + sid;
       float sc = 0.0f;
       if (sid < rows_here) {
         if (single) {
@@ -1412,7 +1491,7 @@ __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
             p.lse[grow] = (den > 0.0f) ? 0.6931471805599453f * (mm + log2f(den)) : -INFINITY;
           sc = (den > 0.0f) ? p.output_scale * a / den : 0.0f;
         } else {
-          float* ml = p.ws_ml + (grow * p.max_splits + split) * 2;
+          float* ml = p.ws_ml + (grow * p.max_splits + sr.slot) * 2;
           ml[0] = m_s;
           ml[1] = l_row;
           sc = 1.0f;
@@ -1428,11 +1507,11 @@ __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
       tc_fence_after();
       // Per latent group: this warpgroup's NRH columns in one batch of TMEM
       // loads, then the stores (row k of the warpgroup at base + k * stride).
-      const int64_t grow0 = static_cast<int64_t>(b) * p.rows_per_req + row0 + rbase;
+      const int64_t grow0 = static_cast<int64_t>(sr.row_at) + row0 + rbase;
       const int64_t stride = single ? MLA_LATENT_DIM
                                     : static_cast<int64_t>(p.max_splits) * MLA_LATENT_DIM;
       float* const obase =
-          single ? nullptr : p.ws_o + (grow0 * p.max_splits + split) * MLA_LATENT_DIM;
+          single ? nullptr : p.ws_o + (grow0 * p.max_splits + sr.slot) * MLA_LATENT_DIM;
       const int nrow = min(NRH, rows_here - rbase);
       // Each warp turns its 32 dims x 8 rows at a time around through 1 KB of
       // the P^T buffers (free after the last PV), so that a lane stores 4
@@ -1487,7 +1566,7 @@ __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
       for (int d = 0; d < 4; ++d) {
         const int dim = d * 128 + tok;
         for (int row = rbase; row < min(rows_here, rbase + NRH); ++row) {
-          const int64_t grow = static_cast<int64_t>(b) * p.rows_per_req + row0 + row;
+          const int64_t grow = static_cast<int64_t>(sr.row_at) + row0 + row;
           p.out[grow * MLA_LATENT_DIM + dim] = __float2bfloat16_rn(0.0f);
           if (p.out_f32) p.out_f32[grow * MLA_LATENT_DIM + dim] = 0.0f;
         }
@@ -1500,7 +1579,12 @@ __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Shared prefixes: as in the E4M3 kernel.
+  if (!kShared || !(p.chain & SHARED_RELEASE))
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (kShared) {
+    if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
 }
 
 // 2-D BF16 view [rows, 576] with a (64, box_y) box, 128-byte swizzle.
@@ -1588,6 +1672,56 @@ static cudaError_t launch_split_bf16(const void* q, const void* kv, int64_t num_
                                                            num_ctas, prm, stream)
                  : launch_split_bf16_w_t<NR, false, false>(q, kv, num_pages, batch, groups,
                                                             num_ctas, prm, stream);
+  }
+}
+
+// The segments of a decode over shared prefixes: num_ctas items of prm.cta_items.
+template <typename Kernel>
+static cudaError_t launch_shared_bf16_t(Kernel kernel, int nr, int threads, uint32_t smem,
+                                        std::atomic<uint64_t>& attr_done, const void* q,
+                                        const void* kv, int64_t rows, int num_ctas,
+                                        const DecodeParams& prm, cudaStream_t stream) {
+  cudaError_t e = ensure_smem_attr(kernel, static_cast<int>(smem), attr_done);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tm_kv, tm_q;
+  if (!make_map_bf16(&tm_kv, kv, static_cast<uint64_t>(prm.num_pages) * MLA_PAGE_SIZE,
+                     MLA_PAGE_SIZE) ||
+      !make_map_bf16(&tm_q, q, static_cast<uint64_t>(rows), nr))
+    return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = (prm.chain & SHARED_JOIN) ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, tm_kv, tm_q, prm);
+}
+
+template <int NR>
+static cudaError_t launch_shared_bf16_w(const void* q, const void* kv, int64_t rows, int num_ctas,
+                                        const DecodeParams& prm, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};
+  return launch_shared_bf16_t(mla_split_kv_bf16_wide_kernel<NR, false, true, true>, NR,
+                              CfgW<NR>::kThreads, CfgW<NR>::kSmemBytes, attr_done, q, kv, rows,
+                              num_ctas, prm, stream);
+}
+
+cudaError_t launch_shared_bf16(int nr, const void* q, const void* kv, int64_t rows, int num_ctas,
+                               const DecodeParams& prm, cudaStream_t stream) {
+  switch (nr) {
+    case 16: {
+      static std::atomic<uint64_t> attr_done{0};
+      return launch_shared_bf16_t(mla_split_kv_bf16_q16_kernel<false, true, true>, q16::NR,
+                                  q16::kThreads, q16::kSmemBytes, attr_done, q, kv, rows,
+                                  num_ctas, prm, stream);
+    }
+    case 32: return launch_shared_bf16_w<32>(q, kv, rows, num_ctas, prm, stream);
+    case 48: return launch_shared_bf16_w<48>(q, kv, rows, num_ctas, prm, stream);
+    default: return cudaErrorInvalidValue;
   }
 }
 

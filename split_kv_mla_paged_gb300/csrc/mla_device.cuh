@@ -22,6 +22,22 @@ constexpr uint32_t kVoteBarrier = 2;
 constexpr uint32_t kVoteBarrierWg0 = 3;
 constexpr uint32_t kSoftmaxBarrierWg0 = 6;
 
+// One segment of a decode over shared prefixes (the plan's records): rows
+// [first_row, first_row + n_rows) of the batch's rows attend keys [key0, key0 +
+// len) of request `request`'s pages, in `splits` splits of `chunk` keys.
+struct Segment {
+  int32_t first_row, n_rows;
+  int32_t row_in_req;  // first_row's index within its request (suffixes; 0 for a prefix)
+  int32_t request;     // whose page table is read (a prefix: its group's first request)
+  int32_t key0;        // a multiple of the page size
+  int32_t len;         // a prefix: its keys; -1: a suffix, up to the request's kv_len
+  int32_t splits, chunk;
+};
+static_assert(sizeof(Segment) == 32, "two 16-byte loads");
+// DecodeParams::chain: the next launch may start once every CTA of this one has
+// (prefixes); this launch ends no earlier than the one before it (suffixes).
+constexpr int SHARED_RELEASE = 1, SHARED_JOIN = 2;
+
 struct DecodeParams {
   const int32_t* page_table;
   const int32_t* kv_lens;
@@ -71,6 +87,13 @@ struct DecodeParams {
   float* lse;
   float* out_f32;
   const uint8_t* kv_fp4;   // 4-bit page pool (mla_decode_fp4 only)
+  // Decode over shared prefixes (mla_decode_shared only): the plan's segments,
+  // the slot of a suffix segment's first partial, and what the launch does for
+  // its neighbours on the stream (SHARED_*).
+  const Segment* segs;
+  int32_t num_segs;
+  int32_t suffix_slot;
+  int32_t chain;
 };
 
 // Barrier indices inside the aux block.  The BF16 kernels use the first 17;
@@ -334,6 +357,12 @@ struct MergeParams {
   __nv_bfloat16* out;
   float* lse;
   float* out_f32;
+  // Decode over shared prefixes: per request the slots of its group's prefix
+  // (from slot 0) and of its own suffix (from suffix_slot); query_lens as in
+  // DecodeParams (rows of other query slots are empty whatever their slots hold).
+  const int2* shared_slots;
+  int32_t suffix_slot;
+  const int32_t* query_lens;
 };
 
 // Raise a kernel's dynamic shared-memory limit to `bytes` once per device
@@ -352,6 +381,16 @@ inline cudaError_t ensure_smem_attr(Kernel fn, int bytes, std::atomic<uint64_t>&
 
 // Launches the merge as a programmatic dependent of the preceding grid.
 cudaError_t launch_merge(const MergeParams& mp, int kv_split, cudaStream_t stream);
+// The merge of a decode over shared prefixes, after its segments' launches.
+cudaError_t launch_merge_shared(const MergeParams& mp, int kv_split, cudaStream_t stream);
+// A decode over shared prefixes: one launch of the segments' kernel with nr rows a
+// CTA, over the `num_ctas` items of prm.cta_items; `rows` is the batch's.
+cudaError_t launch_shared_fp8(int nr, const void* q, const void* kv, int64_t rows, int num_ctas,
+                              const DecodeParams& prm, cudaStream_t stream);
+cudaError_t launch_shared_fp4(int nr, const void* q, const void* kv, int64_t rows, int num_ctas,
+                              const DecodeParams& prm, cudaStream_t stream);
+cudaError_t launch_shared_bf16(int nr, const void* q, const void* kv, int64_t rows, int num_ctas,
+                               const DecodeParams& prm, cudaStream_t stream);
 // cuTensorMapEncodeTiled through the runtime's driver entry point.
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 bool aligned(const void* p, uintptr_t a);

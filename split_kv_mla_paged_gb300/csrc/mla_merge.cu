@@ -25,7 +25,7 @@ namespace mla {
 // every rescale there is an exact power of two for the split kernel's
 // integer maxima); it pays one more round trip per group and serves rows
 // whose groups hold many slots.
-template <int G, int U, bool kMaxFirst>
+template <int G, int U, bool kMaxFirst, bool kShared = false>
 __device__ __forceinline__ void merge_body(const MergeParams& p) {
   __shared__ float sm_m[G];
   __shared__ float sm_l[G];
@@ -37,19 +37,31 @@ __device__ __forceinline__ void merge_body(const MergeParams& p) {
   const int g = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   int ns = p.uniform_s;
-  if (p.splits) {
+  // kShared: the row's slots are its group's prefix splits, then from suffix_slot
+  // on its own; a padding query slot's row takes none of them.
+  int n_prefix = 0;
+  if constexpr (kShared) {
+    const int b = row / p.rows_per_req;
+    const int2 n = p.shared_slots[b];
+    n_prefix = n.x;
+    ns = n.x + n.y;
+    if (p.query_lens && (row - b * p.rows_per_req) / p.num_heads >= p.query_lens[b]) ns = 0;
+  } else if (p.splits) {
     ns = min(p.splits[row / p.rows_per_req], p.stride_s);
     if (ns <= 1) return;  // the split kernel wrote this row directly
   }
   const int dim = quarter * 128 + lane * 4;
   const float* pml = p.pml + static_cast<int64_t>(row) * p.stride_s * 2;
   const float* po = p.po + static_cast<int64_t>(row) * p.stride_s * MLA_LATENT_DIM + dim;
+  auto slot_of = [&](int s) -> int {
+    return kShared && s >= n_prefix ? s - n_prefix + p.suffix_slot : s;
+  };
   float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   if constexpr (kMaxFirst) {
     // Lane k reads the (m, l) of slots g + G k, g + G (k + 32), ...
     for (int s = g + G * lane; s < ns; s += G * 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(pml + s * 2);
+      const float2 ml = *reinterpret_cast<const float2*>(pml + slot_of(s) * 2);
       if (ml.y > 0.0f) m = fmaxf(m, ml.x);
     }
 #pragma unroll
@@ -62,7 +74,7 @@ __device__ __forceinline__ void merge_body(const MergeParams& p) {
     for (int u = 0; u < U; ++u) {
       const int s = s0 + u * G;
       const bool in = s < ns;
-      const int slot = in ? s : s0;  // weight-0 padded load of a valid slot
+      const int slot = slot_of(in ? s : s0);  // weight-0 padded load of a valid slot
       const float2 ml = *reinterpret_cast<const float2*>(pml + slot * 2);
       ou[u] = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(slot) * MLA_LATENT_DIM);
       mu[u] = (in && ml.y > 0.0f) ? ml.x : -INFINITY;
@@ -146,6 +158,11 @@ __global__ void __launch_bounds__(32 * G) mla_merge_kernel(const MergeParams p) 
   merge_body<G, 4, kMaxFirst>(p);
 }
 
+template <int G>
+__global__ void __launch_bounds__(32 * G) mla_merge_shared_kernel(const MergeParams p) {
+  merge_body<G, 4, false, true>(p);
+}
+
 // Grids of more than two 512-thread CTAs per SM: three per SM (at most 40
 // registers, two loads in flight per group instead of four), so that the
 // grid fits one wave.
@@ -205,6 +222,31 @@ cudaError_t launch_merge(const MergeParams& mp, int kv_split, cudaStream_t strea
   }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+template <int G>
+static cudaError_t launch_merge_shared_g(const MergeParams& mp, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(mp.rows, 4);
+  cfg.blockDim = dim3(32 * G);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mla_merge_shared_kernel<G>, mp);
+}
+
+cudaError_t launch_merge_shared(const MergeParams& mp, int kv_split, cudaStream_t stream) {
+  switch (kv_split) {
+    case 1: return launch_merge_shared_g<1>(mp, stream);
+    case 2: return launch_merge_shared_g<2>(mp, stream);
+    case 4: return launch_merge_shared_g<4>(mp, stream);
+    case 8: return launch_merge_shared_g<8>(mp, stream);
+    case 16: return launch_merge_shared_g<16>(mp, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace mla

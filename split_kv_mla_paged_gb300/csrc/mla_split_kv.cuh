@@ -220,7 +220,89 @@ struct ItemInfo {
       n_tiles;
   bool sparse;
   float c_log2, kv_scale;
+  // Shared prefixes (kMode 3) only: the batch row of row 0 of the segment's
+  // request, its page table from key 0 of the segment on, the partials' slot.
+  int row_at, slot;
+  const int32_t* table;
 };
+
+// The segment `seg` of a decode over shared prefixes and its split: keys count
+// from the segment's first one, so that the causal limit of a suffix is that of
+// a request of its own; a prefix, which every row sees whole, gets a length that
+// puts that limit behind its end.  False (reported) where the plan does not fit.
+__device__ __forceinline__ bool item_segment(const DecodeParams& p, int seg, int split,
+                                             ItemInfo& it) {
+  const int4 a = reinterpret_cast<const int4*>(p.segs + seg)[0];
+  const int4 c = reinterpret_cast<const int4*>(p.segs + seg)[1];
+  const Segment s{a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  const bool suffix = s.len < 0;
+  it.b = s.request;
+  it.split = split;
+  it.grp = 0;
+  it.q_b = suffix && p.query_lens ? p.query_lens[s.request] : p.q_len;
+  const int len = suffix ? p.kv_lens[s.request] - s.key0 : s.len;
+  it.nsplit = s.splits;
+  const bool bad = len < 0 || it.q_b < 1 || it.q_b > p.q_len ||
+                   (suffix && p.causal && len < it.q_b) || split >= s.splits ||
+                   s.chunk < kTileTokens || (s.chunk % kTileTokens) != 0 ||
+                   static_cast<int64_t>(s.splits) * s.chunk < len ||
+                   (s.splits > 1 && static_cast<int64_t>(s.splits - 1) * s.chunk >= len) ||
+                   static_cast<int64_t>(s.key0) + len >
+                       static_cast<int64_t>(p.max_pages) * MLA_PAGE_SIZE;
+  if (bad) {
+    if (threadIdx.x == 0) report(p.status, MLA_ERR_INVALID_ARG);
+    return false;
+  }
+  it.L = suffix ? len : len + it.q_b;
+  it.t0 = split * s.chunk;
+  it.tok_end = min(len, it.t0 + s.chunk);
+  it.win_lo = 0;
+  it.win_hi = it.L;
+  it.sparse = false;
+  it.row0 = s.row_in_req;
+  it.row_at = s.first_row - s.row_in_req;
+  it.rows_here = s.n_rows;
+  it.rows_valid =
+      suffix ? max(0, min(s.n_rows, it.q_b * p.num_heads - s.row_in_req)) : s.n_rows;
+  it.table = p.page_table + static_cast<int64_t>(s.request) * p.max_pages + s.key0 / MLA_PAGE_SIZE;
+  it.slot = split + (suffix ? p.suffix_slot : 0);
+  it.c_log2 = p.c_log2;
+  it.kv_scale = p.kv_scale;
+  if (p.q_scale_dev || p.kv_scale_dev || p.sm_scale_dev) {
+    const float qs = p.q_scale_dev ? *p.q_scale_dev : p.q_scale_h;
+    it.kv_scale = p.kv_scale_dev ? *p.kv_scale_dev : p.kv_scale;
+    const float ss = p.sm_scale_dev ? *p.sm_scale_dev : p.sm_scale_h;
+    it.c_log2 = ss * qs * it.kv_scale * 1.4426950408889634f;
+  }
+  it.n_tiles = (it.rows_valid > 0 && it.tok_end > it.t0)
+                   ? (it.tok_end - it.t0 + kTileTokens - 1) / kTileTokens
+                   : 0;
+  return true;
+}
+
+// Where an item's rows, pages and partials are: from its request, or (kMode 3)
+// from its segment.
+template <int kMode>
+__device__ __forceinline__ int item_row_at(const DecodeParams& p, const ItemInfo& it) {
+  if constexpr (kMode == 3)
+    return it.row_at;
+  else
+    return it.b * p.rows_per_req;
+}
+template <int kMode>
+__device__ __forceinline__ const int32_t* item_table(const DecodeParams& p, const ItemInfo& it) {
+  if constexpr (kMode == 3)
+    return it.table;
+  else
+    return p.page_table + static_cast<int64_t>(it.b) * p.max_pages;
+}
+template <int kMode>
+__device__ __forceinline__ int item_slot(const ItemInfo& it) {
+  if constexpr (kMode == 3)
+    return it.slot;
+  else
+    return it.split;
+}
 
 // Item (b, split, grp): the plan checks (a bad plan is reported as
 // MLA_ERR_INVALID_ARG and gives false), then the split's token range in the
@@ -292,7 +374,7 @@ __device__ __forceinline__ bool item_info(const DecodeParams& p, int b, int spli
 // or like the selection's entries); -1 where it is not loaded.  Bad ids are
 // reported by the producer, which reads page 0 in their place, as here.  key0
 // (restricted key sets): the first key position of the page.
-template <bool kGather>
+template <bool kGather, int kMode>
 __device__ __forceinline__ int fp4_page(const DecodeParams& p, const ItemInfo& it, int pi,
                                         int& key0) {
   key0 = 0;
@@ -307,7 +389,7 @@ __device__ __forceinline__ int fp4_page(const DecodeParams& p, const ItemInfo& i
       return -1;
     key0 = lp * MLA_PAGE_SIZE;
   }
-  const int pg = p.page_table[static_cast<int64_t>(it.b) * p.max_pages + lp];
+  const int pg = item_table<kMode>(p, it)[lp];
   return (pg < 0 || pg >= p.num_pages) ? 0 : pg;
 }
 
@@ -332,7 +414,9 @@ __device__ __forceinline__ bool decode_item(const DecodeParams& p, int it, int n
 // group) grid, 1 the CTA item list (one item per CTA), 2 persistent CTAs
 // that each loop over items blockIdx.x, blockIdx.x + gridDim.x, ... of the
 // list, carrying every barrier phase from one item to the next so that the
-// next item's Q and first tiles load while the current one finishes.
+// next item's Q and first tiles load while the current one finishes; 3 the item
+// list of a decode over shared prefixes (segments in the place of requests, one
+// item per CTA, partials whatever the number of splits).
 template <int NR, bool kGather, int kMode, bool kFp4 = false>
 __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     mla_split_kv_kernel(const __grid_constant__ CUtensorMap tm_kv_lat,
@@ -342,6 +426,8 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
   using C = Cfg<NR, kFp4>;
   constexpr bool kPersist = kMode == 2;
   static_assert(!kFp4 || !kPersist, "the 4-bit cache has one item per CTA");
+  constexpr bool kShared = kMode == 3;
+  static_assert(!kShared || !kGather, "shared prefixes take whole key ranges");
   // Grid (request, split x row group), dispatched split-major: every
   // request's first splits go out before anyone's later ones, so the empty
   // slots of short requests (split >= splits[b], exiting at once) do not hold
@@ -351,7 +437,24 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
   // have work, in the same order.
   const int ngroups = (p.rows_per_req + p.rows_per_group - 1) / p.rows_per_group;
   ItemInfo first{};
-  if constexpr (!kPersist) {
+  if constexpr (kShared) {
+    // The next launch's CTAs may take the SMs that this one leaves free.
+    if (p.chain & SHARED_RELEASE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int entry = p.cta_items[blockIdx.x];
+    const int seg = entry >> MLA_ITEM_B_SHIFT;
+    bool fits = entry >= 0 && seg < p.num_segs;
+    if (!fits) {
+      if (threadIdx.x == 0) report(p.status, MLA_ERR_INVALID_ARG);
+    } else {
+      fits = item_segment(
+          p, seg, (entry >> MLA_ITEM_S_SHIFT) & ((1 << (MLA_ITEM_B_SHIFT - MLA_ITEM_S_SHIFT)) - 1),
+          first);
+    }
+    if (!fits) {
+      if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
+      return;
+    }
+  } else if constexpr (!kPersist) {
     int b, split, grp;
     if constexpr (kMode == 1) {
       if (!decode_item(p, p.cta_items[blockIdx.x], ngroups, b, split, grp)) return;
@@ -404,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     if ((threadIdx.x >> 5) == 0) {
       const int pi = first.t0 / MLA_PAGE_SIZE + static_cast<int>(threadIdx.x & 31);
       if (pi < (first.tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE)
-        pre_window = p.page_table[static_cast<int64_t>(first.b) * p.max_pages + pi];
+        pre_window = item_table<kMode>(p, first)[pi];
     }
   }
   (void)pre_window;
@@ -414,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     const int ew = static_cast<int>(threadIdx.x >> 5) - C::kExpandWarp0;
     const int ch = ew + C::kExpandWarps * static_cast<int>(threadIdx.x & 31);
     if (ew >= 0 && ch < first.n_tiles * 8)
-      pre_page = fp4_page<kGather>(p, first, first.t0 / MLA_PAGE_SIZE + (ch >> 1), pre_key0);
+      pre_page = fp4_page<kGather, kMode>(p, first, first.t0 / MLA_PAGE_SIZE + (ch >> 1), pre_key0);
   }
   (void)pre_page;
   (void)pre_key0;
@@ -535,7 +638,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           }
         }
         if (lane == 0) {
-          const int qrow = b * p.rows_per_req + row0;
+          const int qrow = item_row_at<kMode>(p, item) + row0;
           mbar_arrive_expect_tx(bar(BAR_QFULL), C::kQBytes);
 #pragma unroll
           for (int d = 0; d < 4; ++d)
@@ -544,7 +647,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
                       bar(BAR_QFULL));
         }
         ++nq;
-        const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+        const int32_t* pt = item_table<kMode>(p, item);
         const int page0 = t0 / MLA_PAGE_SIZE;
         const int page_end = (tok_end + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;  // exclusive
         // Page ids of 8 tiles (32 pages) per window, one per lane; the next
@@ -1042,7 +1145,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           if (ch >= n_chunks) return 0;
           int key0;
           const int pg =
-              fp4_page<kGather>(p, first, t0 / MLA_PAGE_SIZE + (ch >> 4) * 4 + (ch & 3), key0);
+              fp4_page<kGather, kMode>(p, first, t0 / MLA_PAGE_SIZE + (ch >> 4) * 4 + (ch & 3), key0);
           if (pg < 0) return 0;
           if constexpr (kGather) hide = max(0, win_lo - key0);
           return pg;
@@ -1162,7 +1265,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           key0 = 0;
           const int ch = ew + W * (w * 32 + lane);
           if (ch >= n_chunks) return -1;
-          return fp4_page<kGather>(p, first, t0 / MLA_PAGE_SIZE + (ch >> 1), key0);
+          return fp4_page<kGather, kMode>(p, first, t0 / MLA_PAGE_SIZE + (ch >> 1), key0);
         };
         int key0 = pre_key0, key0_next;  // (window 0 was read before the set-up)
         int window = pre_page, window_next = chunk_window(1, key0_next);
@@ -1869,7 +1972,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         warp_reduce_rows<NRH, false>(lsum, lane, red_sum + quad * NR + rbase);
       }
       named_bar_sync(kSoftmaxBarrier, NT);
-      const bool single = (nsplit == 1);
+      const bool single = !kShared && nsplit == 1;
       float* scale_s = alpha_s;
       if (own >= 0) {
         if (n_tiles > 0) {
@@ -1877,7 +1980,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           l_row += (rs[own] + rs[NR + own]) + (rs[2 * NR + own] + rs[3 * NR + own]);
         }
         const float m_s = (k_row == -INFINITY) ? -INFINITY : k_row - 8.0f;
-        const int64_t grow = static_cast<int64_t>(b) * p.rows_per_req + row0 + own;
+        const int64_t grow = static_cast<int64_t>(item_row_at<kMode>(p, item)) + row0 + own;
         float sc = 0.0f;
         if (own < rows_here) {
           if (single) {
@@ -1892,7 +1995,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
             if (p.lse) p.lse[grow] = ls;
             sc = (den > 0.0f) ? kv_scale * p.output_scale * a / den : 0.0f;
           } else {
-            float* ml = p.ws_ml + (grow * p.max_splits + split) * 2;
+            float* ml = p.ws_ml + (grow * p.max_splits + item_slot<kMode>(item)) * 2;
             ml[0] = m_s;
             ml[1] = l_row;
             sc = kv_scale;
@@ -1917,11 +2020,12 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
         // Per latent block: every column of this warpgroup's rows (and their
         // lo products up to 48 rows) in one batch of TMEM loads and one wait,
         // then the stores.  Row k of the warpgroup goes to base + k * stride.
-        const int64_t grow0 = static_cast<int64_t>(b) * p.rows_per_req + row0 + rbase;
+        const int64_t grow0 = static_cast<int64_t>(item_row_at<kMode>(p, item)) + row0 + rbase;
         const int64_t stride = single ? MLA_LATENT_DIM
                                       : static_cast<int64_t>(p.max_splits) * MLA_LATENT_DIM;
         float* const obase = single ? nullptr
-                                    : p.ws_o + (grow0 * p.max_splits + split) * MLA_LATENT_DIM;
+                                    : p.ws_o + (grow0 * p.max_splits + item_slot<kMode>(item)) *
+                                                   MLA_LATENT_DIM;
         const int nrow = min(NRH, rows_here - rbase);  // rows of this warpgroup to store
         // With a P^T buffer to spare (free after the item's last PV), each
         // warp turns its 32 dims x 8 rows at a time around through 1 KB of it,
@@ -2032,7 +2136,13 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     tmem_dealloc(tmem, C::kTmemCols);
   }
   // This CTA's partials are written: the merge may start once every CTA is here.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (Shared prefixes: and once the launch before this one, whose end the merge
+  // does not wait for itself, has ended.)
+  if (!kShared || !(p.chain & SHARED_RELEASE))
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (kShared) {
+    if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
 }
 #undef MLA_ITEM_NAMES
 
@@ -2099,6 +2209,20 @@ static cudaError_t launch_split_t(const void* q, const void* kv, int64_t num_pag
   if (!make_map(&q_lat, q, q_rows, 128, NR, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&q_rope, q, q_rows, 64, NR, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
+  if constexpr (kMode == 3) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_ctas);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (prm.chain & SHARED_JOIN) ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, mla_split_kv_kernel<NR, kGather, kMode, kFp4>, kv_lat, kv_rope,
+                              q_lat, q_rope, prm);
+  }
   // Persistent: num_ctas CTAs loop over the prm.num_items items of the list.
   const dim3 grid = kMode != 0 ? dim3(num_ctas) : dim3(batch, prm.max_splits * groups);
   mla_split_kv_kernel<NR, kGather, kMode, kFp4>
@@ -2117,6 +2241,14 @@ static cudaError_t launch_split(const void* q, const void* kv, int64_t num_pages
   if (num_ctas < prm.num_items)
     return launch_split_t<NR, kGather, 2>(q, kv, num_pages, batch, groups, num_ctas, prm, stream);
   return launch_split_t<NR, kGather, 1>(q, kv, num_pages, batch, groups, num_ctas, prm, stream);
+}
+
+// One launch of a decode over shared prefixes (the batch's rows as one request's).
+template <int NR, bool kFp4>
+static cudaError_t launch_segments(const void* q, const void* kv, int64_t rows, int num_ctas,
+                                   DecodeParams prm, cudaStream_t stream) {
+  prm.rows_per_req = static_cast<int32_t>(rows);
+  return launch_split_t<NR, false, 3, kFp4>(q, kv, prm.num_pages, 1, 1, num_ctas, prm, stream);
 }
 
 // Validated launch state shared by mla_decode, mla_decode_splitkv and

@@ -21,7 +21,9 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <exception>
 #include <string>
+#include <vector>
 
 #include "mla_internal.h"
 
@@ -224,4 +226,227 @@ extern "C" int mla_decode_plan_items_bf16(const int32_t* splits, int32_t batch, 
                                           int32_t* n_items_out) {
   return plan_items("mla_decode_plan_items_bf16", splits, batch, num_heads, q_len, true,
                     items_out, capacity, n_items_out);
+}
+
+// ---------------------------------------------------------------------------
+// Decode over shared prefixes
+// ---------------------------------------------------------------------------
+namespace mla {
+
+// Time of one 128-key tile of the split kernels by cache and rows per CTA, and of
+// the rest of a CTA (start, epilogue, its partials' share of the merge), in
+// nanoseconds as measured with all SMs at work: what matters are their ratios.
+static int64_t tile_ns(int kind, int nr) {
+  if (kind == MLA_CACHE_BF16) return nr <= 16 ? 3300 : nr <= 32 ? 9000 : 10000;
+  if (kind == MLA_CACHE_FP4) return nr <= 16 ? 1750 : nr <= 32 ? 2500 : nr <= 48 ? 2800 : 4200;
+  return nr <= 16 ? 1650 : nr <= 32 ? 2370 : nr <= 48 ? 2640 : 3000;
+}
+static int64_t cta_ns(int rows) { return 2600 + 94 * static_cast<int64_t>(rows); }
+
+struct SharedSegment {  // layout of the device's Segment
+  int32_t first_row, n_rows, row_in_req, request, key0, len, splits, chunk;
+  int64_t keys;  // host only: keys of this plan
+};
+
+}  // namespace mla
+
+extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offsets,
+                               const int32_t* prefix_lens, int32_t batch, int32_t groups,
+                               int32_t num_heads, int32_t q_len, int32_t causal,
+                               int32_t cache_kind, int32_t sm_count, int32_t* data_out,
+                               int64_t capacity, mla_shared_plan_t* plan_out) try {
+  const std::string who = "mla_shared_plan";
+  if (!kv_lens || !group_offsets || !prefix_lens || !plan_out) {
+    set_error(who + ": null pointer argument");
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (batch < 1 || batch > MLA_ITEM_MAX_BATCH || groups < 1 || groups > batch || num_heads < 1 ||
+      q_len < 1 || sm_count < 1) {
+    set_error(who + ": batch in [1, MLA_ITEM_MAX_BATCH], groups in [1, batch], num_heads, q_len "
+                    "and sm_count >= 1");
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (static_cast<int64_t>(num_heads) * q_len > MLA_MAX_ROWS) {
+    set_error(who + ": num_heads * q_len exceeds MLA_MAX_ROWS");
+    return MLA_ERR_UNSUPPORTED;
+  }
+  if (cache_kind != MLA_CACHE_FP8 && cache_kind != MLA_CACHE_BF16 && cache_kind != MLA_CACHE_FP4) {
+    set_error(who + ": unknown cache kind");
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (group_offsets[0] != 0 || group_offsets[groups] != batch) {
+    set_error(who + ": group_offsets must start at 0 and end at batch");
+    return MLA_ERR_INVALID_ARG;
+  }
+  const int per_req = num_heads * q_len;
+  const bool bf16 = cache_kind == MLA_CACHE_BF16;
+  std::vector<SharedSegment> segs;
+  int64_t rows_max[2] = {0, 0};  // rows of the largest prefix and suffix segment
+  auto add = [&](int kind, int64_t row, int64_t n_rows, int request, int key0, int64_t keys,
+                 bool suffix) {
+    const RowGroups rg = bf16 ? row_groups(static_cast<int>(n_rows))
+                              : row_groups_fp8(static_cast<int>(n_rows));
+    for (int64_t r = 0; r < n_rows; r += rg.rows) {
+      const int32_t n = static_cast<int32_t>(std::min<int64_t>(rg.rows, n_rows - r));
+      segs.push_back({static_cast<int32_t>(row + r), n, suffix ? static_cast<int32_t>(r) : 0,
+                      request, key0, suffix ? -1 : static_cast<int32_t>(keys), 1, 0, keys});
+      rows_max[kind] = std::max<int64_t>(rows_max[kind], n);
+    }
+  };
+  for (int g = 0; g < groups; ++g) {
+    const int first = group_offsets[g], last = group_offsets[g + 1];
+    if (last <= first || last > batch) {
+      set_error(who + ": group_offsets must ascend");
+      return MLA_ERR_INVALID_ARG;
+    }
+    if (prefix_lens[g] < 0 || prefix_lens[g] % MLA_PAGE_SIZE != 0) {
+      set_error(who + ": prefix_lens[" + std::to_string(g) + "] is not a multiple of " +
+                std::to_string(MLA_PAGE_SIZE));
+      return MLA_ERR_INVALID_ARG;
+    }
+    for (int b = first; b < last; ++b) {
+      const int64_t own = static_cast<int64_t>(kv_lens[b]) - prefix_lens[g];
+      if (kv_lens[b] < 1 || own < (causal ? q_len : 0) ||
+          kv_lens[b] > INT32_MAX - MLA_TILE_TOKENS - MLA_MAX_ROWS) {
+        set_error(who + ": kv_lens[" + std::to_string(b) + "] = " + std::to_string(kv_lens[b]) +
+                  " does not hold its prefix and, under causal, q_len keys, or is too large");
+        return MLA_ERR_INVALID_ARG;
+      }
+    }
+    if (prefix_lens[g] > 0)
+      add(0, static_cast<int64_t>(first) * per_req, static_cast<int64_t>(last - first) * per_req,
+          first, 0, prefix_lens[g], false);
+  }
+  const size_t n_prefix = segs.size();
+  for (int g = 0; g < groups; ++g)
+    for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b)
+      add(1, static_cast<int64_t>(b) * per_req, per_req, b, prefix_lens[g],
+          static_cast<int64_t>(kv_lens[b]) - prefix_lens[g], true);
+  if (segs.size() > MLA_ITEM_MAX_BATCH) {
+    set_error(who + ": too many row groups");
+    return MLA_ERR_UNSUPPORTED;
+  }
+  int nr[2];
+  for (int k = 0; k < 2; ++k) {
+    nr[k] = static_cast<int>((rows_max[k] + 15) / 16 * 16);
+    if (!bf16 && nr[k] > kMaxRowsPerCta) nr[k] = kMaxRowsPerCtaFp8;
+  }
+  if (n_prefix == 0) nr[0] = nr[1];
+
+  // One time per CTA for all segments, prefixes and suffixes alike: the smallest
+  // whose CTAs fit one wave of the SMs, or two waves where that ends sooner; one
+  // split each where there are more segments than that.
+  const int64_t T = MLA_TILE_TOKENS;
+  const int64_t cost[2] = {tile_ns(cache_kind, nr[0]), tile_ns(cache_kind, nr[1])};
+  const int64_t fixed[2] = {cta_ns(nr[0]), cta_ns(nr[1])};
+  auto chunk_of = [&](size_t s, int64_t ns) -> int64_t {
+    const int k = s < n_prefix ? 0 : 1;
+    const int64_t keys = std::max<int64_t>(segs[s].keys, 1);
+    int64_t tiles = std::max<int64_t>(1, (ns - fixed[k]) / cost[k]);
+    const int64_t all = ceil_div(keys, T);
+    // Splits of equal size: as few keys as this number of splits needs.
+    tiles = ceil_div(all, ceil_div(all, std::min(tiles, all)));
+    return tiles * T;
+  };
+  auto ctas_at = [&](int64_t ns, int64_t slots[2]) -> int64_t {
+    int64_t n = 0;
+    slots[0] = slots[1] = 0;
+    for (size_t s = 0; s < segs.size(); ++s) {
+      const int64_t k = ceil_div(std::max<int64_t>(segs[s].keys, 1), chunk_of(s, ns));
+      n += k;
+      int64_t& m = slots[s < n_prefix ? 0 : 1];
+      m = std::max(m, k);
+    }
+    return n;
+  };
+  int64_t most = 0;
+  for (size_t s = 0; s < segs.size(); ++s) {
+    const int k = s < n_prefix ? 0 : 1;
+    most = std::max(most, fixed[k] + cost[k] * ceil_div(std::max<int64_t>(segs[s].keys, 1), T));
+  }
+  int64_t best = most, best_cost = -1;
+  int64_t slots[2];
+  for (int w = 1; w <= kMaxWaves; ++w) {
+    auto fits = [&](int64_t ns) {
+      return ctas_at(ns, slots) <= static_cast<int64_t>(w) * sm_count &&
+             slots[0] + slots[1] <= MLA_MAX_SPLITS;
+    };
+    if (!fits(most)) continue;
+    int64_t lo = 1, hi = most;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (fits(mid)) hi = mid; else lo = mid + 1;
+    }
+    if (best_cost < 0 || lo * w < best_cost) {
+      best_cost = lo * w;
+      best = lo;
+    }
+  }
+  const int64_t total = ctas_at(best, slots);
+  int64_t n_ctas[2] = {0, 0};
+  for (size_t s = 0; s < segs.size(); ++s) {
+    segs[s].chunk = static_cast<int32_t>(chunk_of(s, best));
+    segs[s].splits =
+        static_cast<int32_t>(ceil_div(std::max<int64_t>(segs[s].keys, 1), segs[s].chunk));
+    n_ctas[s < n_prefix ? 0 : 1] += segs[s].splits;
+  }
+  if (total > INT32_MAX) {
+    set_error(who + ": too many CTAs");
+    return MLA_ERR_UNSUPPORTED;
+  }
+  mla_shared_plan_t p = {};
+  p.cache_kind = cache_kind;
+  p.batch = batch;
+  p.groups = groups;
+  p.q_len = q_len;
+  p.num_heads = num_heads;
+  p.causal = causal ? 1 : 0;
+  p.num_segments = static_cast<int32_t>(segs.size());
+  p.prefix_nr = nr[0];
+  p.suffix_nr = nr[1];
+  p.prefix_ctas = static_cast<int32_t>(n_ctas[0]);
+  p.suffix_ctas = static_cast<int32_t>(n_ctas[1]);
+  p.prefix_slots = static_cast<int32_t>(slots[0]);
+  p.suffix_slots = static_cast<int32_t>(slots[1]);
+  // The merge's thread groups, by mla_decode_plan's rule.
+  const int64_t rows = static_cast<int64_t>(batch) * per_req;
+  int32_t g = 16;
+  while (g > 1 && (g * 2 > slots[0] + slots[1] || rows * g > 6 * static_cast<int64_t>(sm_count)))
+    g >>= 1;
+  p.kv_split = g;
+  p.data_len = 8 * static_cast<int64_t>(segs.size()) + 2 * static_cast<int64_t>(batch) + total;
+  p.workspace_bytes = ws_total(rows, slots[0] + slots[1]);
+  *plan_out = p;
+  if (!data_out) return MLA_OK;
+  if (capacity < p.data_len) {
+    set_error(who + ": capacity " + std::to_string(capacity) + " below the " +
+              std::to_string(p.data_len) + " values of the plan");
+    return MLA_ERR_INVALID_ARG;
+  }
+  int32_t* out = data_out;
+  for (const SharedSegment& s : segs) {
+    const int32_t v[8] = {s.first_row, s.n_rows, s.row_in_req, s.request,
+                          s.key0,      s.len,    s.splits,     s.chunk};
+    out = std::copy(v, v + 8, out);
+  }
+  // Per request: partials of its group's prefix and of its own suffix.  (Row
+  // groups of one segment set have the same splits.)
+  std::vector<int32_t> of_prefix(batch, 0), of_suffix(batch, 0);
+  for (size_t s = 0; s < n_prefix; ++s) of_prefix[segs[s].request] = segs[s].splits;
+  for (size_t s = n_prefix; s < segs.size(); ++s) of_suffix[segs[s].request] = segs[s].splits;
+  for (int k = 0; k < groups; ++k)
+    for (int b = group_offsets[k]; b < group_offsets[k + 1]; ++b) {
+      *out++ = of_prefix[group_offsets[k]];
+      *out++ = of_suffix[b];
+    }
+  // Items, split-major; the row groups of one split side by side.
+  for (int k = 0; k < 2; ++k)
+    for (int64_t i = 0; i < slots[k]; ++i)
+      for (size_t s = k ? n_prefix : 0; s < (k ? segs.size() : n_prefix); ++s)
+        if (i < segs[s].splits)
+          *out++ = static_cast<int32_t>((s << MLA_ITEM_B_SHIFT) | (i << MLA_ITEM_S_SHIFT));
+  return MLA_OK;
+} catch (const std::exception&) {
+  set_error("mla_shared_plan: out of host memory");
+  return MLA_ERR_UNSUPPORTED;
 }
