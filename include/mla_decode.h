@@ -474,6 +474,111 @@ MLA_API int mla_decode_shared(const void* q, const void* kv_pages, int64_t num_p
                               void* out_bf16, float* lse_f32, float* out_f32_debug,
                               const mla_decode_options_t* options, void* stream);
 
+/*
+ * Verification of drafted tokens (what follows a decode of the MTP-verify block):
+ * slot 0 of a request's query block is its last token, slots 1 .. q_b - 1 are n =
+ * q_b - 1 drafted ones, and slot i's probabilities p_i are those of the token
+ * behind it.
+ *   Draft i (x_i, drawn from q_i) is accepted while u_i q_i(x_i) < p_i(x_i), i = 0,
+ *   1, ...; a of them are.  The next token is drawn from max(p_a - q_a, 0) when
+ *   a < n (from p_a where that is 0 everywhere), from p_n when a == n: the smallest
+ *   k whose cumulated weight exceeds u times the sum of the weights.
+ * Drafts and next tokens then are distributed as tokens drawn from p one by one.
+ * Without draft_probs a draft is certain, q_i(x_i) = 1: it is accepted while u_i <
+ * p_i(x_i), and a rejected one is left out of p_a.
+ * Products and sums are exact: probabilities from 2^-26 on are taken as they are,
+ * smaller ones as the nearest multiple of 2^-50, so that results do not depend on
+ * the order of a sum.  In the sums NaNs and negative values count as 0, values
+ * above 1 as 1, and the values of a row must not sum to more than 8192.  A row
+ * without a positive weight gives token -1.
+ *
+ * target_probs   [batch][q_len][vocab], probs_type MLA_PROBS_F32 or MLA_PROBS_BF16;
+ *                strides in elements, 0 = contiguous.  draft_probs [batch][q_len -
+ *                1][vocab] of the same type, or NULL.
+ * draft_tokens   int32 [batch][q_len - 1] (NULL where q_len == 1): x.
+ * uniforms       fp32 [batch][q_len] in [0, 1): u_i for the drafts, the last of the
+ *                row (whatever q_b) for the next token.  Outside [0, 1) that last one
+ *                is taken as the nearest number inside.
+ * query_lens     int32 [batch] or NULL (q_b = q_len): q_b in [1, q_len].
+ * tokens_out     int32 [batch][q_len]: the a accepted drafts, the next token, then -1.
+ * accepted_out   int32 [batch]: a.
+ * kv_lens, new_lens   int32 [batch] or both NULL: cached keys with the query block,
+ *                and those that stay valid, kv_lens - n + a.  May be the same array.
+ * status         int32 or NULL: set to MLA_ERR_INVALID_ARG for a query count outside
+ *                [1, q_len] (that request is skipped) or a draft outside the
+ *                vocabulary (it is rejected); never cleared by the call.
+ * All on the device.  Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (sizes),
+ * MLA_ERR_CUDA.  Zero-initialise the structure.
+ */
+#define MLA_PROBS_F32 0
+#define MLA_PROBS_BF16 1
+#define MLA_VERIFY_MAX_VOCAB (1 << 27)
+typedef struct {
+  const void* target_probs;
+  int64_t target_batch_stride, target_row_stride;
+  const void* draft_probs;
+  int64_t draft_batch_stride, draft_row_stride;
+  const int32_t* draft_tokens;
+  const float* uniforms;
+  const int32_t* query_lens;
+  const int32_t* kv_lens;
+  int32_t* tokens_out;
+  int32_t* accepted_out;
+  int32_t* new_lens;
+  int32_t* status;
+  int32_t batch, q_len, vocab, probs_type;
+} mla_verify_args_t;
+
+MLA_API int mla_verify_drafts(const mla_verify_args_t* args, void* stream);
+
+/*
+ * Eviction, first part: which keys of each request stay, by the weight that each
+ * has received (mla_key_weights).  Request b keeps K_b = min(kv_lens[b], keep[b],
+ * kept_stride) keys: the first `first` and the last `last` ones before all others,
+ * then by falling weight; among equal weights (and among protected keys, where K_b
+ * does not suffice for them) the lower position first.  -0 equals 0; a NaN ranks
+ * below every number.
+ *
+ * weights        fp32 [batch][weights_stride]: weight of key j of request b at
+ *                [b][j], j < kv_lens[b] <= weights_stride.
+ * keep           int32 [batch], >= 0.
+ * kept           int32 [batch][kept_stride]: the K_b positions, ascending; what lies
+ *                behind them stays as it was.
+ * new_lens       int32 [batch]: K_b.  May be kv_lens.
+ * new_weights    fp32 [batch][new_weights_stride] or NULL: weights[b][kept[b][i]] at
+ *                [b][i], i < K_b <= new_weights_stride; not overlapping weights.
+ * status         int32 or NULL: set to MLA_ERR_INVALID_ARG for a length outside [0,
+ *                weights_stride], a negative keep or K_b > new_weights_stride; that
+ *                request keeps nothing (new_lens 0).  Never cleared by the call.
+ * All on the device.  Strides in elements.
+ */
+MLA_API int mla_evict_select(const float* weights, int64_t weights_stride, const int32_t* kv_lens,
+                             const int32_t* keep, int32_t batch, int32_t first, int32_t last,
+                             int32_t* kept, int64_t kept_stride, int32_t* new_lens,
+                             float* new_weights, int64_t new_weights_stride, int32_t* status,
+                             void* stream);
+
+/*
+ * Eviction, second part: row kept[b][i] of request b, found through src_table, goes
+ * to row i of request b through dst_table, i < counts[b]; both pools of one kind.
+ * Rows keep their bytes (their rotation is that of the position they were written
+ * at).  No destination page may be a source page of the call, nor belong to two
+ * requests: destinations are freshly allocated pages (mla_pool_alloc), and the old
+ * ones are given back afterwards (mla_pool_release), as shared pages must not
+ * change.
+ *
+ * src_table      int32 [batch][src_max_pages]; dst_table int32 [batch][dst_max_pages].
+ * kept           int32 [batch][kept_stride]; counts int32 [batch], counts[b] <=
+ *                kept_stride.
+ * status         int32 or NULL: set to MLA_ERR_INVALID_ARG for a count, position or
+ *                page id out of range (what needs it is not copied); never cleared.
+ */
+MLA_API int mla_rows_move(const void* src_pool, int64_t src_pages, const int32_t* src_table,
+                          int32_t src_max_pages, void* dst_pool, int64_t dst_pages,
+                          const int32_t* dst_table, int32_t dst_max_pages, int32_t cache_kind,
+                          const int32_t* kept, int64_t kept_stride, const int32_t* counts,
+                          int32_t batch, int32_t* status, void* stream);
+
 /* Zero the 256-byte status header of a new workspace (async on `stream`).
  * Call once per workspace before its first mla_decode; after that the
  * header only changes when the device reports a condition, and

@@ -29,7 +29,8 @@ __all__ = [
     "decode", "merge", "MLA_ERR_NO_PAGES", "CACHE_FP8", "CACHE_BF16", "CACHE_FP4",
     "FP4_PAGE_BYTES", "mla_decode_fp4", "mla_decode_fp4_sparse", "PrologueArgs", "mla_prologue", "mla_pages_copy", "mla_pages_remap",
     "PagePool", "copy_pages", "fp4_pool", "SharedPlan", "mla_shared_plan", "mla_decode_shared",
-    "shared_groups",
+    "shared_groups", "PROBS_F32", "PROBS_BF16", "VerifyArgs", "mla_verify_drafts",
+    "verify_drafts", "mla_evict_select", "mla_rows_move", "evict",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -56,7 +57,8 @@ EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_workspace_size", "mla_decode_
                     "mla_pages_copy", "mla_pages_remap", "mla_pool_create", "mla_pool_destroy",
                     "mla_pool_free_pages", "mla_pool_references", "mla_pool_alloc",
                     "mla_pool_release", "mla_pool_fork", "mla_pool_compact", "mla_shared_plan",
-                    "mla_decode_shared")
+                    "mla_decode_shared", "mla_verify_drafts", "mla_evict_select",
+                    "mla_rows_move")
 
 HEAD_DIM = 576
 LATENT_DIM = 512
@@ -96,6 +98,23 @@ class PrologueArgs(ctypes.Structure):
                 ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
                 ("q_out", ctypes.c_void_p), ("num_heads", ctypes.c_int32),
                 ("q_kind", ctypes.c_int32), ("status", ctypes.c_void_p)]
+
+
+# Types of probabilities (mla_decode.h: MLA_PROBS_*).
+PROBS_F32, PROBS_BF16 = 0, 1
+
+
+class VerifyArgs(ctypes.Structure):
+    """mla_verify_args_t (include/mla_decode.h)."""
+    _fields_ = [("target_probs", ctypes.c_void_p), ("target_batch_stride", ctypes.c_int64),
+                ("target_row_stride", ctypes.c_int64), ("draft_probs", ctypes.c_void_p),
+                ("draft_batch_stride", ctypes.c_int64), ("draft_row_stride", ctypes.c_int64),
+                ("draft_tokens", ctypes.c_void_p), ("uniforms", ctypes.c_void_p),
+                ("query_lens", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("tokens_out", ctypes.c_void_p), ("accepted_out", ctypes.c_void_p),
+                ("new_lens", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("q_len", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("probs_type", ctypes.c_int32)]
 
 
 class _SharedPlanInfo(ctypes.Structure):
@@ -206,6 +225,14 @@ def load_library() -> ctypes.CDLL:
         lib.mla_pool_fork.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp]
         lib.mla_pool_compact.restype = ctypes.c_int
         lib.mla_pool_compact.argtypes = [vp, i64, vp, vp, vp, vp]
+        lib.mla_verify_drafts.restype = ctypes.c_int
+        lib.mla_verify_drafts.argtypes = [ctypes.POINTER(VerifyArgs), vp]
+        lib.mla_evict_select.restype = ctypes.c_int
+        lib.mla_evict_select.argtypes = [vp, i64, vp, vp, i32, i32, i32, vp, i64, vp, vp, i64, vp,
+                                         vp]
+        lib.mla_rows_move.restype = ctypes.c_int
+        lib.mla_rows_move.argtypes = [vp, i64, vp, i32, vp, i64, vp, i32, i32, vp, i64, vp, i32, vp,
+                                      vp]
         lib.mla_shared_plan.restype = ctypes.c_int
         lib.mla_shared_plan.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, i64,
                                         ctypes.POINTER(_SharedPlanInfo)]
@@ -694,6 +721,101 @@ def mla_decode_shared(q, kv_pages, num_pages: int, page_table, max_pages_per_req
              stream=stream)
 
 
+def _probs(t, name: str, device: int, dtype, rows: int):
+    """Address and strides of probabilities [batch, rows, vocab] with a dense last
+    dimension.  Strides of dimensions of size 1 are immaterial."""
+    ptr = _device_tensor(t, name, device, dtype, 0, False)
+    if t.dim() != 3 or t.shape[1] < rows or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [batch, {rows}, vocab] with a dense last dimension")
+    vocab = t.shape[2]
+    row = _row_stride(t, 1, name) if t.shape[1] > 1 else vocab
+    batch = _row_stride(t, 0, name) if t.shape[0] > 1 else max(rows, 1) * row
+    return ptr, batch, row
+
+
+def mla_verify_drafts(target_probs, draft_tokens, uniforms, tokens_out, accepted_out, *,
+                      draft_probs=None, query_lens=None, kv_lens=None, new_lens=None, status=None,
+                      stream=None) -> None:
+    """Verify drafted tokens against target_probs [batch, q_len, vocab] (float32 or
+    bfloat16, dense last dimension) with given uniform numbers [batch, q_len], and
+    draw the next token (see mla_verify_drafts in mla_decode.h)."""
+    import torch
+    i32 = torch.int32
+    dev = _device_of(target_probs, "target_probs")
+    dtype = target_probs.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"target_probs must be float32 or bfloat16, got {dtype}")
+    if target_probs.dim() != 3:
+        raise ValueError("target_probs must be [batch, q_len, vocab]")
+    batch, q_len, vocab = target_probs.shape
+    target, t_batch, t_row = _probs(target_probs, "target_probs", dev, dtype, q_len)
+    draft = d_batch = d_row = 0
+    if draft_probs is not None and q_len > 1:
+        draft, d_batch, d_row = _probs(draft_probs, "draft_probs", dev, dtype, q_len - 1)
+        if draft_probs.shape[0] < batch or draft_probs.shape[2] != vocab:
+            raise ValueError("draft_probs must be [batch, q_len - 1, vocab]")
+    if (new_lens is None) != (kv_lens is None):
+        raise ValueError("kv_lens and new_lens go together")
+    a = VerifyArgs(target, t_batch, t_row, draft or None, d_batch, d_row,
+                   _device_tensor(draft_tokens, "draft_tokens", dev, i32, batch * (q_len - 1)),
+                   _device_tensor(uniforms, "uniforms", dev, torch.float32, batch * q_len),
+                   _device_tensor(query_lens, "query_lens", dev, i32, batch),
+                   _device_tensor(kv_lens, "kv_lens", dev, i32, batch),
+                   _device_tensor(tokens_out, "tokens_out", dev, i32, batch * q_len),
+                   _device_tensor(accepted_out, "accepted_out", dev, i32, batch),
+                   _device_tensor(new_lens, "new_lens", dev, i32, batch),
+                   _device_tensor(status, "status", dev, i32, 1), batch, q_len, vocab,
+                   PROBS_BF16 if dtype is torch.bfloat16 else PROBS_F32)
+    _call_on(dev, load_library().mla_verify_drafts, ctypes.byref(a), stream=stream)
+
+
+def _rows_of(t, name: str, device: int, dtype, batch: int):
+    """Address, row stride and width of a [batch, n] tensor with dense rows."""
+    if t is None:
+        return None, 0
+    ptr = _device_tensor(t, name, device, dtype)
+    if t.dim() != 2 or t.shape[0] < batch:
+        raise ValueError(f"{name} must be [batch, n] with {batch} rows")
+    return ptr, t.shape[1]
+
+
+def mla_evict_select(weights, kv_lens, keep, kept, new_lens, *, first: int = 0, last: int = 0,
+                     new_weights=None, status=None, stream=None) -> None:
+    """Positions of the keys that stay, kept int32 [batch, n], by their weights
+    float32 [batch, keys] (see mla_evict_select in mla_decode.h)."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    dev = _device_of(weights, "weights")
+    batch = kv_lens.shape[0]
+    w, w_stride = _rows_of(weights, "weights", dev, f32, batch)
+    k, k_stride = _rows_of(kept, "kept", dev, i32, batch)
+    nw, nw_stride = _rows_of(new_weights, "new_weights", dev, f32, batch)
+    _call_on(dev, load_library().mla_evict_select, w, w_stride,
+             _device_tensor(kv_lens, "kv_lens", dev, i32, batch),
+             _device_tensor(keep, "keep", dev, i32, batch), batch, first, last, k, k_stride,
+             _device_tensor(new_lens, "new_lens", dev, i32, batch), nw, nw_stride,
+             _device_tensor(status, "status", dev, i32, 1), stream=stream)
+
+
+def mla_rows_move(src_pool, src_pages: int, src_table, dst_pool, dst_pages: int, dst_table, kept,
+                  counts, *, cache_kind: int, status=None, stream=None) -> None:
+    """Copy row kept[b][i] of request b (through src_table) to row i of request b
+    (through dst_table), i < counts[b]."""
+    import torch
+    i32 = torch.int32
+    dev = _device_of(dst_pool, "dst_pool")
+    batch = counts.shape[0]
+    src_t, src_width = _rows_of(src_table, "src_table", dev, i32, batch)
+    dst_t, dst_width = _rows_of(dst_table, "dst_table", dev, i32, batch)
+    k, k_stride = _rows_of(kept, "kept", dev, i32, batch)
+    _call_on(dev, load_library().mla_rows_move,
+             _device_pool(src_pool, "src_pool", dev, src_pages, cache_kind), src_pages, src_t,
+             src_width, _device_pool(dst_pool, "dst_pool", dev, dst_pages, cache_kind), dst_pages,
+             dst_t, dst_width, cache_kind, k, k_stride,
+             _device_tensor(counts, "counts", dev, i32, batch), batch,
+             _device_tensor(status, "status", dev, i32, 1), stream=stream)
+
+
 def shared_groups(page_lists, kv_lens, q_len: int = 1, least: int = PAGE_SIZE):
     """Groups of consecutive requests whose page lists begin with the same pages,
     for mla_shared_plan: (group_offsets, prefix_lens).  A request joins the group
@@ -1178,6 +1300,91 @@ def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> 
         mla_pages_copy(src_pool, src_pool.shape[0], src_kind, dst_pool, dst_pool.shape[0],
                        dst_kind, lists_d[0], lists_d[1], n,
                        rows=lists_d[2] if rows is not None else None)
+
+
+def verify_drafts(target_probs, draft_tokens, uniforms, *, draft_probs=None, query_lens=None,
+                  kv_lens=None, stream=None):
+    """Allocate the outputs with torch and run mla_verify_drafts: (tokens [batch,
+    q_len], accepted [batch], new_lens [batch] or None)."""
+    import torch
+    dev, (batch, q_len) = target_probs.device, target_probs.shape[:2]
+    tokens = torch.empty((batch, q_len), dtype=torch.int32, device=dev)
+    accepted = torch.empty((batch,), dtype=torch.int32, device=dev)
+    new_lens = None if kv_lens is None else torch.empty_like(accepted)
+    status = torch.zeros((1,), dtype=torch.int32, device=dev)
+    mla_verify_drafts(target_probs, draft_tokens, uniforms, tokens, accepted,
+                      draft_probs=draft_probs, query_lens=query_lens, kv_lens=kv_lens,
+                      new_lens=new_lens, status=status, stream=stream)
+    _check_status_tensor(status, stream, "verify_drafts: a query count or draft is out of range")
+    return tokens, accepted, new_lens
+
+
+def _check_status_tensor(status, stream, message: str) -> None:
+    """Wait for `stream` and raise where a call's status tensor was set."""
+    import torch
+    dev = status.device
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    (stream if stream is not None else torch.cuda.current_stream(dev)).synchronize()
+    if int(status.item()) != MLA_OK:
+        raise MlaError(int(status.item()), message)
+
+
+def evict(pool: PagePool, kv_pages, page_lists, kv_lens, weights, keep, *, first: int = 0,
+          last: int = 0, stream=None):
+    """Keep the `keep` keys of each request that have the largest weights (the
+    first `first` and last `last` ones always), in fresh pages of the pool, and
+    give the old pages back.
+
+    page_lists: each request's page ids (host lists); kv_lens and keep: host
+    integers (keep one per request, or one for all); weights float32 [requests,
+    keys].  Returns (new page lists, new lengths (host), new weights).  Needs free
+    pages for what stays beside the pages that are in use; MlaError
+    (MLA_ERR_NO_PAGES) otherwise, with nothing changed."""
+    import torch
+    lens = _host_ids(kv_lens, "kv_lens")
+    batch = lens.shape[0]
+    keep = np.ascontiguousarray(np.broadcast_to(_host_ids(keep, "keep"), (batch,)))
+    lists = [_host_ids(p, "page_lists") for p in page_lists]
+    if len(lists) != batch:
+        raise ValueError("page_lists and kv_lens must have the same length")
+    if batch == 0:
+        return [], lens, weights
+    if lens.min() < 0 or keep.min() < 0 or lens.max() > weights.shape[1]:
+        raise ValueError("kv_lens and keep must be >= 0, and kv_lens within the weights")
+    for p, n in zip(lists, lens):
+        if p.shape[0] * PAGE_SIZE < n:
+            raise ValueError("a page list is shorter than its request")
+        if p.shape[0] and (p.min() < 0 or p.max() >= kv_pages.shape[0]):
+            raise ValueError("page id outside the pool")
+    stay = np.minimum(lens, keep).astype(np.int32)
+    need = (stay + PAGE_SIZE - 1) // PAGE_SIZE
+    fresh = pool.alloc(int(need.sum()))
+    new_lists = np.split(fresh, np.cumsum(need)[:-1])
+    dev, most = kv_pages.device, max(1, int(stay.max()))
+
+    def table(rows):
+        out = np.full((batch, max(1, max(r.shape[0] for r in rows))), -1, dtype=np.int32)
+        for b, r in enumerate(rows):
+            out[b, :r.shape[0]] = r
+        return torch.from_numpy(out).to(dev)
+
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+        kept = torch.empty((batch, most), dtype=torch.int32, device=dev)
+        new_weights = torch.zeros((batch, most), dtype=torch.float32, device=dev)
+        both = torch.from_numpy(np.stack([lens, keep])).to(dev)
+        counts, status = torch.zeros_like(both[0]), torch.zeros_like(both[0, :1])
+        mla_evict_select(weights, both[0], both[1], kept, counts, first=first, last=last,
+                         new_weights=new_weights, status=status)
+        mla_rows_move(kv_pages, kv_pages.shape[0], table(lists), kv_pages, kv_pages.shape[0],
+                      table(new_lists), kept, counts, cache_kind=_cache_kind(kv_pages),
+                      status=status)
+    _check_status_tensor(status, stream, "evict: a length or page id is out of range")
+    for p in lists:
+        pool.release(p)
+    return new_lists, stay, new_weights
 
 
 def merge(partial_o, partial_ml, kv_split: int, want_f32: bool = True, stream=None):
