@@ -532,6 +532,52 @@ typedef struct {
 MLA_API int mla_verify_drafts(const mla_verify_args_t* args, void* stream);
 
 /*
+ * Attention weight that each cached key received from a decode's query rows, for an
+ * eviction: over the rows r of request b that see key j (query_lens and causal as
+ * for the decode),
+ *   weights[b][j] = decay * previous[b][j] + sum_r exp(s_rj - lse_r),  j < kv_lens[b],
+ * with the scores s of the definition above and the decode's LSE, of the whole key
+ * range: a decode over key windows or selected pages gives no such LSE.  With sinks
+ * a row's weights sum to less than 1.  Rows without a visible key (LSE -inf) add
+ * nothing.  What lies behind kv_lens stays as it was.
+ *
+ * Zero-initialise the structure.
+ * q, kv_pages    as for mla_decode_shared's cache kinds, 16-byte aligned.
+ * lse            fp32 [batch][q_len][num_heads].
+ * weights        fp32 [batch][weights_stride], kv_lens[b] <= weights_stride.
+ * previous       fp32 [batch][previous_stride] or NULL (nothing is added; decay is
+ *                then not used), previous_stride >= kv_lens[b].  May be weights.
+ * q_scale_dev, kv_scale_dev, softmax_scale_dev   device fp32 or NULL, as in
+ *                mla_decode_options_t.
+ * status         int32 or NULL: set to MLA_ERR_INVALID_ARG for a length outside [0,
+ *                min(weights_stride, previous_stride, 32 * max_pages_per_req)] or a
+ *                query count outside [1, q_len] (that request is skipped) or a bad
+ *                page id, to MLA_ERR_TIMEOUT for a wait that ran out; never cleared.
+ * All on the device; no workspace.
+ */
+typedef struct {
+  const void* q;
+  const void* kv_pages;
+  int64_t num_pages;
+  const int32_t* page_table;
+  const int32_t* kv_lens;
+  const int32_t* query_lens;
+  const float* lse;
+  float* weights;
+  int64_t weights_stride;
+  const float* previous;
+  int64_t previous_stride;
+  const float* q_scale_dev;
+  const float* kv_scale_dev;
+  const float* softmax_scale_dev;
+  int32_t* status;
+  int32_t max_pages_per_req, batch, q_len, num_heads, causal, cache_kind;
+  float q_scale, kv_scale, softmax_scale, decay;
+} mla_key_weights_args_t;
+
+MLA_API int mla_key_weights(const mla_key_weights_args_t* args, void* stream);
+
+/*
  * Eviction, first part: which keys of each request stay, by the weight that each
  * has received (mla_key_weights).  Request b keeps K_b = min(kv_lens[b], keep[b],
  * kept_stride) keys: the first `first` and the last `last` ones before all others,

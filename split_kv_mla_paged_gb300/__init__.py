@@ -30,7 +30,7 @@ __all__ = [
     "FP4_PAGE_BYTES", "mla_decode_fp4", "mla_decode_fp4_sparse", "PrologueArgs", "mla_prologue", "mla_pages_copy", "mla_pages_remap",
     "PagePool", "copy_pages", "fp4_pool", "SharedPlan", "mla_shared_plan", "mla_decode_shared",
     "shared_groups", "PROBS_F32", "PROBS_BF16", "VerifyArgs", "mla_verify_drafts",
-    "verify_drafts", "mla_evict_select", "mla_rows_move", "evict",
+    "verify_drafts", "KeyWeightsArgs", "mla_key_weights", "key_weights", "mla_evict_select", "mla_rows_move", "evict",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -58,7 +58,7 @@ EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_workspace_size", "mla_decode_
                     "mla_pool_free_pages", "mla_pool_references", "mla_pool_alloc",
                     "mla_pool_release", "mla_pool_fork", "mla_pool_compact", "mla_shared_plan",
                     "mla_decode_shared", "mla_verify_drafts", "mla_evict_select",
-                    "mla_rows_move")
+                    "mla_rows_move", "mla_key_weights")
 
 HEAD_DIM = 576
 LATENT_DIM = 512
@@ -115,6 +115,23 @@ class VerifyArgs(ctypes.Structure):
                 ("new_lens", ctypes.c_void_p), ("status", ctypes.c_void_p),
                 ("batch", ctypes.c_int32), ("q_len", ctypes.c_int32), ("vocab", ctypes.c_int32),
                 ("probs_type", ctypes.c_int32)]
+
+
+class KeyWeightsArgs(ctypes.Structure):
+    """mla_key_weights_args_t (include/mla_decode.h)."""
+    _fields_ = [("q", ctypes.c_void_p), ("kv_pages", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("query_lens", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("weights_stride", ctypes.c_int64), ("previous", ctypes.c_void_p),
+                ("previous_stride", ctypes.c_int64), ("q_scale_dev", ctypes.c_void_p),
+                ("kv_scale_dev", ctypes.c_void_p), ("softmax_scale_dev", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("max_pages_per_req", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("q_len", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("cache_kind", ctypes.c_int32), ("q_scale", ctypes.c_float),
+                ("kv_scale", ctypes.c_float), ("softmax_scale", ctypes.c_float),
+                ("decay", ctypes.c_float)]
 
 
 class _SharedPlanInfo(ctypes.Structure):
@@ -225,6 +242,8 @@ def load_library() -> ctypes.CDLL:
         lib.mla_pool_fork.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp]
         lib.mla_pool_compact.restype = ctypes.c_int
         lib.mla_pool_compact.argtypes = [vp, i64, vp, vp, vp, vp]
+        lib.mla_key_weights.restype = ctypes.c_int
+        lib.mla_key_weights.argtypes = [ctypes.POINTER(KeyWeightsArgs), vp]
         lib.mla_verify_drafts.restype = ctypes.c_int
         lib.mla_verify_drafts.argtypes = [ctypes.POINTER(VerifyArgs), vp]
         lib.mla_evict_select.restype = ctypes.c_int
@@ -779,6 +798,40 @@ def _rows_of(t, name: str, device: int, dtype, batch: int):
     return ptr, t.shape[1]
 
 
+def mla_key_weights(q, kv_pages, num_pages: int, page_table, max_pages_per_req: int, kv_lens, lse,
+                    weights, batch: int, q_len: int, num_heads: int, causal: bool, q_scale: float,
+                    kv_scale: float, softmax_scale: float, *, cache_kind: int, previous=None,
+                    decay: float = 1.0, query_lens=None, q_scale_dev=None, kv_scale_dev=None,
+                    softmax_scale_dev=None, status=None, stream=None) -> None:
+    """Attention weight that each cached key received from the rows of a decode
+    with log-sum-exps lse: weights[b][j] = decay * previous[b][j] + the rows' sum
+    (see mla_key_weights in mla_decode.h).  weights and previous are float32
+    [batch, keys] and may be the same tensor."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    dev = _device_of(q, "q")
+    rows = batch * q_len * num_heads
+    q_at = _device_tensor(q, "q", dev, None, rows * HEAD_DIM)
+    if q.element_size() != (2 if cache_kind == CACHE_BF16 else 1):
+        raise ValueError("q must be BF16 for a BF16 cache, E4M3 otherwise")
+    if _cache_kind(kv_pages) != cache_kind:
+        raise ValueError("kv_pages is not a pool of cache_kind")
+    w, w_stride = _rows_of(weights, "weights", dev, f32, batch)
+    prev, prev_stride = _rows_of(previous, "previous", dev, f32, batch)
+    a = KeyWeightsArgs(
+        q_at, _device_pool(kv_pages, "kv_pages", dev, num_pages, cache_kind), num_pages,
+        _device_tensor(page_table, "page_table", dev, i32, batch * max_pages_per_req),
+        _device_tensor(kv_lens, "kv_lens", dev, i32, batch),
+        _device_tensor(query_lens, "query_lens", dev, i32, batch),
+        _device_tensor(lse, "lse", dev, f32, rows), w, w_stride, prev, prev_stride,
+        _device_tensor(q_scale_dev, "q_scale_dev", dev, f32, 1),
+        _device_tensor(kv_scale_dev, "kv_scale_dev", dev, f32, 1),
+        _device_tensor(softmax_scale_dev, "softmax_scale_dev", dev, f32, 1),
+        _device_tensor(status, "status", dev, i32, 1), max_pages_per_req, batch, q_len, num_heads,
+        1 if causal else 0, cache_kind, q_scale, kv_scale, softmax_scale, decay)
+    _call_on(dev, load_library().mla_key_weights, ctypes.byref(a), stream=stream)
+
+
 def mla_evict_select(weights, kv_lens, keep, kept, new_lens, *, first: int = 0, last: int = 0,
                      new_weights=None, status=None, stream=None) -> None:
     """Positions of the keys that stay, kept int32 [batch, n], by their weights
@@ -1300,6 +1353,33 @@ def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> 
         mla_pages_copy(src_pool, src_pool.shape[0], src_kind, dst_pool, dst_pool.shape[0],
                        dst_kind, lists_d[0], lists_d[1], n,
                        rows=lists_d[2] if rows is not None else None)
+
+
+def key_weights(q, kv_pages, page_table, kv_lens, lse, *, num_heads: int, q_len: int, causal: bool,
+                softmax_scale: float, q_scale: float = 1.0, kv_scale: float = 1.0, previous=None,
+                decay: float = 1.0, query_lens=None, stream=None):
+    """Run mla_key_weights with the arguments and the LSE of a decode; kv_lens is a
+    host sequence.  previous float32 [batch, keys] is updated in place, or zeros as
+    wide as the longest request are; returns it."""
+    import torch
+    dev = q.device
+    lens = _host_ids(kv_lens.cpu() if hasattr(kv_lens, "cpu") else kv_lens, "kv_lens")
+    batch = lens.shape[0]
+    weights = previous
+    if weights is None:
+        weights = torch.zeros((batch, max(1, int(lens.max()) if batch else 1)), dtype=torch.float32,
+                              device=dev)
+    if query_lens is not None:
+        query_lens = torch.as_tensor(query_lens, dtype=torch.int32).to(dev).contiguous()
+    status = torch.zeros((1,), dtype=torch.int32, device=dev)
+    mla_key_weights(q, kv_pages, kv_pages.shape[0], page_table, page_table.shape[1],
+                    torch.from_numpy(lens).to(dev), lse, weights, batch, q_len, num_heads, causal,
+                    q_scale, kv_scale, softmax_scale, cache_kind=_cache_kind(kv_pages),
+                    previous=previous, decay=decay, query_lens=query_lens, status=status,
+                    stream=stream)
+    _check_status_tensor(status, stream, "key_weights: a length, query count or page id is out of "
+                                         "range, or a device wait ran out")
+    return weights
 
 
 def verify_drafts(target_probs, draft_tokens, uniforms, *, draft_probs=None, query_lens=None,

@@ -14,7 +14,7 @@ SOURCES = [os.path.join(CSRC, "mla_decode.cu"), os.path.join(CSRC, "mla_decode_b
            os.path.join(CSRC, "mla_shared.cu"), os.path.join(CSRC, "mla_shared_fp4.cu"),
            os.path.join(CSRC, "mla_merge.cu"), os.path.join(CSRC, "kv_append.cu"),
            os.path.join(CSRC, "prologue.cu"), os.path.join(CSRC, "pages.cu"),
-           os.path.join(CSRC, "verify.cu"), os.path.join(CSRC, "evict.cu"),
+           os.path.join(CSRC, "key_weights.cu"), os.path.join(CSRC, "verify.cu"), os.path.join(CSRC, "evict.cu"),
            os.path.join(CSRC, "page_pool.cpp"), os.path.join(CSRC, "plan.cpp")]
 OBJ_DIR = os.path.join(HERE, "_build")
 DEPENDS = SOURCES + [

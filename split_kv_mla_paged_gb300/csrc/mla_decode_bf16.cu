@@ -38,22 +38,6 @@ constexpr uint32_t kRopeOffB = 8 * kBlkBytesB;              // block 8 = rope
 constexpr uint32_t kPageBlkBytesB = MLA_PAGE_SIZE * 128;    // 4096: one page of one block
 constexpr uint32_t kPageBytesB = MLA_PAGE_SIZE * kRowBytesB;
 
-// Instruction descriptor for kind::f16 with BF16 A and B, fp32 D.
-__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, uint32_t a_mn,
-                                                  uint32_t b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) |
-         ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // tcgen05.mma kind::f16 with the A operand in TMEM (lane = row, two 16-bit
 // elements per 32-bit column, element 2c in the low half; K = 16 elements =
 // 8 columns per instruction).
