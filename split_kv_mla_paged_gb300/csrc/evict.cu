@@ -8,13 +8,14 @@
 // above T stays, and of those equal to T the first ones by position.
 //
 // It must read 4 bytes per key and write 4 (8 with weights) per kept key.  A
-// cluster takes a request, each CTA a contiguous slice of it, whose keys stay in
-// shared memory where they fit, so that the four passes read device memory once.
-// The counts are joined in the first CTA of the cluster.
+// cluster takes a request, each CTA a contiguous slice of it, whose weights stay in
+// shared memory where they fit, so that the three passes over all keys (count the
+// first digit, list the keys that have the wanted one, write) read device memory
+// once; the other digits are counted in the short list.  The counts are joined in
+// the first CTA of the cluster.
 //
-// Move.  Bytes only: a warp copies 288 16-byte vectors of 8 E4M3 or 4 BF16 rows at
-// a time, nine per lane and all in flight; a page of the 4-bit cache (three planes)
-// is one warp's work, so that the scale plane is written in whole sectors.
+// Move.  Bytes only: a warp copies the 288 16-byte vectors of 8 E4M3 or 4 BF16 rows,
+// nine per lane and all in flight, or 8 rows of the 4-bit cache's three planes.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -28,11 +29,8 @@ namespace cg = cooperative_groups;
 
 namespace mla {
 
-constexpr int kEvictThreads = 1024;
-constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictMaxCluster = 16;
 constexpr int kEvictBins = 2048;
-constexpr int kEvictCached = 45056;  // keys of a slice that fit in shared memory (176 KB)
 
 struct EvictParams {
   const float* weights;
@@ -46,27 +44,58 @@ struct EvictParams {
   float* new_weights;
   int64_t new_weights_stride;
   int32_t* status;
-  int32_t cached;  // keys of a slice that the launch has shared memory for
+  int32_t cached;      // kCached: keys of a CTA's slice
+  int32_t candidates;  // candidates of a warp that shared memory holds
 };
 
 // Weights as integers of the same order; -0 as 0, NaN below all.
 __device__ __forceinline__ uint32_t evict_key(float w) {
   const uint32_t u = __float_as_uint(w + 0.0f);
-  if (w != w) return 0;
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return w == w ? k : 0u;
 }
+constexpr uint32_t kEvictProtected = 0xFFFFFFFFu;  // above every number's key
 
-__global__ void __launch_bounds__(kEvictThreads, 1) mla_evict_select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t cache[];
-  __shared__ uint32_t hist[kEvictBins];      // of this CTA's slice
-  __shared__ uint32_t hist_all[kEvictBins];  // first CTA of the cluster: of all slices
-  __shared__ uint32_t warp_sum[kEvictWarps];
-  __shared__ uint32_t found[2];              // the digit, and how many of it are still wanted
+// Sums over the lanes below this one and over all lanes of four counts, a byte each
+// (sums to 128).  (With votes and their population counts, two a key, the passes took
+// twice as long: those counts issue at an eighth of the other integer operations.)
+__device__ __forceinline__ uint32_t scan_bytes(uint32_t n, int lane, uint32_t& total) {
+  uint32_t upto = n;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += v;
+  }
+  total = __shfl_sync(0xffffffffu, upto, 31);
+  return upto - n;
+}
+__device__ __forceinline__ uint32_t byte_of(uint32_t x, int m) { return (x >> (8 * m)) & 0xFFu; }
+
+// kCluster: several CTAs a request, whose counts meet in the first one; else the
+// CTA's own counts are the request's.  kCached: a CTA's slice of the weights is kept
+// in shared memory; else every pass reads it again, from L2.
+template <bool kCluster, int kThreads, bool kCached>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    mla_evict_select_kernel(const EvictParams p) {
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ uint32_t dynamic[];
+  // Counts of the digits: of this CTA (kCluster), and of the request, two digits'
+  // in turn, in the first CTA.
+  __shared__ uint32_t own[kCluster ? kEvictBins : 1];
+  __shared__ uint32_t hist[2][kEvictBins];
+  __shared__ uint32_t warp_sum[kWarps];
+  __shared__ uint32_t found[2];  // the digit, and how many of it are still wanted
   __shared__ uint32_t above_s[kEvictMaxCluster], equal_s[kEvictMaxCluster];
-  __shared__ uint32_t warp_above[kEvictWarps], warp_equal[kEvictWarps];
+  __shared__ uint32_t warp_above[kWarps], warp_equal[kWarps];
   cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = static_cast<int>(cluster.num_blocks());
-  const int rank = static_cast<int>(cluster.block_rank());
+  const int ranks = kCluster ? static_cast<int>(cluster.num_blocks()) : 1;
+  const int rank = kCluster ? static_cast<int>(cluster.block_rank()) : 0;
+  auto sync_all = [&]() {
+    if constexpr (kCluster)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
   const int b = blockIdx.x / ranks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = p.kv_lens[b];
@@ -74,137 +103,289 @@ __global__ void __launch_bounds__(kEvictThreads, 1) mla_evict_select_kernel(cons
   const int want = static_cast<int>(min(static_cast<int64_t>(min(len, budget)), p.kept_stride));
   const bool bad = len < 0 || len > p.weights_stride || budget < 0 ||
                    (p.new_weights && want > p.new_weights_stride);
+  const float* w = p.weights + b * p.weights_stride;
+  // This CTA's slice: each warp has a contiguous run of whole 128s, four keys a lane.
+  const int n = bad ? 0 : len;
+  const int per_warp = ((n + ranks * kWarps - 1) / (ranks * kWarps) + 127) / 128 * 128;
+  const int64_t run0 = static_cast<int64_t>(per_warp) * (rank * kWarps + warp);
+  const int k0 = static_cast<int>(min(run0, static_cast<int64_t>(n)));
+  const int k1 = static_cast<int>(min(run0 + per_warp, static_cast<int64_t>(n)));
+  uint32_t* my_cache = dynamic + warp * per_warp;
+  uint32_t* my_list = dynamic + (kCached ? p.cached : 0) + warp * p.candidates;
+  const bool vectors = (reinterpret_cast<uintptr_t>(w) & 15) == 0;  // runs start on 128s
+  if constexpr (kCached) {  // all of it in flight at once
+    if (vectors) {
+      for (int k = k0 + 4 * lane; k < k1; k += 128) {
+        const int bytes = min(16, 4 * (k1 - k));  // zeros behind the last weight
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         smem_u32(my_cache + (k - k0))),
+                     "l"(w + k), "r"(bytes)
+                     : "memory");
+      }
+    } else {
+      for (int k = k0 + lane; k < k1; k += 32)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                         smem_u32(my_cache + (k - k0))),
+                     "l"(w + k)
+                     : "memory");
+    }
+  }
+  for (int i = threadIdx.x; i < kEvictBins; i += kThreads) {
+    if constexpr (kCluster) own[i] = 0;
+    hist[0][i] = 0;
+    hist[1][i] = 0;
+  }
+  if constexpr (kCached) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  }
+  sync_all();  // counts are clear; kv_lens, which may be new_lens, has been read
   if (bad || want == 0) {  // the same for the whole cluster
-    cluster.sync();  // kv_lens may be new_lens
     if (rank == 0 && threadIdx.x == 0) {
       p.new_lens[b] = 0;
       if (bad && p.status) atomicCAS(p.status, 0, MLA_ERR_INVALID_ARG);
     }
     return;
   }
-  const float* w = p.weights + b * p.weights_stride;
-  // This CTA's slice: whole warps of 32 keys, each warp a contiguous run.
-  const int per_warp = ((len + ranks * kEvictWarps - 1) / (ranks * kEvictWarps) + 31) / 32 * 32;
-  const int64_t slice0 = static_cast<int64_t>(per_warp) * kEvictWarps * rank;
-  const int64_t run0 = slice0 + static_cast<int64_t>(per_warp) * warp;
-  const int k0 = static_cast<int>(min(run0, static_cast<int64_t>(len)));
-  const int k1 = static_cast<int>(min(run0 + per_warp, static_cast<int64_t>(len)));
-  const bool cached = per_warp * kEvictWarps <= p.cached;
-  uint32_t* my_cache = cache + warp * per_warp;
   const int tail = len - p.last;  // first protected key of the end (last may exceed len)
-  auto key_of = [&](int k, float v) -> uint32_t {
-    return (k < p.first || k >= tail) ? 0xFFFFFFFFu : evict_key(v);
-  };
-  // fn(key index, key) for every key of this warp's run, 32 at a time; fn runs on
-  // all lanes (valid = false past the run's end).
-  auto each = [&](auto fn, bool from_cache) {
-    constexpr int kBatch = 8;
-    for (int base = k0; base < k1; base += 32 * kBatch) {
-      uint32_t v[kBatch];
+  // Keys of positions k .. k + 3 from their weights.  Behind the end they are 0, which
+  // no weight is ranked below: as positions behind all others, they never stay.
+  auto keys_of = [&](int base, int k, const float (&v)[4], uint32_t (&key)[4]) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int k = base + u * 32 + lane;
-        if (from_cache)
-          v[u] = k < k1 ? my_cache[k - k0] : 0;
-        else
-          v[u] = k < k1 ? key_of(k, w[k]) : 0;
+    for (int u = 0; u < 4; ++u) key[u] = evict_key(v[u]);
+    if (base < p.first || base + 128 > min(tail, k1)) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (k + u < p.first || k + u >= tail) key[u] = kEvictProtected;
+        if (k + u >= k1) key[u] = 0;
       }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (base + u * 32 < k1) fn(base + u * 32 + lane, v[u], base + u * 32 + lane < k1);
     }
   };
-  uint32_t prefix = 0, mask = 0;            // digits of T found so far
-  uint32_t need = static_cast<uint32_t>(want);  // how many keys with that prefix stay
-  if (want == len) {
-    prefix = 0;  // all stay: as if every key equalled T
-  } else {
-#pragma unroll 1
-    for (int d = 0; d < 3; ++d) {
-      const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
-      const int bins = d == 2 ? 1024 : 2048;
-      for (int i = threadIdx.x; i < bins; i += kEvictThreads) {
-        hist[i] = 0;
-        if (rank == 0) hist_all[i] = 0;
-      }
-      __syncthreads();
-      each(
-          [&](int k, uint32_t key, bool valid) {
-            if (d == 0 && cached && valid) my_cache[k - k0] = key;
-            const bool in = valid && (key & mask) == prefix;
-            const uint32_t vote = __ballot_sync(0xffffffffu, in);
-            if (vote == 0) return;
-            const uint32_t bin = (key >> shift) & (bins - 1);
-            // A warp whose keys share the digit counts once: equal weights (zeros)
-            // would otherwise queue up behind one counter.
-            const uint32_t lead = __shfl_sync(0xffffffffu, bin, __ffs(vote) - 1);
-            if (__all_sync(0xffffffffu, !in || bin == lead)) {
-              if (lane == 0) atomicAdd(&hist[lead], __popc(vote));
-            } else if (in) {
-              atomicAdd(&hist[bin], 1u);
-            }
-          },
-          d > 0 && cached);
-      cluster.sync();  // hist_all is clear, and this slice is counted
-      uint32_t* all = cluster.map_shared_rank(hist_all, 0);
-      for (int i = threadIdx.x; i < bins; i += kEvictThreads)
-        if (hist[i]) atomicAdd(&all[i], hist[i]);
-      cluster.sync();
-      if (rank == 0) {
-        // Two bins a thread, from the highest down: the one where the count from
-        // above reaches `need`.
-        const int hi = bins - 1 - 2 * static_cast<int>(threadIdx.x);
-        const uint32_t c0 = hi >= 0 ? hist_all[hi] : 0, c1 = hi >= 1 ? hist_all[hi - 1] : 0;
-        uint32_t upto = c0 + c1;
+  auto load4 = [&](int k, bool whole, float (&v)[4]) {
+    if (whole) {
+      const float4 x = *reinterpret_cast<const float4*>(w + k);
+      v[0] = x.x;
+      v[1] = x.y;
+      v[2] = x.z;
+      v[3] = x.w;
+    } else {
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const uint32_t v = __shfl_up_sync(0xffffffffu, upto, off);
-          if (lane >= off) upto += v;
-        }
-        if (lane == 31) warp_sum[warp] = upto;
-        __syncthreads();
-        uint32_t above = upto - (c0 + c1);
-        for (int i = 0; i < warp; ++i) above += warp_sum[i];
-        uint32_t digit = 0xFFFFFFFFu, rest = 0;
-        if (above < need && above + c0 >= need) {
-          digit = hi;
-          rest = need - above;
-        } else if (above + c0 < need && above + c0 + c1 >= need) {
-          digit = hi - 1;
-          rest = need - above - c0;
-        }
-        if (digit != 0xFFFFFFFFu)
-          for (int r = 0; r < ranks; ++r) {
-            uint32_t* f = cluster.map_shared_rank(found, r);
-            f[0] = digit;
-            f[1] = rest;
-          }
-      }
-      cluster.sync();
-      prefix |= found[0] << shift;
-      mask |= static_cast<uint32_t>(bins - 1) << shift;
-      need = found[1];
+      for (int u = 0; u < 4; ++u) v[u] = k + u < k1 ? w[k + u] : 0.0f;
     }
-  }
-  // Keys above T (all stay) and equal to T (the first `need` stay), per warp and CTA.
+  };
+  // fn(position of the lane's first key, its keys) for this warp's run, 512 keys at a
+  // time: keys [m][u] are positions + 128 m + u.  Keys behind the run are 0.
+  constexpr int kBatch = 4;
+  auto each = [&](auto fn) {
+    for (int base = k0; base < k1; base += 128 * kBatch) {
+      uint32_t key[kBatch][4];
+      if constexpr (kCached) {
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (base + 128 * m < k1)
+            x = *reinterpret_cast<const uint4*>(my_cache + (base + 128 * m - k0) + 4 * lane);
+          key[m][0] = x.x;
+          key[m][1] = x.y;
+          key[m][2] = x.z;
+          key[m][3] = x.w;
+        }
+      } else {
+        float v[kBatch][4];
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m)
+          load4(base + 128 * m + 4 * lane, vectors && base + 128 * (m + 1) <= k1, v[m]);
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m)
+          keys_of(base + 128 * m, base + 128 * m + 4 * lane, v[m], key[m]);
+      }
+      fn(base + 4 * lane, key);
+    }
+  };
+  // Counts a digit.  A warp whose keys share it counts once: equal weights (zeros)
+  // would otherwise queue up behind one counter.
+  auto count = [&](uint32_t* bins, uint32_t bin, bool in, uint32_t vote) {
+    const uint32_t lead = __shfl_sync(0xffffffffu, bin, __ffs(vote) - 1);
+    if (__all_sync(0xffffffffu, !in || bin == lead)) {
+      if (lane == 0) atomicAdd(&bins[lead], __popc(vote));
+    } else if (in) {
+      atomicAdd(&bins[bin], 1u);
+    }
+  };
   const bool all_stay = want == len;
-  uint32_t above = 0, equal = 0;
-  if (all_stay) {
-    equal = static_cast<uint32_t>(k1 - k0);
+  uint32_t prefix = 0;                          // digits of T found so far
+  uint32_t need = static_cast<uint32_t>(want);  // how many keys with those digits stay
+  uint32_t above = 0, equal = 0;                // this warp's keys above T, equal to T
+  // Joins the counts of digit d and finds it: the one where the count from the
+  // highest down reaches `need`.
+  auto find = [&](int d, int bins) -> uint32_t {
+    __syncthreads();
+    if constexpr (kCluster) {
+      uint32_t* to = cluster.map_shared_rank(&hist[d & 1][0], 0);
+      for (int i = threadIdx.x; i < bins; i += kThreads) {
+        const uint32_t c = own[i];
+        if (c) {
+          atomicAdd(&to[i], c);
+          own[i] = 0;
+        }
+      }
+      cluster.sync();
+    }
+    if (rank == 0) {
+      uint32_t* h = hist[d & 1];
+      // Each thread kEach digits, from the highest down.
+      constexpr int kEach = kEvictBins / kThreads;
+      const int hi = bins - 1 - kEach * static_cast<int>(threadIdx.x);
+      uint32_t c[kEach], mine = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        c[i] = hi >= i ? h[hi - i] : 0;
+        mine += c[i];
+      }
+      if (d == 0) {  // clear for the third digit; only this thread reads these
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) h[hi - i] = 0;
+      }
+      uint32_t upto = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += v;
+      }
+      if (lane == 31) warp_sum[warp] = upto;
+      __syncthreads();
+      uint32_t before = lane < warp ? warp_sum[lane] : 0;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+      before += upto - mine;
+      if (before < need && before + mine >= need) {
+        uint32_t digit = 0, rest = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          if (before < need && before + c[i] >= need) {
+            digit = static_cast<uint32_t>(hi - i);
+            rest = need - before;
+          }
+          before += c[i];
+        }
+        for (int r = 0; r < ranks; ++r) {
+          uint32_t* f = kCluster ? cluster.map_shared_rank(&found[0], r) : found;
+          f[0] = digit;
+          f[1] = rest;
+        }
+      }
+    }
+    sync_all();
+    need = found[1];
+    return found[0];
+  };
+  if (!all_stay) {
+    {
+      uint32_t* to = kCluster ? own : hist[0];
+      auto count4 = [&](const uint32_t (&key)[4]) {
+        const uint32_t c0 = key[0] >> 21, c1 = key[1] >> 21, c2 = key[2] >> 21, c3 = key[3] >> 21;
+        if (c0 == c1 && c0 == c2 && c0 == c3) {  // equal weights (zeros) queue up less
+          atomicAdd(&to[c0], 4u);
+        } else {
+          atomicAdd(&to[c0], 1u);
+          atomicAdd(&to[c1], 1u);
+          atomicAdd(&to[c2], 1u);
+          atomicAdd(&to[c3], 1u);
+        }
+      };
+      if constexpr (kCached) {
+        for (int base = k0; base < k1; base += 128) {
+          uint4* at = reinterpret_cast<uint4*>(my_cache + (base - k0) + 4 * lane);
+          const uint4 x = *at;
+          const float v[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
+                              __uint_as_float(x.w)};
+          uint32_t key[4];
+          keys_of(base, base + 4 * lane, v, key);
+          *at = make_uint4(key[0], key[1], key[2], key[3]);
+          count4(key);
+        }
+      } else {
+        each([&](int k, const uint32_t (&key)[kBatch][4]) {
+#pragma unroll
+          for (int m = 0; m < kBatch; ++m)
+            if (k + 128 * m - 4 * lane < k1) count4(key[m]);
+        });
+      }
+    }
+    const uint32_t top = find(0, 2048);
+    prefix = top << 21;
+    // Keys with that first digit are the candidates; those above it stay.
+    uint32_t listed = 0;
+    const uint32_t room = static_cast<uint32_t>(p.candidates);
+    each([&](int, const uint32_t (&key)[kBatch][4]) {
+      uint32_t is = 0;
+#pragma unroll
+      for (int m = 0; m < kBatch; ++m)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (key[m][u] > (prefix | 0x1FFFFFu)) ++above;
+          if (key[m][u] - prefix < 0x200000u) ++is;
+        }
+      uint32_t all;  // (as one byte pair: up to 16 a lane, 512 in all)
+      uint32_t at = listed + scan_bytes(is, lane, all);
+      listed += all;
+      if (listed <= room && is) {  // (a list that is too short is not read)
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (key[m][u] - prefix < 0x200000u) my_list[at++] = key[m][u];
+      }
+    });
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) above += __shfl_xor_sync(0xffffffffu, above, off);
+    __syncwarp();
+    // fn(key, in) for the candidates, from the list, or from the run where it was
+    // too short.
+    auto each_candidate = [&](auto fn) {
+      if (listed <= room) {
+        for (uint32_t i = 0; i < listed; i += 32) {
+          const bool in = i + lane < listed;
+          fn(in ? my_list[i + lane] : 0u, in);
+        }
+      } else {
+        each([&](int k, const uint32_t (&key)[kBatch][4]) {
+#pragma unroll
+          for (int m = 0; m < kBatch; ++m)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              fn(key[m][u], k + 128 * m + u < k1 && key[m][u] >> 21 == top);
+        });
+      }
+    };
+#pragma unroll 1
+    for (int d = 1; d < 3; ++d) {
+      const int shift = d == 1 ? 10 : 0, bins = d == 1 ? 2048 : 1024;
+      const uint32_t mask = d == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+      uint32_t* to = kCluster ? own : hist[d & 1];
+      each_candidate([&](uint32_t key, bool in) {
+        in = in && (key & mask) == prefix;
+        const uint32_t vote = __ballot_sync(0xffffffffu, in);
+        if (vote) count(to, (key >> shift) & (bins - 1), in, vote);
+      });
+      prefix |= find(d, bins) << shift;
+    }
+    each_candidate([&](uint32_t key, bool in) {
+      above += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
+      equal += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
+    });
   } else {
-    each(
-        [&](int, uint32_t key, bool valid) {
-          above += __popc(__ballot_sync(0xffffffffu, valid && key > prefix));
-          equal += __popc(__ballot_sync(0xffffffffu, valid && key == prefix));
-        },
-        cached);
+    above = static_cast<uint32_t>(k1 - k0);
   }
+  // Where this run's first kept key goes: keys above T all stay, of those equal to T
+  // the first `need`.
   if (lane == 0) {
     warp_above[warp] = above;
     warp_equal[warp] = equal;
   }
   __syncthreads();
-  uint32_t cta_above = warp_above[lane], cta_equal = warp_equal[lane];
+  uint32_t cta_above = lane < kWarps ? warp_above[lane % kWarps] : 0;
+  uint32_t cta_equal = lane < kWarps ? warp_equal[lane % kWarps] : 0;
   uint32_t before_above = lane < warp ? cta_above : 0, before_equal = lane < warp ? cta_equal : 0;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
@@ -213,35 +394,78 @@ __global__ void __launch_bounds__(kEvictThreads, 1) mla_evict_select_kernel(cons
     before_above += __shfl_xor_sync(0xffffffffu, before_above, off);
     before_equal += __shfl_xor_sync(0xffffffffu, before_equal, off);
   }
-  if (warp == 0 && lane < ranks) {
-    cluster.map_shared_rank(above_s, lane)[rank] = cta_above;
-    cluster.map_shared_rank(equal_s, lane)[rank] = cta_equal;
+  if constexpr (kCluster) {
+    if (warp == 0 && lane < ranks) {
+      cluster.map_shared_rank(above_s, lane)[rank] = cta_above;
+      cluster.map_shared_rank(equal_s, lane)[rank] = cta_equal;
+    }
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+      before_above += above_s[r];
+      before_equal += equal_s[r];
+    }
   }
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) {
-    before_above += above_s[r];
-    before_equal += equal_s[r];
-  }
-  uint32_t at = before_above + min(before_equal, need);  // where this run's first kept key goes
+  // What follows on the stream (the rows' move) may be made ready.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  uint32_t at = before_above + min(before_equal, need);
   int32_t* kept = p.kept + b * p.kept_stride;
   float* new_weights = p.new_weights ? p.new_weights + b * p.new_weights_stride : nullptr;
-  const uint32_t below = (1u << lane) - 1u;
-  each(
-      [&](int k, uint32_t key, bool valid) {
-        const bool eq = valid && (all_stay || key == prefix);
-        const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-        const bool stay = (valid && !all_stay && key > prefix) ||
-                          (eq && before_equal + __popc(eqs & below) < need);
-        const uint32_t stays = __ballot_sync(0xffffffffu, stay);
-        if (stay) {
-          const uint32_t to = at + __popc(stays & below);
-          kept[to] = k;
-          if (new_weights) new_weights[to] = w[k];
+  if (all_stay) {
+    for (int k = k0 + lane; k < k1; k += 32) {
+      kept[k] = k;
+      if (new_weights) new_weights[k] = w[k];
+    }
+  } else if (above + equal > 0) {
+    each([&](int k, const uint32_t (&key)[kBatch][4]) {
+      uint32_t stay = 0;             // a bit per key
+      uint32_t stays = 0, ties = 0;  // a byte per block of 128
+#pragma unroll
+      for (int m = 0; m < kBatch; ++m)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (key[m][u] > prefix) {
+            stay |= 1u << (4 * m + u);
+            stays += 1u << (8 * m);
+          }
+          if (key[m][u] == prefix) ties += 1u << (8 * m);
         }
-        at += __popc(stays);
-        before_equal += __popc(eqs);
-      },
-      cached && !all_stay);
+      if (__any_sync(0xffffffffu, ties)) {
+        uint32_t all;
+        const uint32_t place = scan_bytes(ties, lane, all);
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m) {
+          uint32_t rank_of = before_equal + byte_of(place, m);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (key[m][u] == prefix && rank_of++ < need) {
+              stay |= 1u << (4 * m + u);
+              stays += 1u << (8 * m);
+            }
+          before_equal += byte_of(all, m);
+        }
+      }
+      uint32_t all;
+      const uint32_t place = scan_bytes(stays, lane, all);
+#pragma unroll
+      for (int m = 0; m < kBatch; ++m) {
+        uint32_t to = at + byte_of(place, m);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (stay >> (4 * m + u) & 1u) {
+            kept[to] = k + 128 * m + u;
+            if (new_weights) {
+              // The weight back from its key, but for keys that several weights have.
+              const uint32_t x = key[m][u];
+              float v = __uint_as_float(x & 0x80000000u ? x ^ 0x80000000u : ~x);
+              if (x == kEvictProtected || x == 0x80000000u || x == 0) v = w[k + 128 * m + u];
+              new_weights[to] = v;
+            }
+            ++to;
+          }
+        at += byte_of(all, m);
+      }
+    });
+  }
   if (rank == 0 && threadIdx.x == 0) p.new_lens[b] = want;
 }
 
@@ -292,6 +516,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) mla_rows_move_kernel(const Mo
   constexpr int kRows = 288 / kVecs;  // rows of a warp
   constexpr int kEach = 9;            // vectors of a lane
   static_assert(kRows * kVecs == 32 * kEach, "whole vectors per lane");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 31;
   const int row0 = (blockIdx.x * kMoveWarps + static_cast<int>(threadIdx.x >> 5)) * kRows;
@@ -316,63 +541,59 @@ __global__ void __launch_bounds__(32 * kMoveWarps) mla_rows_move_kernel(const Mo
   }
 }
 
-// A destination page of the 4-bit cache per warp; lane r looks after row r.
+// The 4-bit cache: a page per CTA, eight rows a warp (a warp per page took 21.4 us
+// where this takes 15.6, 131,072 rows).  Codes are 16 vectors a row, the rope part
+// four; of the scales a lane copies four blocks' bytes of one row, the lanes of eight
+// rows side by side.
 __global__ void __launch_bounds__(32 * kMoveWarps) mla_rows_move_fp4_kernel(const MoveParams p) {
+  static_assert(kMoveWarps == 4, "a page per CTA");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 31;
-  const int row0 = (blockIdx.x * kMoveWarps + static_cast<int>(threadIdx.x >> 5)) * MLA_PAGE_SIZE;
-  const int n = min(MLA_PAGE_SIZE, move_count(p, b) - row0);
+  const int row0 = blockIdx.x * MLA_PAGE_SIZE + static_cast<int>(threadIdx.x >> 5) * 8;
+  const int n = min(8, move_count(p, b) - row0);
   if (n <= 0) return;
   int64_t from = -1, to = 0;
   if (lane < n && !move_row(p, b, row0 + lane, from, to)) from = -1;
-  const bool mine = from >= 0;
-  // Addresses of a row's parts: its page, and its slot times the part's row size.
-  const uint8_t* src = p.src + (from >> 5) * MLA_FP4_PAGE_BYTES;
-  uint8_t* dst = p.dst + (to >> 5) * MLA_FP4_PAGE_BYTES;
-  const int ss = static_cast<int>(from & 31), ds = static_cast<int>(to & 31);
-  uint8_t sc[kFp4Blocks];
+  uint4 code[4], rope;
+  uint8_t scale[4];
+  // Part `k` of a lane's row r: its offsets in the source and the destination.
+  auto page_at = [](int64_t place) { return (place >> 5) * MLA_FP4_PAGE_BYTES; };
+  int64_t code_from[4], code_to[4];
 #pragma unroll
-  for (int k = 0; k < kFp4Blocks; ++k)
-    sc[k] = mine ? src[kFp4ScaleOffset + k * MLA_PAGE_SIZE + ss] : 0;
-  const uint64_t src_codes = reinterpret_cast<uint64_t>(src + ss * kFp4RowCodes);
-  const uint64_t src_rope = reinterpret_cast<uint64_t>(src + kFp4RopeOffset + ss * MLA_ROPE_DIM);
-  const uint64_t dst_codes = reinterpret_cast<uint64_t>(dst + ds * kFp4RowCodes);
-  const uint64_t dst_rope = reinterpret_cast<uint64_t>(dst + kFp4RopeOffset + ds * MLA_ROPE_DIM);
-  // Codes: 16 vectors a row, two rows at a time; 8 steps in flight.
-#pragma unroll 1
-  for (int r0 = 0; r0 < n; r0 += 16) {
-    uint4 v[8];
-    uint64_t d[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int r = r0 + 2 * u + (lane >> 4);
-      const uint64_t s = __shfl_sync(0xffffffffu, src_codes, r & 31);
-      d[u] = __shfl_sync(0xffffffffu, mine ? dst_codes : 0, r & 31);
-      if (r >= n) d[u] = 0;
-      if (d[u]) v[u] = reinterpret_cast<const uint4*>(s)[lane & 15];
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (d[u]) reinterpret_cast<uint4*>(d[u])[lane & 15] = v[u];
+  for (int u = 0; u < 4; ++u) {
+    const int r = 2 * u + (lane >> 4);
+    const int64_t f = __shfl_sync(0xffffffffu, from, r), t = __shfl_sync(0xffffffffu, to, r);
+    code_from[u] = f < 0 ? -1 : page_at(f) + (f & 31) * kFp4RowCodes + (lane & 15) * 16;
+    code_to[u] = page_at(t) + (t & 31) * kFp4RowCodes + (lane & 15) * 16;
   }
-  {
-    uint4 v[4];
-    uint64_t d[4];
+  const int64_t rope_f = __shfl_sync(0xffffffffu, from, lane >> 2);
+  const int64_t rope_t = __shfl_sync(0xffffffffu, to, lane >> 2);
+  const int64_t scale_f = __shfl_sync(0xffffffffu, from, lane & 7);
+  const int64_t scale_t = __shfl_sync(0xffffffffu, to, lane & 7);
+  const uint8_t* scale_src = p.src + page_at(scale_f) + kFp4ScaleOffset + (scale_f & 31) +
+                             (lane >> 3) * MLA_PAGE_SIZE;
+  uint8_t* scale_dst = p.dst + page_at(scale_t) + kFp4ScaleOffset + (scale_t & 31) +
+                       (lane >> 3) * MLA_PAGE_SIZE;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = 8 * u + (lane >> 2);
-      const uint64_t s = __shfl_sync(0xffffffffu, src_rope, r);
-      d[u] = __shfl_sync(0xffffffffu, mine ? dst_rope : 0, r);
-      if (d[u]) v[u] = reinterpret_cast<const uint4*>(s)[lane & 3];
-    }
+  for (int u = 0; u < 4; ++u)
+    if (code_from[u] >= 0) code[u] = *reinterpret_cast<const uint4*>(p.src + code_from[u]);
+  if (rope_f >= 0)
+    rope = *reinterpret_cast<const uint4*>(p.src + page_at(rope_f) + kFp4RopeOffset +
+                                           (rope_f & 31) * MLA_ROPE_DIM + (lane & 3) * 16);
+  if (scale_f >= 0) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (d[u]) reinterpret_cast<uint4*>(d[u])[lane & 3] = v[u];
+    for (int u = 0; u < 4; ++u) scale[u] = scale_src[u * 4 * MLA_PAGE_SIZE];
   }
-  if (mine) {
 #pragma unroll
-    for (int k = 0; k < kFp4Blocks; ++k)
-      dst[kFp4ScaleOffset + k * MLA_PAGE_SIZE + ds] = sc[k];
+  for (int u = 0; u < 4; ++u)
+    if (code_from[u] >= 0) *reinterpret_cast<uint4*>(p.dst + code_to[u]) = code[u];
+  if (rope_f >= 0)
+    *reinterpret_cast<uint4*>(p.dst + page_at(rope_t) + kFp4RopeOffset +
+                              (rope_t & 31) * MLA_ROPE_DIM + (lane & 3) * 16) = rope;
+  if (scale_f >= 0) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) scale_dst[u * 4 * MLA_PAGE_SIZE] = scale[u];
   }
 }
 
@@ -403,34 +624,50 @@ extern "C" int mla_evict_select(const float* weights, int64_t weights_stride,
   }
   EvictParams p = {weights, weights_stride, kv_lens,  keep,        first,
                    last,    kept,           kept_stride, new_lens, new_weights,
-                   new_weights_stride, status, 0};
-  // CTAs per request: one up to 8,192 keys, 8 above, 16 where few requests have
-  // more than 8 slices' worth of cached keys each.
+                   new_weights_stride, status, 0, 0};
+  // CTAs per request: one up to 8,192 keys; 8 above, of 512 threads, so that two fit
+  // an SM (clusters of 8 leave SMs of a GPC without a place: 16 of 1024 threads took
+  // two waves); 16 of 1024 where few requests have more keys than 8 such CTAs keep.
+  constexpr int64_t kKeep = 18432;  // weights that a CTA of 512 threads keeps (72 KB)
   int ranks = weights_stride <= 8192 ? 1 : 8;
-  if (batch <= 9 && weights_stride > 8 * static_cast<int64_t>(kEvictCached)) ranks = 16;
-  const int64_t slice =
-      ((weights_stride + ranks * kEvictWarps - 1) / (ranks * kEvictWarps) + 31) / 32 * 32 *
-      kEvictWarps;
-  p.cached = static_cast<int32_t>(slice <= kEvictCached ? slice : 0);
-  static std::atomic<uint64_t> attr_done{0}, attr2_done{0};
-  cudaError_t e = ensure_smem_attr(mla_evict_select_kernel, kEvictCached * 4, attr_done);
+  if (batch <= 9 && weights_stride > 8 * kKeep) ranks = 16;
+  const int threads = ranks == 8 ? 512 : 1024, warps = threads / 32;
+  const int64_t per_warp =
+      ((weights_stride + ranks * warps - 1) / (ranks * warps) + 127) / 128 * 128;
+  const int64_t slice = per_warp * warps;
+  // Shared memory besides the counts: 86 KB where two CTAs share an SM, else 190 KB;
+  // at least 4,096 candidates.
+  const int64_t room = ranks == 8 ? 22016 : 48640;
+  const bool cached = slice <= room - 4096;
+  p.cached = static_cast<int32_t>(cached ? slice : 0);
+  const int64_t list = (room - p.cached) / warps;
+  p.candidates = static_cast<int32_t>(list < per_warp ? list : per_warp);
+  const auto kernel =
+      ranks == 1   ? mla_evict_select_kernel<false, 1024, true>
+      : ranks == 8 ? (cached ? mla_evict_select_kernel<true, 512, true>
+                             : mla_evict_select_kernel<true, 512, false>)
+                   : (cached ? mla_evict_select_kernel<true, 1024, true>
+                             : mla_evict_select_kernel<true, 1024, false>);
+  static std::atomic<uint64_t> attr_done[5], wide_done[2];
+  const int which = ranks == 1 ? 0 : (ranks == 8 ? 1 : 3) + (cached ? 0 : 1);
+  cudaError_t e = ensure_smem_attr(kernel, static_cast<int>(room * 4), attr_done[which]);
   if (e != cudaSuccess) return cuda_fail("mla_evict_select: set-up", e);
   if (ranks > 8) {
     int dev = 0;
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail("mla_evict_select: set-up", e);
     const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-    if (!bit || !(attr2_done.load() & bit)) {
-      e = cudaFuncSetAttribute(mla_evict_select_kernel,
-                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (!bit || !(wide_done[cached].load() & bit)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return cuda_fail("mla_evict_select: set-up", e);
-      attr2_done.fetch_or(bit);
+      wide_done[cached].fetch_or(bit);
     }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(batch * ranks));
-  cfg.blockDim = dim3(kEvictThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.cached) * 4;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes =
+      (static_cast<size_t>(p.cached) + static_cast<size_t>(p.candidates) * warps) * 4;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -438,8 +675,8 @@ extern "C" int mla_evict_select(const float* weights, int64_t weights_stride,
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, mla_evict_select_kernel, p);
+  cfg.numAttrs = ranks == 1 ? 0 : 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return cuda_fail("mla_evict_select: launch", e);
   return MLA_OK;
 }
@@ -476,17 +713,25 @@ extern "C" int mla_rows_move(const void* src_pool, int64_t src_pages, const int3
                         reinterpret_cast<uint8_t*>(dst_pool),
                         src_pages, dst_pages, src_table, dst_table, src_max_pages, dst_max_pages,
                         kept, kept_stride, counts, status};
-  const int rows = cache_kind == MLA_CACHE_FP4 ? 32 : cache_kind == MLA_CACHE_FP8 ? 8 : 4;
-  const dim3 grid(static_cast<unsigned>((kept_stride + rows * kMoveWarps - 1) / (rows * kMoveWarps)),
-                  static_cast<unsigned>(batch));
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (cache_kind == MLA_CACHE_FP8)
-    mla_rows_move_kernel<576><<<grid, 32 * kMoveWarps, 0, st>>>(p);
-  else if (cache_kind == MLA_CACHE_BF16)
-    mla_rows_move_kernel<1152><<<grid, 32 * kMoveWarps, 0, st>>>(p);
-  else
-    mla_rows_move_fp4_kernel<<<grid, 32 * kMoveWarps, 0, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const int rows = cache_kind == MLA_CACHE_FP4 ? 8 : cache_kind == MLA_CACHE_FP8 ? 8 : 4;
+  // Launched as a programmatic dependent, so that it is ready when a selection before
+  // it ends; the kernels wait for what precedes them on the stream first.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim =
+      dim3(static_cast<unsigned>((kept_stride + rows * kMoveWarps - 1) / (rows * kMoveWarps)),
+           static_cast<unsigned>(batch));
+  cfg.blockDim = dim3(32 * kMoveWarps);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg,
+                                           cache_kind == MLA_CACHE_FP8    ? mla_rows_move_kernel<576>
+                                           : cache_kind == MLA_CACHE_BF16 ? mla_rows_move_kernel<1152>
+                                                                          : mla_rows_move_fp4_kernel,
+                                           p);
   if (e != cudaSuccess) return cuda_fail("mla_rows_move: launch", e);
   return MLA_OK;
 }
