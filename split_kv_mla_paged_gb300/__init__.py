@@ -630,15 +630,16 @@ def _device_tensor(t, name: str, device: int, dtype=None, least: int = 0, contig
     number of elements."""
     if t is None:
         return None
+    if (t.get_device() == device and (dtype is None or t.dtype is dtype)
+            and (not contiguous or t.is_contiguous()) and (not least or t.numel() >= least)):
+        return t.data_ptr()
     if t.get_device() != device:
         raise ValueError(f"{name} must be a CUDA tensor on device {device}, like the call's others")
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() < least:
-        raise ValueError(f"{name} has {t.numel()} elements, this call needs {least}")
-    return t.data_ptr()
+    raise ValueError(f"{name} has {t.numel()} elements, this call needs {least}")
 
 
 _PAGE_BYTES = {CACHE_FP8: PAGE_SIZE * HEAD_DIM, CACHE_BF16: 2 * PAGE_SIZE * HEAD_DIM,
@@ -718,7 +719,7 @@ def mla_decode_shared(q, kv_pages, num_pages: int, page_table, max_pages_per_req
     q_at = _device_tensor(q, "q", dev, None, rows * HEAD_DIM)
     if q.element_size() != (2 if kind == CACHE_BF16 else 1):
         raise ValueError("q must be BF16 for a BF16 cache, E4M3 otherwise")
-    if _cache_kind(kv_pages) != kind:
+    if not _is_pool(kv_pages, kind):
         raise ValueError("kv_pages is not a pool of the plan's cache kind")
     opts = _fp4_options(
         _device_tensor(q_scale_dev, "q_scale_dev", dev, f32, 1),
@@ -744,11 +745,17 @@ def _probs(t, name: str, device: int, dtype, rows: int):
     """Address and strides of probabilities [batch, rows, vocab] with a dense last
     dimension.  Strides of dimensions of size 1 are immaterial."""
     ptr = _device_tensor(t, name, device, dtype, 0, False)
-    if t.dim() != 3 or t.shape[1] < rows or (t.shape[2] > 1 and t.stride(2) != 1):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [batch, {rows}, vocab]")
+    (n, have, vocab), (batch, row, last) = t.shape, t.stride()
+    if have < rows or (vocab > 1 and last != 1):
         raise ValueError(f"{name} must be [batch, {rows}, vocab] with a dense last dimension")
-    vocab = t.shape[2]
-    row = _row_stride(t, 1, name) if t.shape[1] > 1 else vocab
-    batch = _row_stride(t, 0, name) if t.shape[0] > 1 else max(rows, 1) * row
+    if have == 1:
+        row = vocab
+    if n == 1:
+        batch = max(rows, 1) * row
+    if row == 0 or batch == 0:
+        raise ValueError(f"{name} may not repeat one row (stride 0)")
     return ptr, batch, row
 
 
@@ -788,6 +795,19 @@ def mla_verify_drafts(target_probs, draft_tokens, uniforms, tokens_out, accepted
     _call_on(dev, load_library().mla_verify_drafts, ctypes.byref(a), stream=stream)
 
 
+def _is_pool(pool, kind: int) -> bool:
+    """Whether a tensor has the type and shape of a pool of this kind."""
+    import torch
+    shape, dtype = pool.shape, pool.dtype
+    if kind == CACHE_FP4:
+        return dtype is torch.uint8 and len(shape) == 2 and shape[1] == FP4_PAGE_BYTES
+    if len(shape) != 3 or shape[1] != PAGE_SIZE or shape[2] != HEAD_DIM:
+        return False
+    if kind == CACHE_BF16:
+        return dtype is torch.bfloat16
+    return kind == CACHE_FP8 and (dtype is torch.uint8 or dtype is torch.float8_e4m3fn)
+
+
 def _rows_of(t, name: str, device: int, dtype, batch: int):
     """Address, row stride and width of a [batch, n] tensor with dense rows."""
     if t is None:
@@ -814,7 +834,7 @@ def mla_key_weights(q, kv_pages, num_pages: int, page_table, max_pages_per_req: 
     q_at = _device_tensor(q, "q", dev, None, rows * HEAD_DIM)
     if q.element_size() != (2 if cache_kind == CACHE_BF16 else 1):
         raise ValueError("q must be BF16 for a BF16 cache, E4M3 otherwise")
-    if _cache_kind(kv_pages) != cache_kind:
+    if not _is_pool(kv_pages, cache_kind):
         raise ValueError("kv_pages is not a pool of cache_kind")
     w, w_stride = _rows_of(weights, "weights", dev, f32, batch)
     prev, prev_stride = _rows_of(previous, "previous", dev, f32, batch)

@@ -289,27 +289,40 @@ __device__ __forceinline__ int bf16_window_page(const DecodeParams& p, const Spl
 //  * P^T goes K-major (a row's 64 tokens = one 128-byte swizzled line) into
 //    the consumed rope block; PV is the swapped O^T += V^T P^T as before.
 // ---------------------------------------------------------------------------
+//
+// A decode over shared prefixes also runs it with 32 rows (NR_ = 32), four copies of
+// them in the lanes and 16 tokens a thread: Q takes the same 288 columns of TMEM, O^T
+// twice as many, which leaves room for one S buffer.  Its tile takes about the time
+// of the 16-row one (the MMAs read as much of K and V, the loads are the same), where
+// the 48-row kernel below takes 2.5 times as long.
+template <int NR_>
+struct CfgQ {
+  static constexpr int NR = NR_;
+  static_assert(NR == 16 || NR == 32, "NR");
+  static constexpr int NS = NR == 16 ? 2 : 1;  // S buffers
+  static constexpr int kTok = NR / 2;          // tokens of a softmax thread per tile
+  static constexpr int NST = 3;
+  static constexpr int kThreads = 96 + 128;  // TMA, QK issuer, PV issuer, softmax warpgroup
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kQCol = 0;                // 288 columns
+  static constexpr uint32_t kSCol = 288;              // NS x 64 columns
+  static constexpr uint32_t kOCol = kSCol + NS * 64;  // 4 x NR columns
+  static_assert(kOCol + 4 * NR <= kTmemCols, "TMEM");
+  static constexpr uint32_t kQStage = (NST - 1) * kTileBytesB;  // Q staged by TMA in the last stage
+  static constexpr uint32_t kAux = NST * kTileBytesB;
+  static constexpr uint32_t kBars = kAux;  // 17 x 8 B
+  static constexpr uint32_t kTmemSlot = kAux + 136;
+  static constexpr uint32_t kFlags = kAux + 144;
+  static constexpr uint32_t kStageInfo = kAux + 160;           // NST x 4 B: rows loaded per page
+  static constexpr uint32_t kRedMax = kAux + 176;              // 4 warps x NR rows
+  static constexpr uint32_t kRedSum = kRedMax + 16 * NR;       // 2 x 4 x NR
+  static constexpr uint32_t kKref = kRedSum + 32 * NR;         // NR
+  static constexpr uint32_t kAlpha = kKref + 4 * NR;           // NR
+  static constexpr uint32_t kEnd = kAlpha + 4 * NR;
+  static constexpr uint32_t kSmemBytes = kEnd + 1024;
+  static_assert(kSmemBytes <= 232448u, "shared memory");
+};
 namespace q16 {
-constexpr int NR = 16;
-constexpr int NST = 3;
-constexpr int kThreads = 96 + 128;  // TMA, QK issuer, PV issuer, softmax warpgroup
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kQCol = 0;      // 288 columns
-constexpr uint32_t kSCol = 288;    // 2 x 64 columns
-constexpr uint32_t kOCol = 416;    // 4 x 16 columns
-constexpr uint32_t kQStage = (NST - 1) * kTileBytesB;  // Q staged by TMA in the last stage
-constexpr uint32_t kAux = NST * kTileBytesB;
-constexpr uint32_t kBars = kAux;               // 17 x 8 B
-constexpr uint32_t kTmemSlot = kAux + 136;
-constexpr uint32_t kFlags = kAux + 144;
-constexpr uint32_t kStageInfo = kAux + 160;    // NST x 4 B: rows loaded per page
-constexpr uint32_t kRedMax = kAux + 176;       // 4 warps x 16 rows
-constexpr uint32_t kRedSum = kRedMax + 256;    // 2 x 4 x 16
-constexpr uint32_t kKref = kRedSum + 512;      // 16
-constexpr uint32_t kAlpha = kKref + 64;        // 16
-constexpr uint32_t kEnd = kAlpha + 64;
-constexpr uint32_t kSmemBytes = kEnd + 1024;
-static_assert(kSmemBytes <= 232448u, "shared memory");
 constexpr int BAR_QTMEM = BAR_PFREE0;  // Q copied into TMEM (128 arrivals)
 // PV(i) completion, alternating by tile parity (this kernel has no P^T
 // buffer barriers): with QK and PV issued by different warps, a waiter is
@@ -318,11 +331,15 @@ constexpr int BAR_ODONE_0 = BAR_ODONE;
 constexpr int BAR_ODONE_1 = BAR_PFREE1;
 }  // namespace q16
 
-template <bool kGather, bool kItems, bool kShared = false>
-__global__ void __launch_bounds__(q16::kThreads, 1)
+template <bool kGather, bool kItems, bool kShared = false, int NR = 16>
+__global__ void __launch_bounds__(CfgQ<NR>::kThreads, 1)
     mla_split_kv_bf16_q16_kernel(const __grid_constant__ CUtensorMap tm_kv,
                                  const __grid_constant__ CUtensorMap tm_q, const DecodeParams p) {
   using namespace q16;
+  using C = CfgQ<NR>;
+  static_assert(NR == 16 || kShared, "32 rows: shared prefixes only");
+  constexpr int NST = C::NST, T = C::kTok;
+  constexpr uint32_t kQStage = C::kQStage, kQCol = C::kQCol, kSCol = C::kSCol, kOCol = C::kOCol;
   SplitRange sr;
   int b = 0;
   if constexpr (kShared) {
@@ -358,13 +375,13 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(base);
-  auto bar = [&](int i) -> uint32_t { return sbase + kBars + 8u * i; };
-  volatile int* flags = reinterpret_cast<volatile int*>(base + kFlags);
+  auto bar = [&](int i) -> uint32_t { return sbase + C::kBars + 8u * i; };
+  volatile int* flags = reinterpret_cast<volatile int*>(base + C::kFlags);
   volatile int* abort_flag = flags + 2;
-  float* red_max = reinterpret_cast<float*>(base + kRedMax);
-  float* red_sum = reinterpret_cast<float*>(base + kRedSum);
-  float* kref = reinterpret_cast<float*>(base + kKref);
-  float* alpha_s = reinterpret_cast<float*>(base + kAlpha);
+  float* red_max = reinterpret_cast<float*>(base + C::kRedMax);
+  float* red_sum = reinterpret_cast<float*>(base + C::kRedSum);
+  float* kref = reinterpret_cast<float*>(base + C::kKref);
+  float* alpha_s = reinterpret_cast<float*>(base + C::kAlpha);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -391,13 +408,13 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(sbase + kTmemSlot, kTmemCols);
+    tmem_alloc(sbase + C::kTmemSlot, C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + kTmemSlot);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + C::kTmemSlot);
 
   if (warp == 0) {
     // ================= TMA producer =================
@@ -420,7 +437,7 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
                                            window_nv);
     int window_next = bf16_window_page<kGather>(p, sr, pt, b, page0, page_end, 1, lane, last_lp,
                                                 window_next_nv);
-    volatile uint32_t* stage_info = reinterpret_cast<volatile uint32_t*>(base + kStageInfo);
+    volatile uint32_t* stage_info = reinterpret_cast<volatile uint32_t*>(base + C::kStageInfo);
     int issued = 0;
     int st = 0, round = 0;
     for (int i = 0; i < n_tiles; ++i) {
@@ -530,16 +547,16 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
       const int st = j % NST;
       bool w = !expired_here(p, WAIT_TILE_FULL, j) &&
                mbar_wait_abort(bar(BAR_FULL0 + st), (j / NST) & 1, p.wait_cycles, abort_flag);
-      const int use = j >> 1;
+      const int sb = C::NS == 2 ? (j & 1) : 0, use = C::NS == 2 ? (j >> 1) : j;
       if (w && use >= 1)
-        w = mbar_wait_abort(bar(BAR_SFREE0 + (j & 1)), (use - 1) & 1, p.wait_cycles, abort_flag);
+        w = mbar_wait_abort(bar(BAR_SFREE0 + sb), (use - 1) & 1, p.wait_cycles, abort_flag);
       w = __all_sync(0xffffffffu, w && !*abort_flag);
       if (!w) return false;
       const uint32_t info =
-          kGather ? *reinterpret_cast<volatile uint32_t*>(base + kStageInfo + 4 * st) : 0u;
+          kGather ? *reinterpret_cast<volatile uint32_t*>(base + C::kStageInfo + 4 * st) : 0u;
       zero_unloaded_rows_bf16<kGather>(base + st * kTileBytesB, lane, info,
                                        tok_end - (t0 + j * kTokB));
-      if (lane == 0) issue_qk(st, j & 1);
+      if (lane == 0) issue_qk(st, sb);
       __syncwarp();
       return true;
     };
@@ -581,13 +598,13 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
     // ================= softmax warpgroup =================
     const int w = warp & 3;                 // TMEM lane quadrant this warp may access
     const int lidx = w * 32 + lane;         // TMEM lane
-    const int row = lidx & 15;              // query row of this thread
-    const int slot = lidx >> 4;             // tokens 8*slot .. 8*slot + 7 of a tile
-    const bool hi = lane >= 16;
-    const int sid = threadIdx.x - 96;       // 0..127; owner of row sid when < 16
+    const int row = lidx & (NR - 1);        // query row of this thread
+    const int slot = lidx / NR;             // tokens T*slot .. T*slot + T - 1 of a tile
+    const bool hi = NR == 16 && lane >= 16;
+    const int sid = threadIdx.x - 96;       // 0..127; owner of row sid when < NR
     const uint32_t lane_addr = static_cast<uint32_t>(w * 32) << 16;
     bool ok = true;
-    // ---- Q: staged rows -> TMEM (lane l gets row l % 16) ----
+    // ---- Q: staged rows -> TMEM (lane l gets row l % NR) ----
     ok = mbar_wait(bar(BAR_QFULL), 0, p.wait_cycles);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
@@ -630,28 +647,29 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
       sel_next = sel_window(1);
     }
     for (int i = 0; i < n_tiles; ++i) {
-      const int sb = i & 1;
-      const int use = i >> 1;
+      const int sb = C::NS == 2 ? (i & 1) : 0;
+      const int use = C::NS == 2 ? (i >> 1) : i;
       if (ok)
         ok = !expired_here(p, WAIT_S_FULL, i) &&
              mbar_wait_abort(bar(BAR_SFULL0 + sb), use & 1, p.wait_cycles, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) *abort_flag = 1;  // the other roles stop waiting
-      float t[8];
+      float t[T];
       if (ok) {
         tc_fence_after();
         uint32_t r[16];
         tmem_ld16(tmem + lane_addr + kSCol + sb * 64 + w * 16, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t[k] = __uint_as_float(hi ? r[8 + k] : r[k]);
+        for (int k = 0; k < T; ++k)
+          t[k] = __uint_as_float(NR == 16 && hi ? r[(8 + k) & 15] : r[k]);
         tc_fence_before();
         mbar_arrive(bar(BAR_SFREE0 + sb));
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t[k] = 0.0f;
+        for (int k = 0; k < T; ++k) t[k] = 0.0f;
       }
-      const int j0 = t0 + i * kTokB + slot * 8;
+      const int j0 = t0 + i * kTokB + slot * T;
       if constexpr (kGather) {
         // Restricted key sets: the token's key position decides.
         int64_t pos0 = j0;
@@ -667,34 +685,34 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
         }
         const int plim = p.causal ? min(sr.win_hi, L - q_b + qi + 1) : sr.win_hi;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < T; ++k) {
           const bool vis = row_ok && page_ok && j0 + k < tok_end && pos0 + k >= sr.win_lo &&
                            pos0 + k < plim;
           t[k] = vis ? t[k] * c : -INFINITY;
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t[k] = (row_ok && j0 + k < lim) ? t[k] * c : -INFINITY;
+        for (int k = 0; k < T; ++k) t[k] = (row_ok && j0 + k < lim) ? t[k] * c : -INFINITY;
       }
       bool over = false;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) over |= t[k] > kreg + 0.75f;
+      for (int k = 0; k < T; ++k) over |= t[k] > kreg + 0.75f;
       const bool any_over = bar_sync_or(kVoteBarrier, 128, over);
       if (sid < NR && i > 0) {
-        const float* rs = red_sum + ((i - 1) & 1) * 64;
-        l_row += (rs[sid] + rs[16 + sid]) + (rs[32 + sid] + rs[48 + sid]);
+        const float* rs = red_sum + ((i - 1) & 1) * 4 * NR;
+        l_row += (rs[sid] + rs[NR + sid]) + (rs[2 * NR + sid] + rs[3 * NR + sid]);
       }
       if (any_over) {
         float m = t[0];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) m = fmaxf(m, t[k]);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        if (!hi) red_max[w * 16 + row] = m;
+        for (int k = 1; k < T; ++k) m = fmaxf(m, t[k]);
+        if constexpr (NR == 16) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (!hi) red_max[w * NR + row] = m;
         if (sid == 0) flags[0] = 0;
         named_bar_sync(kSoftmaxBarrier, 128);
         if (sid < NR) {
-          const float mt = fmaxf(fmaxf(red_max[sid], red_max[16 + sid]),
-                                 fmaxf(red_max[32 + sid], red_max[48 + sid]));
+          const float mt = fmaxf(fmaxf(red_max[sid], red_max[NR + sid]),
+                                 fmaxf(red_max[2 * NR + sid], red_max[3 * NR + sid]));
           float k_new = k_row;
           if (mt > k_row + 0.75f) k_new = ceilf(mt);
           float alpha = 1.0f;
@@ -721,14 +739,14 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
           if (ok) {
             tc_fence_after();
 #pragma unroll 1
-            for (int d = 0; d < 4; ++d) {
+            for (int d = 0; d < NR / 4; ++d) {  // 16 columns of latent block d / (NR / 16)
               uint32_t r[16];
-              const uint32_t addr = tmem + lane_addr + kOCol + d * NR;
+              const uint32_t addr = tmem + lane_addr + kOCol + d * 16;
               tmem_ld16(addr, r);
               tmem_ld_wait();
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha_s[k]);
+                r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha_s[(d * 16) % NR + k]);
               tmem_st16(addr, r);
             }
             tmem_st_wait();
@@ -736,25 +754,32 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) t[k] = softmax_weight<false>(t[k], kreg);
+      for (int k = 0; k < T; ++k) t[k] = softmax_weight<false>(t[k], kreg);
       if (ok) {
-        // P^T row `row`, tokens 8*slot..+7: one 16-byte chunk of the row's
+        // P^T row `row`, tokens T*slot..: 16-byte chunks (8 tokens) of the row's
         // swizzled 128-byte line in the rope block of this tile's stage.
         uint8_t* pbuf = base + (i % NST) * kTileBytesB + kRopeOffB;
-        uint4 v;
-        v.x = pack_bf16x2(t[0], t[1]);
-        v.y = pack_bf16x2(t[2], t[3]);
-        v.z = pack_bf16x2(t[4], t[5]);
-        v.w = pack_bf16x2(t[6], t[7]);
-        *reinterpret_cast<uint4*>(pbuf + (row >> 3) * 1024 + (row & 7) * 128 +
-                                  ((slot ^ (row & 7)) * 16)) = v;
+#pragma unroll
+        for (int h = 0; h < T / 8; ++h) {
+          uint4 v;
+          v.x = pack_bf16x2(t[8 * h + 0], t[8 * h + 1]);
+          v.y = pack_bf16x2(t[8 * h + 2], t[8 * h + 3]);
+          v.z = pack_bf16x2(t[8 * h + 4], t[8 * h + 5]);
+          v.w = pack_bf16x2(t[8 * h + 6], t[8 * h + 7]);
+          *reinterpret_cast<uint4*>(pbuf + (row >> 3) * 1024 + (row & 7) * 128 +
+                                    (((slot * (T / 8) + h) ^ (row & 7)) * 16)) = v;
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bar(BAR_PFULL0 + (i & 1)));
       }
       float sum = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
-      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      if (!hi) red_sum[(i & 1) * 64 + w * 16 + row] = sum;
+      if constexpr (NR == 16)
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      else
+        sum += ((t[8 % T] + t[9 % T]) + (t[10 % T] + t[11 % T])) +
+               ((t[12 % T] + t[13 % T]) + (t[14 % T] + t[15 % T]));
+      if (!hi) red_sum[(i & 1) * 4 * NR + w * NR + row] = sum;
     }
     if (!ok && lane == 0) {
       report(p.status, MLA_ERR_TIMEOUT);
@@ -766,8 +791,8 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
     float* scale_s = alpha_s;
     if (sid < NR) {
       if (n_tiles > 0) {
-        const float* rs = red_sum + ((n_tiles - 1) & 1) * 64;
-        l_row += (rs[sid] + rs[16 + sid]) + (rs[32 + sid] + rs[48 + sid]);
+        const float* rs = red_sum + ((n_tiles - 1) & 1) * 4 * NR;
+        l_row += (rs[sid] + rs[NR + sid]) + (rs[2 * NR + sid] + rs[3 * NR + sid]);
       }
       const float m_s = (k_row == -INFINITY) ? -INFINITY : k_row - 8.0f;
       const int64_t grow = static_cast<int64_t>(sr.row_at) + row0 + sid;
@@ -800,17 +825,20 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
     if (ok && fin && n_tiles > 0) {
       tc_fence_after();
       // The rows' scales in registers, not re-read after every store.
-      float sc_r[16];
+      float sc_r[NR];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) sc_r[k] = scale_s[k];
+      for (int k = 0; k < NR; ++k) sc_r[k] = scale_s[k];
 #pragma unroll 1
       for (int d = 0; d < 4; ++d) {
         const int dim = d * 128 + lidx;
-        uint32_t r[16];
-        tmem_ld16(tmem + lane_addr + kOCol + d * NR, r);
+        uint32_t r[NR];
+#pragma unroll
+        for (int h = 0; h < NR / 16; ++h)
+          tmem_ld16(tmem + lane_addr + kOCol + d * NR + h * 16,
+                    *reinterpret_cast<uint32_t(*)[16]>(&r[h * 16]));
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < NR; ++k) {
           if (k < rows_here) {
             const float v = __uint_as_float(r[k]) * sc_r[k];
             const int64_t grow = static_cast<int64_t>(sr.row_at) + row0 + k;
@@ -839,7 +867,7 @@ __global__ void __launch_bounds__(q16::kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
   // Shared prefixes: as in the E4M3 kernel.
   if (!kShared || !(p.chain & SHARED_RELEASE))
@@ -942,35 +970,26 @@ __device__ __forceinline__ void zero_unloaded_rows_w(uint8_t* kvp, int lane, uin
   }
 }
 
-template <int NR, bool kGather, bool kItems, bool kShared = false>
+template <int NR, bool kGather, bool kItems>
 __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
     mla_split_kv_bf16_wide_kernel(const __grid_constant__ CUtensorMap tm_kv,
                                   const __grid_constant__ CUtensorMap tm_q, const DecodeParams p) {
   using C = CfgW<NR>;
   using bw::kTok;
   SplitRange sr;
-  int b = 0;
-  if constexpr (kShared) {
-    if (p.chain & SHARED_RELEASE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!segment_range(p, sr)) {
-      if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
-      return;
-    }
-  } else {
-    const int ngroups = (p.rows_per_req + p.rows_per_group - 1) / p.rows_per_group;
-    int split, grp;
-    if (!cta_coords<kItems>(p, ngroups, b, split, grp)) return;
-    if (split >= p.splits[b]) return;  // empty split slot of a shorter request
-    if (!split_range<kGather, kTok>(p, b, split, sr)) return;
-    sr.row_at = b * p.rows_per_req;
-    sr.row0 = grp * p.rows_per_group;
-    sr.rows_here = min(p.rows_per_group, p.rows_per_req - sr.row0);
-    // Rows of real query tokens (the others are padding slots of a shorter
-    // query block: no key is visible to them).
-    sr.rows_valid = max(0, min(sr.rows_here, sr.q_b * p.num_heads - sr.row0));
-    sr.slot = split;
-    sr.table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-  }
+  const int ngroups = (p.rows_per_req + p.rows_per_group - 1) / p.rows_per_group;
+  int b, split, grp;
+  if (!cta_coords<kItems>(p, ngroups, b, split, grp)) return;
+  if (split >= p.splits[b]) return;  // empty split slot of a shorter request
+  if (!split_range<kGather, kTok>(p, b, split, sr)) return;
+  sr.row_at = b * p.rows_per_req;
+  sr.row0 = grp * p.rows_per_group;
+  sr.rows_here = min(p.rows_per_group, p.rows_per_req - sr.row0);
+  // Rows of real query tokens (the others are padding slots of a shorter
+  // query block: no key is visible to them).
+  sr.rows_valid = max(0, min(sr.rows_here, sr.q_b * p.num_heads - sr.row0));
+  sr.slot = split;
+  sr.table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
   const int L = sr.L, nsplit = sr.nsplit, q_b = sr.q_b, tok_end = sr.tok_end, t0 = sr.t0;
   const bool sparse = sr.sparse;
   const float c_log2 =
@@ -1452,7 +1471,7 @@ __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
     }
     // ---- epilogue (as in the FP8 kernel; O^T has NR columns per group) ----
     named_bar_sync(kSoftmaxBarrier, NT);
-    const bool single = !kShared && nsplit == 1;
+    const bool single = (nsplit == 1);
     float* scale_s = alpha_s;
     if (sid < NR) {
       if (n_tiles > 0) {
@@ -1563,12 +1582,7 @@ __global__ void __launch_bounds__(CfgW<NR>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
-  // Shared prefixes: as in the E4M3 kernel.
-  if (!kShared || !(p.chain & SHARED_RELEASE))
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if constexpr (kShared) {
-    if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
-  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // 2-D BF16 view [rows, 576] with a (64, box_y) box, 128-byte swizzle.
@@ -1613,17 +1627,17 @@ static cudaError_t launch_split_bf16_q16_t(const void* q, const void* kv, int64_
   static std::atomic<uint64_t> attr_done{0};
   {
     const cudaError_t e = ensure_smem_attr(mla_split_kv_bf16_q16_kernel<kGather, kItems>,
-                                           static_cast<int>(q16::kSmemBytes), attr_done);
+                                           static_cast<int>(CfgQ<16>::kSmemBytes), attr_done);
     if (e != cudaSuccess) return e;
   }
   CUtensorMap tm_kv, tm_q;
   if (!make_map_bf16(&tm_kv, kv, static_cast<uint64_t>(num_pages) * MLA_PAGE_SIZE,
                      MLA_PAGE_SIZE) ||
-      !make_map_bf16(&tm_q, q, static_cast<uint64_t>(batch) * prm.rows_per_req, q16::NR))
+      !make_map_bf16(&tm_q, q, static_cast<uint64_t>(batch) * prm.rows_per_req, CfgQ<16>::NR))
     return cudaErrorInvalidValue;
   const dim3 grid = kItems ? dim3(num_ctas) : dim3(batch, prm.max_splits * groups);
   mla_split_kv_bf16_q16_kernel<kGather, kItems>
-      <<<grid, q16::kThreads, q16::kSmemBytes, stream>>>(tm_kv, tm_q, prm);
+      <<<grid, CfgQ<16>::kThreads, CfgQ<16>::kSmemBytes, stream>>>(tm_kv, tm_q, prm);
   return cudaGetLastError();
 }
 
@@ -1636,7 +1650,7 @@ static cudaError_t launch_split_bf16(const void* q, const void* kv, int64_t num_
                                      cudaStream_t stream) {
   const bool gather = prm.kv_bounds != nullptr || prm.block_idx != nullptr;
   const bool items = prm.cta_items != nullptr;
-  if constexpr (NR == q16::NR) {
+  if constexpr (NR == CfgQ<16>::NR) {
     if (gather)
       return items ? launch_split_bf16_q16_t<true, true>(q, kv, num_pages, batch, groups,
                                                           num_ctas, prm, stream)
@@ -1660,22 +1674,23 @@ static cudaError_t launch_split_bf16(const void* q, const void* kv, int64_t num_
 }
 
 // The segments of a decode over shared prefixes: num_ctas items of prm.cta_items.
-template <typename Kernel>
-static cudaError_t launch_shared_bf16_t(Kernel kernel, int nr, int threads, uint32_t smem,
-                                        std::atomic<uint64_t>& attr_done, const void* q,
-                                        const void* kv, int64_t rows, int num_ctas,
+template <int NR>
+static cudaError_t launch_shared_bf16_t(const void* q, const void* kv, int64_t rows, int num_ctas,
                                         const DecodeParams& prm, cudaStream_t stream) {
-  cudaError_t e = ensure_smem_attr(kernel, static_cast<int>(smem), attr_done);
+  using C = CfgQ<NR>;
+  const auto kernel = mla_split_kv_bf16_q16_kernel<false, true, true, NR>;
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = ensure_smem_attr(kernel, static_cast<int>(C::kSmemBytes), attr_done);
   if (e != cudaSuccess) return e;
   CUtensorMap tm_kv, tm_q;
   if (!make_map_bf16(&tm_kv, kv, static_cast<uint64_t>(prm.num_pages) * MLA_PAGE_SIZE,
                      MLA_PAGE_SIZE) ||
-      !make_map_bf16(&tm_q, q, static_cast<uint64_t>(rows), nr))
+      !make_map_bf16(&tm_q, q, static_cast<uint64_t>(rows), NR))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_ctas);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1685,26 +1700,11 @@ static cudaError_t launch_shared_bf16_t(Kernel kernel, int nr, int threads, uint
   return cudaLaunchKernelEx(&cfg, kernel, tm_kv, tm_q, prm);
 }
 
-template <int NR>
-static cudaError_t launch_shared_bf16_w(const void* q, const void* kv, int64_t rows, int num_ctas,
-                                        const DecodeParams& prm, cudaStream_t stream) {
-  static std::atomic<uint64_t> attr_done{0};
-  return launch_shared_bf16_t(mla_split_kv_bf16_wide_kernel<NR, false, true, true>, NR,
-                              CfgW<NR>::kThreads, CfgW<NR>::kSmemBytes, attr_done, q, kv, rows,
-                              num_ctas, prm, stream);
-}
-
 cudaError_t launch_shared_bf16(int nr, const void* q, const void* kv, int64_t rows, int num_ctas,
                                const DecodeParams& prm, cudaStream_t stream) {
   switch (nr) {
-    case 16: {
-      static std::atomic<uint64_t> attr_done{0};
-      return launch_shared_bf16_t(mla_split_kv_bf16_q16_kernel<false, true, true>, q16::NR,
-                                  q16::kThreads, q16::kSmemBytes, attr_done, q, kv, rows,
-                                  num_ctas, prm, stream);
-    }
-    case 32: return launch_shared_bf16_w<32>(q, kv, rows, num_ctas, prm, stream);
-    case 48: return launch_shared_bf16_w<48>(q, kv, rows, num_ctas, prm, stream);
+    case 16: return launch_shared_bf16_t<16>(q, kv, rows, num_ctas, prm, stream);
+    case 32: return launch_shared_bf16_t<32>(q, kv, rows, num_ctas, prm, stream);
     default: return cudaErrorInvalidValue;
   }
 }

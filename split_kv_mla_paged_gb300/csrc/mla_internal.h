@@ -17,6 +17,8 @@ namespace mla {
 // rows) reads each KV tile once.  More rows use more CTAs (row groups).
 constexpr int kMaxRowsPerCta = 48;
 constexpr int kMaxRowsPerCtaFp8 = 96;
+// BF16 kernels of a decode over shared prefixes: 16 or 32 rows, with Q in TMEM.
+constexpr int kMaxRowsSharedBf16 = 32;
 
 struct RowGroups {
   int groups;   // CTAs per (request, split) along the row dimension

@@ -6,7 +6,7 @@
 //   the merge joins as it joins the splits of one request.
 //
 // The split-KV kernels run it as they are, over segments in the place of
-// requests: a prefix segment has up to 96 (BF16: 48) consecutive rows of the
+// requests: a prefix segment has up to 96 (BF16: 32) consecutive rows of the
 // batch, of any requests of its group; a suffix segment has rows of one request.
 // Prefixes and suffixes want CTAs of different row counts and so are two launches
 // (one where the counts are equal).  The second starts as soon as every CTA of

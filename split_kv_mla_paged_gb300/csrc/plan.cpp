@@ -237,10 +237,12 @@ namespace mla {
 // the rest of a CTA (start, epilogue, its partials' share of the merge), in
 // nanoseconds as measured with all SMs at work: what matters are their ratios.
 static int64_t tile_ns(int kind, int nr) {
-  if (kind == MLA_CACHE_BF16) return nr <= 16 ? 3300 : nr <= 32 ? 9000 : 10000;
+  if (kind == MLA_CACHE_BF16) return nr <= 16 ? 3300 : 3500;
   if (kind == MLA_CACHE_FP4) return nr <= 16 ? 1750 : nr <= 32 ? 2500 : nr <= 48 ? 2800 : 4200;
   return nr <= 16 ? 1650 : nr <= 32 ? 2370 : nr <= 48 ? 2640 : 3000;
 }
+// What a second launch adds where its CTAs start as the first one's have.
+constexpr int64_t kSecondLaunchNs = 3000;
 static int64_t cta_ns(int rows) { return 2600 + 94 * static_cast<int64_t>(rows); }
 
 struct SharedSegment {  // layout of the device's Segment
@@ -284,7 +286,7 @@ extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offs
   int64_t rows_max[2] = {0, 0};  // rows of the largest prefix and suffix segment
   auto add = [&](int kind, int64_t row, int64_t n_rows, int request, int key0, int64_t keys,
                  bool suffix) {
-    const RowGroups rg = bf16 ? row_groups(static_cast<int>(n_rows))
+    const RowGroups rg = bf16 ? row_groups(static_cast<int>(n_rows), kMaxRowsSharedBf16)
                               : row_groups_fp8(static_cast<int>(n_rows));
     for (int64_t r = 0; r < n_rows; r += rg.rows) {
       const int32_t n = static_cast<int32_t>(std::min<int64_t>(rg.rows, n_rows - r));
@@ -337,8 +339,7 @@ extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offs
   // whose CTAs fit one wave of the SMs, or two waves where that ends sooner; one
   // split each where there are more segments than that.
   const int64_t T = MLA_TILE_TOKENS;
-  const int64_t cost[2] = {tile_ns(cache_kind, nr[0]), tile_ns(cache_kind, nr[1])};
-  const int64_t fixed[2] = {cta_ns(nr[0]), cta_ns(nr[1])};
+  int64_t cost[2], fixed[2], slots[2];
   auto chunk_of = [&](size_t s, int64_t ns) -> int64_t {
     const int k = s < n_prefix ? 0 : 1;
     const int64_t keys = std::max<int64_t>(segs[s].keys, 1);
@@ -348,38 +349,59 @@ extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offs
     tiles = ceil_div(all, ceil_div(all, std::min(tiles, all)));
     return tiles * T;
   };
-  auto ctas_at = [&](int64_t ns, int64_t slots[2]) -> int64_t {
+  auto ctas_at = [&](int64_t ns, int64_t slots_out[2]) -> int64_t {
     int64_t n = 0;
-    slots[0] = slots[1] = 0;
+    slots_out[0] = slots_out[1] = 0;
     for (size_t s = 0; s < segs.size(); ++s) {
       const int64_t k = ceil_div(std::max<int64_t>(segs[s].keys, 1), chunk_of(s, ns));
       n += k;
-      int64_t& m = slots[s < n_prefix ? 0 : 1];
+      int64_t& m = slots_out[s < n_prefix ? 0 : 1];
       m = std::max(m, k);
     }
     return n;
   };
-  int64_t most = 0;
-  for (size_t s = 0; s < segs.size(); ++s) {
-    const int k = s < n_prefix ? 0 : 1;
-    most = std::max(most, fixed[k] + cost[k] * ceil_div(std::max<int64_t>(segs[s].keys, 1), T));
-  }
-  int64_t best = most, best_cost = -1;
-  int64_t slots[2];
-  for (int w = 1; w <= kMaxWaves; ++w) {
-    auto fits = [&](int64_t ns) {
-      return ctas_at(ns, slots) <= static_cast<int64_t>(w) * sm_count &&
-             slots[0] + slots[1] <= MLA_MAX_SPLITS;
-    };
-    if (!fits(most)) continue;
-    int64_t lo = 1, hi = most;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (fits(mid)) hi = mid; else lo = mid + 1;
+  // Returns the waves times the CTAs' time, and that time, for CTAs of these rows.
+  auto plan_for = [&](int nr0, int nr1, int64_t* ns_out) -> int64_t {
+    cost[0] = tile_ns(cache_kind, nr0);
+    cost[1] = tile_ns(cache_kind, nr1);
+    fixed[0] = cta_ns(nr0);
+    fixed[1] = cta_ns(nr1);
+    int64_t most = 0;
+    for (size_t s = 0; s < segs.size(); ++s) {
+      const int k = s < n_prefix ? 0 : 1;
+      most = std::max(most, fixed[k] + cost[k] * ceil_div(std::max<int64_t>(segs[s].keys, 1), T));
     }
-    if (best_cost < 0 || lo * w < best_cost) {
-      best_cost = lo * w;
-      best = lo;
+    *ns_out = most;
+    int64_t best_cost = -1;
+    for (int w = 1; w <= kMaxWaves; ++w) {
+      auto fits = [&](int64_t ns) {
+        return ctas_at(ns, slots) <= static_cast<int64_t>(w) * sm_count &&
+               slots[0] + slots[1] <= MLA_MAX_SPLITS;
+      };
+      if (!fits(most)) continue;
+      int64_t lo = 1, hi = most;
+      while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (fits(mid)) hi = mid; else lo = mid + 1;
+      }
+      if (best_cost < 0 || lo * w < best_cost) {
+        best_cost = lo * w;
+        *ns_out = lo;
+      }
+    }
+    return best_cost < 0 ? most * ceil_div(static_cast<int64_t>(segs.size()), sm_count) : best_cost;
+  };
+  int64_t best = 0;
+  const int64_t apart = plan_for(nr[0], nr[1], &best);
+  if (nr[0] > nr[1]) {
+    // The suffixes in the prefixes' CTAs: their tiles take longer, but one launch is
+    // saved.
+    int64_t ns = 0;
+    if (plan_for(nr[0], nr[0], &ns) <= apart + kSecondLaunchNs) {
+      nr[1] = nr[0];
+      best = ns;
+    } else {
+      plan_for(nr[0], nr[1], &best);
     }
   }
   const int64_t total = ctas_at(best, slots);
@@ -408,10 +430,13 @@ extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offs
   p.suffix_ctas = static_cast<int32_t>(n_ctas[1]);
   p.prefix_slots = static_cast<int32_t>(slots[0]);
   p.suffix_slots = static_cast<int32_t>(slots[1]);
-  // The merge's thread groups, by mla_decode_plan's rule.
-  const int64_t rows = static_cast<int64_t>(batch) * per_req;
+  // The merge's thread groups: mla_decode_plan's rule, or up to twice as many groups
+  // where each still has four partials (192 rows of 65: 72.9 us with 4 groups, 71.5
+  // with 8, 74.8 with 16; 768 rows of 19: 75.6 with 1, 76.5 with 2).
+  const int64_t rows = static_cast<int64_t>(batch) * per_req, most = slots[0] + slots[1];
   int32_t g = 16;
-  while (g > 1 && (g * 2 > slots[0] + slots[1] || rows * g > 6 * static_cast<int64_t>(sm_count)))
+  while (g > 1 && !(g * 2 <= most && rows * g <= 6 * static_cast<int64_t>(sm_count)) &&
+         !(g * 4 <= most && rows * g <= 12 * static_cast<int64_t>(sm_count)))
     g >>= 1;
   p.kv_split = g;
   p.data_len = 8 * static_cast<int64_t>(segs.size()) + 2 * static_cast<int64_t>(batch) + total;

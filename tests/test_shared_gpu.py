@@ -8,9 +8,9 @@ of two as long as the CTAs form and round them alike.  CTAs of 96 rows round a
 weight p to halves before its two E4M3 terms, the smaller ones do not.  Either is
 p (1 + e) with |e| <= 2^-8 (the second term, at most 2^-4 p, is rounded by at most
 2^-4 of itself), so between them an output, a mean of values with those weights,
-moves by at most 2 * 2^-8 max|v|.  BF16 CTAs of 16 rows take Q as the other operand
-of the product than the wider ones, so that their scores differ in the last bits
-and a weight next to a border is rounded to the other side: p (1 + e) with
+moves by at most 2 * 2^-8 max|v|.  mla_decode's BF16 CTAs of more than 16 rows take Q
+as the other operand of the product than these, so that scores differ in the last
+bits and a weight next to a border is rounded to the other side: p (1 + e) with
 |e| <= 2^-9 on either side, at most 2 * 2^-9 max|v|.  The 4-bit inputs have values
 and scores so far apart that weights reach the range where E4M3 steps no longer
 shrink with them, and the step then depends on the part's own maximum: the E4M3
@@ -84,6 +84,8 @@ SHAPES = [
     (128, 8, [1], [128], [260], True),            # 1024 rows
     (16, 1, [20], [1536], [3] * 20, False),       # 320 rows
     (12, 1, [3], [9984], [5000, 10, 1000], False),
+    (12, 1, [8, 1], [512, 2048], [9000, 8000, 7000, 9001, 33, 9002, 5, 4000, 9000], False),  # two launches
+    (4, 8, [3], [256], [20000, 19000, 8], True),                                          # likewise
 ]
 
 
@@ -98,7 +100,160 @@ def test_matches_the_oracle_and_the_plain_decode(kind, shape):
     assert_parity(out, lse, ref, ref_lse, str(shape))
     plain = _run(inp, pool, causal)
     plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, heads, q_len, causal=causal, cache_kind=KIND[kind]).info
-    forms = {n > (16 if kind == "bf16" else 48) for n in (heads * q_len, plan.suffix_nr, plan.prefix_nr)}
+    forms = {heads * q_len > 16, False} if kind == "bf16" else {n > 48 for n in (heads * q_len, plan.suffix_nr, plan.prefix_nr)}
     tol = PLAN_ABS if len(forms) == 1 and kind != "fp4" else (2.0 ** -8 if kind == "bf16" else 2.0 ** -7) * _largest_value(inp)
     assert float((f32 - plain[2]).abs().max()) <= tol
     assert float((lse - plain[1]).abs().max()) <= PLAN_ABS
+
+
+def _oracle(inp, causal, **kw):
+    return oracle.decode_rows(inp.q, inp.kv, inp.page_table, inp.kv_lens, q_len=inp.q_len, num_heads=inp.num_heads, causal=causal,
+                              softmax_scale=SOFTMAX_SCALE, **kw)
+
+
+KINDS = ["fp8", "fp4", "bf16"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_sinks_output_scale_and_scales(kind):
+    inp, pool, offsets, pl = _case(kind, 12, 2, [3, 1], [640, 96], [2, 200, 5, 300], 5)
+    sinks = np.linspace(-2.0, 3.0, 12).astype(np.float32)
+    scales = {} if kind == "bf16" else dict(q_scale=1.5, kv_scale=0.37)
+    for device_scales in (False, True):
+        out, lse, _ = _run(inp, pool, True, group_offsets=offsets, prefix_lens=pl, sinks=sinks, output_scale=0.5, device_scales=device_scales,
+                           **scales)
+        ref, ref_lse = _oracle(inp, True, sinks=sinks, output_scale=0.5, **scales)
+        assert_parity(out, lse, ref, ref_lse)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_ragged_query_counts(kind):
+    inp, pool, offsets, pl = _case(kind, 12, 8, [4], [320], [8, 100, 9, 8], 6)
+    ql = [1, 8, 3, 5]
+    for sinks in (None, np.zeros(12, np.float32)):
+        out, lse, _ = _run(inp, pool, True, group_offsets=offsets, prefix_lens=pl, query_lens=ql, sinks=sinks)
+        ref, ref_lse = _oracle(inp, True, query_lens=ql, sinks=sinks)
+        empty = np.isinf(ref_lse)
+        assert empty.any() == (sinks is None)
+        l = lse.cpu().numpy().reshape(ref_lse.shape)
+        assert (l[empty] == -np.inf).all()
+        assert_parity(out, torch.from_numpy(np.where(empty, 0.0, l)), ref, np.where(empty, 0.0, ref_lse))
+        assert (out[0, 1:] == 0).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_bad_pages_and_stale_plans_are_reported(kind):
+    inp, pool, offsets, pl = _case(kind, 12, 1, [2], [64], [100, 5], 7)
+    kw = dict(group_offsets=offsets, prefix_lens=pl)
+    for row, entry in ((0, 1), (1, 2)):
+        table = inp.page_table.clone()
+        inp.page_table[row, entry] = 10 ** 6
+        with pytest.raises(mla.MlaError) as err:
+            _run(inp, pool, False, **kw)
+        assert err.value.status == mla.MLA_ERR_INVALID_ARG
+        inp.page_table = table
+    # Lengths that have left the plan: below the prefix, and past the suffix's splits.
+    plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, 12, 1, cache_kind=KIND[kind])
+    data = torch.from_numpy(plan.data).cuda()
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out = torch.empty(2, 1, 12, 512, dtype=torch.bfloat16, device="cuda")
+    wide = torch.cat([inp.page_table, torch.zeros(2, 8, dtype=torch.int32)], 1).clamp(min=0).cuda()  # valid ids behind the ends
+    for lens, good in (([164, 69], True), ([164, 192], True), ([63, 69], False), ([164, 193], False), ([-5, 69], False)):
+        mla.mla_decode_shared(inp.q.cuda(), pool.cuda(), pool.shape[0], wide, wide.shape[1], torch.tensor(lens, dtype=torch.int32).cuda(), plan, data,
+                              2, 1, 12, False, 1.0, 1.0, SOFTMAX_SCALE, ws, plan.workspace_bytes, out)
+        if good:
+            mla.mla_decode_status(ws)
+        else:
+            with pytest.raises(mla.MlaError) as err:
+                mla.mla_decode_status(ws)
+            assert err.value.status == mla.MLA_ERR_INVALID_ARG
+    out, lse, _ = _run(inp, pool, False, **kw)
+    assert_parity(out, lse, *_oracle(inp, False))
+
+
+# Every row group of the segments' kernels: heads, q_len, group size, suffix.
+WIDTHS = {16: (12, 1, 1, 300), 32: (12, 1, 2, 300), 48: (12, 1, 4, 300), 96: (12, 8, 1, 300), "two": (12, 1, 8, 9000)}
+ROLES = [0, 1, 2, 3, 4, 5]
+
+
+@pytest.mark.parametrize("kind,width", [(k, w) for k in KINDS for w in WIDTHS if k != "bf16" or w in (16, 32)])
+def test_expired_waits_end_the_call(kind, width):
+    heads, q_len, size, suffix = WIDTHS[width]
+    inp, pool, offsets, pl = _case(kind, heads, q_len, [size], [6400], [suffix] * size, 8)
+    kw = dict(group_offsets=offsets, prefix_lens=pl, sm_count=4)  # few CTAs, many tiles each
+    info = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, heads, q_len, causal=True, cache_kind=KIND[kind], sm_count=4).info
+    assert (info.prefix_nr, info.suffix_nr) == ((96, 16) if width == "two" else (width, width if width != 32 or kind != "bf16" else info.suffix_nr))
+    ref = _oracle(inp, True)
+    for role in ROLES:
+        if role == 4 and (kind == "bf16" or width == 16):
+            continue  # P^T lives in the KV stages: no such wait
+        mla.mla_debug_set_expire(role, 0 if role == 5 else 2)
+        try:
+            with pytest.raises(mla.MlaError) as err:
+                _run(inp, pool, True, **kw)
+            assert err.value.status == mla.MLA_ERR_TIMEOUT, role
+        finally:
+            mla.mla_debug_set_expire(-1)
+        out, lse, _ = _run(inp, pool, True, **kw)
+        assert_parity(out, lse, *ref, what=f"after role {role}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("suffix", [40, 9000])
+def test_graph_replays_on_another_stream(kind, suffix):
+    inp, pool, offsets, pl = _case(kind, 12, 1, [8], [512], [suffix] * 8, 9)
+    plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, 12, 1, cache_kind=KIND[kind])
+    data, lens = torch.from_numpy(plan.data).cuda(), inp.kv_lens.to(torch.int32).cuda()
+    q, kv, pt = inp.q.cuda(), pool.cuda(), inp.page_table.cuda()
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out, lse = torch.zeros(8, 1, 12, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 1, 12, device="cuda")
+    args = (q, kv, kv.shape[0], pt, pt.shape[1], lens, plan, data, 8, 1, 12, False, 1.0, 1.0, SOFTMAX_SCALE, ws, plan.workspace_bytes, out, lse)
+    mla.mla_decode_shared(*args)
+    first = out.clone(), lse.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for _ in range(3):  # calls that follow each other in one workspace
+            mla.mla_decode_shared(*args)
+    for _ in range(20):
+        out.fill_(7.0)
+        graph.replay()
+    torch.cuda.synchronize()
+    mla.mla_decode_status(ws)
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    q.copy_(q.flip(2))  # the heads in the opposite order
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first[0].flip(2)) and torch.equal(lse, first[1].flip(2))
+    assert_parity(first[0], first[1], *_oracle(inp, False))
+
+
+def test_decode_refuses_what_has_no_shared_form():
+    inp, pool, offsets, pl = _case("fp8", 12, 1, [2], [64], [100, 5], 7)
+    for kw in (dict(kv_bounds=np.array([[0, 5], [0, 5]])), dict(block_idx=np.array([[0], [0]])), dict(persistent_ctas=4), dict(use_items=True), dict(target_ctas=4),
+               dict(kv_split=2)):
+        with pytest.raises(ValueError):
+            _run(inp, pool, False, group_offsets=offsets, prefix_lens=pl, **kw)
+    with pytest.raises(ValueError):
+        _run(inp, pool, False, group_offsets=offsets)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_batches(seed):
+    rng = np.random.default_rng(seed)
+    kind = KINDS[seed % 3]
+    heads, q_len = int(rng.choice([1, 4, 8, 12, 16, 33])), int(rng.choice([1, 1, 2, 3, 8]))
+    sizes = [int(n) for n in rng.integers(1, 9, rng.integers(1, 4))]
+    prefixes = [int(p) * 32 for p in rng.integers(0, 60, len(sizes))]
+    causal = bool(rng.integers(0, 2))
+    suffixes = [int(n) for n in rng.integers(q_len, 700, sum(sizes))]
+    inp, pool, offsets, pl = _case(kind, heads, q_len, sizes, prefixes, suffixes, 100 + seed)
+    ql = None if rng.random() < 0.6 else rng.integers(1, q_len + 1, sum(sizes)).tolist()
+    sinks = None if rng.random() < 0.6 else rng.standard_normal(heads).astype(np.float32)
+    out, lse, _ = _run(inp, pool, causal, group_offsets=offsets, prefix_lens=pl, query_lens=ql, sinks=sinks, sm_count=int(rng.choice([3, 40, 152])))
+    ref, ref_lse = _oracle(inp, causal, query_lens=ql, sinks=sinks)
+    empty = np.isinf(ref_lse)
+    l = lse.cpu().numpy().reshape(ref_lse.shape)
+    assert (np.isinf(l) == empty).all()
+    assert_parity(out, torch.from_numpy(np.where(empty, 0.0, l)), ref, np.where(empty, 0.0, ref_lse), f"{kind} {heads} {q_len} {sizes} {prefixes}")

@@ -49,7 +49,7 @@ def test_segments_cover_every_row_and_key_once(case, kind):
     plan = mla.mla_shared_plan(lens, offsets, prefixes, heads, q_len, causal=causal, cache_kind=kind)
     info, (segs, slots, items) = plan.info, _parts(plan)
     per = heads * q_len
-    cap = 48 if kind == mla.CACHE_BF16 else 96
+    cap = 32 if kind == mla.CACHE_BF16 else 96
     seen = np.zeros((len(lens) * per, 2), int)  # rows covered by prefix and suffix segments
     for first, n, row_in, req, key0, length, splits, chunk in segs:
         suffix = length < 0
@@ -81,7 +81,16 @@ def test_segments_cover_every_row_and_key_once(case, kind):
 
 def test_long_prefixes_fill_one_wave():
     info = mla.mla_shared_plan([131072 + 2000] * 16, [0, 16], [131072], 12, 1, sm_count=152).info
-    assert 130 <= info.prefix_ctas + info.suffix_ctas <= 152 and info.prefix_nr == 96 and info.suffix_nr == 16
+    assert 130 <= info.prefix_ctas + info.suffix_ctas <= 152 and info.prefix_nr == 96
+
+
+def test_long_suffixes_have_ctas_of_their_own_size():
+    # Suffixes as long as the prefix: in 96-row CTAs they would take twice as long.
+    for kind, wide in ((mla.CACHE_FP8, 96), (mla.CACHE_FP4, 96)):
+        info = mla.mla_shared_plan([40000] * 8, [0, 8], [20000 // 32 * 32], 12, 1, cache_kind=kind).info
+        assert info.prefix_nr == wide and info.suffix_nr == 16
+    short = mla.mla_shared_plan([1100] * 4, [0, 4], [1024], 12, 1).info
+    assert short.prefix_nr == short.suffix_nr == 48  # one launch
 
 
 @pytest.mark.parametrize("bad", [
