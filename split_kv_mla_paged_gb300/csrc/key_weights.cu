@@ -41,19 +41,20 @@ constexpr int kKwMaxRows = 128;           // rows of a group (MMA N)
 constexpr int kKwChunk = 8;               // tiles between two row groups
 constexpr uint32_t kKwSmem = 232448;
 // aux: barriers (full, empty: one per stage; Q full, Q empty, S full, S free: two
-// each), TMEM slot, abort flag, scan, -lse log2(e) per row for both epilogue groups.
+// each), TMEM slot, abort flag, scan, -lse log2(e) per row in two terms for both
+// epilogue groups.
 constexpr uint32_t kKwLse = 512;
-constexpr uint32_t kKwAux = kKwLse + 2 * kKwMaxRows * 4;
+constexpr uint32_t kKwAux = kKwLse + 4 * kKwMaxRows * 4;
 
 struct KeyWeightsParams {
   mla_key_weights_args_t a;
-  float c_log2;
+  float c_log2, c_low;  // c in two terms
   int32_t rows_per_req, group_rows, groups, nr;  // nr: group_rows rounded up to 16
   int32_t stages, q_buffers;
   // Accumulators of a score, each over its share of the blocks, added in fp32 by
   // the epilogue: the tensor core drops bits at every instruction that adds to an
   // accumulator, the more the larger it is.  As many as TMEM holds twice.
-  int32_t sums;  // 2 or 4
+  int32_t sums;  // 2, 4 or (BF16, whose scores take twice the instructions) 8
   uint32_t q_bytes;  // of one buffer
   long long wait_cycles;
   int32_t debug_expire;
@@ -432,13 +433,20 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
     const int e = (warp - C::kEpilogue0) >> 2, quad = warp & 3;
     const int tok = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
-    float* neg = lse_s + e * kKwMaxRows;  // -lse log2(e)
+    // -lse log2(e) as a float and what it leaves out: with one term each, it and c
+    // were half of the weights' error.
+    float* neg = lse_s + e * 2 * kKwMaxRows;
+    float* neg_low = neg + kKwMaxRows;
     const uint32_t bar_id = 1 + e;
-    float c = p.c_log2;
+    float c = p.c_log2, c_low = p.c_low;
     if (a.q_scale_dev || a.kv_scale_dev || a.softmax_scale_dev)
-      c = (a.softmax_scale_dev ? *a.softmax_scale_dev : a.softmax_scale) *
-          (a.q_scale_dev ? *a.q_scale_dev : a.q_scale) *
-          (a.kv_scale_dev ? *a.kv_scale_dev : a.kv_scale) * 1.4426950408889634f;
+    {
+      const double x = static_cast<double>(a.softmax_scale_dev ? *a.softmax_scale_dev : a.softmax_scale) *
+                       (a.q_scale_dev ? *a.q_scale_dev : a.q_scale) *
+                       (a.kv_scale_dev ? *a.kv_scale_dev : a.kv_scale) * 1.4426950408889634;
+      c = static_cast<float>(x);
+      c_low = static_cast<float>(x - c);
+    }
     bool ok = true, live = true, new_q = true, stale = true;
     int rows = 0;  // of the group that are real query rows
     int used = 0;  // uses of this warpgroup's buffer
@@ -451,8 +459,12 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
           named_bar_sync(bar_id, 128);  // the old values have been read
           for (int r = (warp & 3) * 32 + lane; r < rows; r += 128) {
             const float l = a.lse[static_cast<int64_t>(walk.b) * p.rows_per_req + row0 + r];
+            constexpr float kLog2e = 1.4426950408889634f;
+            constexpr float kLog2eLow = static_cast<float>(1.4426950408889634 - kLog2e);
             // A row without a visible key gives its keys nothing.
-            neg[r] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+            const float x = l == -INFINITY ? -INFINITY : -l * kLog2e;
+            neg[r] = x;
+            neg_low[r] = isfinite(x) ? fmaf(-l, kLog2eLow, fmaf(-l, kLog2e, -x)) : 0.0f;
           }
           named_bar_sync(bar_id, 128);
           stale = false;
@@ -492,9 +504,10 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
           float v[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(v0[k]) + __uint_as_float(v1[k]);
-          if (p.sums == 4) {
-            tmem_ld16(at + 2 * p.nr + r0, v0);
-            tmem_ld16(at + 3 * p.nr + r0, v1);
+#pragma unroll 1
+          for (int sum = 2; sum < p.sums; sum += 2) {
+            tmem_ld16(at + sum * p.nr + r0, v0);
+            tmem_ld16(at + (sum + 1) * p.nr + r0, v1);
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] += __uint_as_float(v0[k]) + __uint_as_float(v1[k]);
@@ -504,22 +517,28 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(misc(S_FREE + e));
           }
-          float n[16];
+          float n[16], n_low[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k) {
             *reinterpret_cast<float4*>(&n[4 * k]) = *reinterpret_cast<const float4*>(neg + r0 + 4 * k);
+            *reinterpret_cast<float4*>(&n_low[4 * k]) =
+                *reinterpret_cast<const float4*>(neg_low + r0 + 4 * k);
+          }
+          auto weight = [&](int k) {
+            return ex2_approx(fmaf(v[k], c, n[k]) + fmaf(v[k], c_low, n_low[k]));
+          };
           if (whole && r0 + 16 <= rows) {
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              sum0 += ex2_approx(fmaf(v[k], c, n[k]));
-              sum1 += ex2_approx(fmaf(v[k + 1], c, n[k + 1]));
+              sum0 += weight(k);
+              sum1 += weight(k + 1);
             }
           } else {
             int qi = (row0 + r0) / a.num_heads, h = row0 + r0 - qi * a.num_heads;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const bool sees = r0 + k < rows && (!a.causal || j < walk.len - walk.q_b + qi + 1);
-              const float x = ex2_approx(fmaf(v[k], c, n[k]));
+              const float x = weight(k);
               if (sees) sum0 += x;
               if (++h == a.num_heads) {
                 h = 0;
@@ -740,13 +759,14 @@ extern "C" int mla_key_weights(const mla_key_weights_args_t* args, void* stream)
     set_error(w + ": BF16 Q and KV carry no scale (q_scale and kv_scale must be 1)");
     return MLA_ERR_INVALID_ARG;
   }
-  p.c_log2 = static_cast<float>(static_cast<double>(a.softmax_scale) * a.q_scale * a.kv_scale *
-                                1.4426950408889634);
+  const double c = static_cast<double>(a.softmax_scale) * a.q_scale * a.kv_scale * 1.4426950408889634;
+  p.c_log2 = static_cast<float>(c);
+  p.c_low = static_cast<float>(c - p.c_log2);
   p.rows_per_req = a.num_heads * a.q_len;
   p.groups = (p.rows_per_req + kKwMaxRows - 1) / kKwMaxRows;
   p.group_rows = (p.rows_per_req + p.groups - 1) / p.groups;
   p.nr = (p.group_rows + 15) / 16 * 16;
-  p.sums = p.nr <= 64 ? 4 : 2;
+  p.sums = bf16 && p.nr <= 32 ? 8 : p.nr <= 64 ? 4 : 2;
   p.q_bytes = static_cast<uint32_t>(p.nr) * (bf16 ? 1152 : 576);
   p.q_bytes = (p.q_bytes + 1023) / 1024 * 1024;
   // Two Q buffers where six stages still fit beside them.
