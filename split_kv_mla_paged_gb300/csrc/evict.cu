@@ -19,7 +19,9 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
+#include <mutex>
 #include <string>
 
 #include "fp4_format.cuh"
@@ -29,6 +31,7 @@ namespace cg = cooperative_groups;
 
 namespace mla {
 
+constexpr int kEvictThreads = 1024;
 constexpr int kEvictMaxCluster = 16;
 constexpr int kEvictBins = 2048;
 
@@ -74,10 +77,9 @@ __device__ __forceinline__ uint32_t byte_of(uint32_t x, int m) { return (x >> (8
 // kCluster: several CTAs a request, whose counts meet in the first one; else the
 // CTA's own counts are the request's.  kCached: a CTA's slice of the weights is kept
 // in shared memory; else every pass reads it again, from L2.
-template <bool kCluster, int kThreads, bool kCached>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
-    mla_evict_select_kernel(const EvictParams p) {
-  constexpr int kWarps = kThreads / 32;
+template <bool kCluster, bool kCached>
+__global__ void __launch_bounds__(kEvictThreads, 1) mla_evict_select_kernel(const EvictParams p) {
+  constexpr int kThreads = kEvictThreads, kWarps = kThreads / 32;
   extern __shared__ uint32_t dynamic[];
   // Counts of the digits: of this CTA (kCluster), and of the request, two digits'
   // in turn, in the first CTA.
@@ -112,6 +114,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const int k1 = static_cast<int>(min(run0 + per_warp, static_cast<int64_t>(n)));
   uint32_t* my_cache = dynamic + warp * per_warp;
   uint32_t* my_list = dynamic + (kCached ? p.cached : 0) + warp * p.candidates;
+  // 512 offsets in the list's place (256 words at least), and without cached keys the
+  // keys behind them.
+  uint16_t* my_stage = reinterpret_cast<uint16_t*>(my_list);
   const bool vectors = (reinterpret_cast<uintptr_t>(w) & 15) == 0;  // runs start on 128s
   if constexpr (kCached) {  // all of it in flight at once
     if (vectors) {
@@ -173,8 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       for (int u = 0; u < 4; ++u) v[u] = k + u < k1 ? w[k + u] : 0.0f;
     }
   };
-  // fn(position of the lane's first key, its keys) for this warp's run, 512 keys at a
-  // time: keys [m][u] are positions + 128 m + u.  Keys behind the run are 0.
+  // fn(position of the lane's first key, its keys, blocks) for this warp's run, up to
+  // four blocks of 128 keys at a time: key [m][u] is that of position + 128 m + u, m <
+  // blocks.
   constexpr int kBatch = 4;
   auto each = [&](auto fn) {
     for (int base = k0; base < k1; base += 128 * kBatch) {
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       if constexpr (kCached) {
 #pragma unroll
         for (int m = 0; m < kBatch; ++m) {
-          uint4 x = make_uint4(0, 0, 0, 0);
+          uint4 x = make_uint4(0, 0, 0, 0);  // (not looked at behind the run)
           if (base + 128 * m < k1)
             x = *reinterpret_cast<const uint4*>(my_cache + (base + 128 * m - k0) + 4 * lane);
           key[m][0] = x.x;
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         for (int m = 0; m < kBatch; ++m)
           keys_of(base + 128 * m, base + 128 * m + 4 * lane, v[m], key[m]);
       }
-      fn(base + 4 * lane, key);
+      fn(base + 4 * lane, key, (k1 - base + 127) / 128);
     }
   };
   // Counts a digit.  A warp whose keys share it counts once: equal weights (zeros)
@@ -305,10 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
           count4(key);
         }
       } else {
-        each([&](int k, const uint32_t (&key)[kBatch][4]) {
+        each([&](int, const uint32_t (&key)[kBatch][4], int blocks) {
 #pragma unroll
           for (int m = 0; m < kBatch; ++m)
-            if (k + 128 * m - 4 * lane < k1) count4(key[m]);
+            if (m < blocks) count4(key[m]);
         });
       }
     }
@@ -317,14 +323,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     // Keys with that first digit are the candidates; those above it stay.
     uint32_t listed = 0;
     const uint32_t room = static_cast<uint32_t>(p.candidates);
-    each([&](int, const uint32_t (&key)[kBatch][4]) {
+    each([&](int, const uint32_t (&key)[kBatch][4], int blocks) {
       uint32_t is = 0;
 #pragma unroll
       for (int m = 0; m < kBatch; ++m)
+        if (m < blocks) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (key[m][u] > (prefix | 0x1FFFFFu)) ++above;
-          if (key[m][u] - prefix < 0x200000u) ++is;
+          for (int u = 0; u < 4; ++u) {
+            if (key[m][u] > (prefix | 0x1FFFFFu)) ++above;
+            if (key[m][u] - prefix < 0x200000u) ++is;
+          }
         }
       uint32_t all;  // (as one byte pair: up to 16 a lane, 512 in all)
       uint32_t at = listed + scan_bytes(is, lane, all);
@@ -332,9 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       if (listed <= room && is) {  // (a list that is too short is not read)
 #pragma unroll
         for (int m = 0; m < kBatch; ++m)
+          if (m < blocks) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (key[m][u] - prefix < 0x200000u) my_list[at++] = key[m][u];
+            for (int u = 0; u < 4; ++u)
+              if (key[m][u] - prefix < 0x200000u) my_list[at++] = key[m][u];
+          }
       }
     });
 #pragma unroll
@@ -349,12 +359,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
           fn(in ? my_list[i + lane] : 0u, in);
         }
       } else {
-        each([&](int k, const uint32_t (&key)[kBatch][4]) {
+        each([&](int, const uint32_t (&key)[kBatch][4], int blocks) {
 #pragma unroll
           for (int m = 0; m < kBatch; ++m)
+            if (m < blocks) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              fn(key[m][u], k + 128 * m + u < k1 && key[m][u] >> 21 == top);
+              for (int u = 0; u < 4; ++u) fn(key[m][u], key[m][u] >> 21 == top);
+            }
         });
       }
     };
@@ -416,18 +427,20 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       if (new_weights) new_weights[k] = w[k];
     }
   } else if (above + equal > 0) {
-    each([&](int k, const uint32_t (&key)[kBatch][4]) {
+    each([&](int k, const uint32_t (&key)[kBatch][4], int blocks) {
       uint32_t stay = 0;             // a bit per key
       uint32_t stays = 0, ties = 0;  // a byte per block of 128
 #pragma unroll
       for (int m = 0; m < kBatch; ++m)
+        if (m < blocks) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (key[m][u] > prefix) {
-            stay |= 1u << (4 * m + u);
-            stays += 1u << (8 * m);
+          for (int u = 0; u < 4; ++u) {
+            if (key[m][u] > prefix) {
+              stay |= 1u << (4 * m + u);
+              stays += 1u << (8 * m);
+            }
+            if (key[m][u] == prefix) ties += 1u << (8 * m);
           }
-          if (key[m][u] == prefix) ties += 1u << (8 * m);
         }
       if (__any_sync(0xffffffffu, ties)) {
         uint32_t all;
@@ -437,36 +450,108 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
           uint32_t rank_of = before_equal + byte_of(place, m);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (key[m][u] == prefix && rank_of++ < need) {
+            if (m < blocks && key[m][u] == prefix && rank_of++ < need) {
               stay |= 1u << (4 * m + u);
               stays += 1u << (8 * m);
             }
           before_equal += byte_of(all, m);
         }
       }
+      // The kept ones' offsets in order through shared memory (the list has been read),
+      // then a lane for each: stores of all 16 keys under their conditions took 11.6 us
+      // of a million keys' selection, this 7.
       uint32_t all;
       const uint32_t place = scan_bytes(stays, lane, all);
+      uint32_t total = 0;
+      __syncwarp();
 #pragma unroll
       for (int m = 0; m < kBatch; ++m) {
-        uint32_t to = at + byte_of(place, m);
+        uint32_t to = total + byte_of(place, m);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           if (stay >> (4 * m + u) & 1u) {
-            kept[to] = k + 128 * m + u;
-            if (new_weights) {
-              // The weight back from its key, but for keys that several weights have.
-              const uint32_t x = key[m][u];
-              float v = __uint_as_float(x & 0x80000000u ? x ^ 0x80000000u : ~x);
-              if (x == kEvictProtected || x == 0x80000000u || x == 0) v = w[k + 128 * m + u];
-              new_weights[to] = v;
-            }
-            ++to;
+            if constexpr (!kCached) my_list[256 + to] = key[m][u];
+            my_stage[to++] = static_cast<uint16_t>(4 * lane + 128 * m + u);
           }
-        at += byte_of(all, m);
+        total += byte_of(all, m);
       }
+      __syncwarp();
+      const int base = k - 4 * lane;
+      for (uint32_t i = lane; i < total; i += 32) {
+        const int from = base + my_stage[i];
+        kept[at + i] = from;
+        if (new_weights) {
+          // The weight back from its key, but for keys that several weights have.
+          const uint32_t x = kCached ? my_cache[from - k0] : my_list[256 + i];
+          float v = __uint_as_float(x & 0x80000000u ? x ^ 0x80000000u : ~x);
+          if (x == kEvictProtected || x == 0x80000000u || x == 0) v = w[from];
+          new_weights[at + i] = v;
+        }
+      }
+      at += total;
     });
   }
   if (rank == 0 && threadIdx.x == 0) p.new_lens[b] = want;
+}
+
+constexpr int64_t kEvictRoom = 48640;  // words of shared memory beside the counts (190 KB)
+
+using EvictKernel = void (*)(EvictParams);
+static EvictKernel evict_kernel(bool cluster, bool cached) {
+  if (cluster)
+    return cached ? mla_evict_select_kernel<true, true> : mla_evict_select_kernel<true, false>;
+  return cached ? mla_evict_select_kernel<false, true> : mla_evict_select_kernel<false, false>;
+}
+
+// CTAs per request: the most, up to 16, that let all requests run at once with a CTA
+// an SM (how many clusters of a size fit depends on the SMs of each GPC and is asked of
+// the device once: on a GB300 7 of 16, 15 of 9, 23 of 6, 36 of 4), but none for less
+// than 2,048 keys.  Against 8 CTAs of 512 threads for every request, two to an SM: 16
+// requests of 131,072 keys 22.4 -> 17.5 us.
+static cudaError_t evict_ranks(int64_t keys, int batch, int* ranks_out) {
+  constexpr int kSizes[] = {16, 10, 9, 6, 5, 4, 3, 2};
+  static std::mutex mu;
+  static int fit[64][8];
+  static bool known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!known[dev]) {
+    const int bytes = static_cast<int>(kEvictRoom * 4);
+    for (int cluster = 0; cluster < 2; ++cluster)
+      for (int cached = 0; cached < 2; ++cached) {
+        const auto kernel = evict_kernel(cluster, cached);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && cluster)
+          e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+      }
+    for (int i = 0; i < 8; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(kSizes[i]);
+      cfg.blockDim = dim3(kEvictThreads);
+      cfg.dynamicSmemBytes = bytes;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = kSizes[i];
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&fit[dev][i], evict_kernel(true, true), &cfg);
+      if (e != cudaSuccess) return e;
+    }
+    known[dev] = true;
+  }
+  *ranks_out = 1;
+  for (int i = 0; i < 8; ++i)
+    if (fit[dev][i] >= batch && keys > 2048 * static_cast<int64_t>(kSizes[i] - 1) && keys > 8192) {
+      *ranks_out = kSizes[i];
+      break;
+    }
+  return cudaSuccess;
 }
 
 struct MoveParams {
@@ -625,47 +710,24 @@ extern "C" int mla_evict_select(const float* weights, int64_t weights_stride,
   EvictParams p = {weights, weights_stride, kv_lens,  keep,        first,
                    last,    kept,           kept_stride, new_lens, new_weights,
                    new_weights_stride, status, 0, 0};
-  // CTAs per request: one up to 8,192 keys; 8 above, of 512 threads, so that two fit
-  // an SM (clusters of 8 leave SMs of a GPC without a place: 16 of 1024 threads took
-  // two waves); 16 of 1024 where few requests have more keys than 8 such CTAs keep.
-  constexpr int64_t kKeep = 18432;  // weights that a CTA of 512 threads keeps (72 KB)
-  int ranks = weights_stride <= 8192 ? 1 : 8;
-  if (batch <= 9 && weights_stride > 8 * kKeep) ranks = 16;
-  const int threads = ranks == 8 ? 512 : 1024, warps = threads / 32;
+  int ranks = 1;
+  cudaError_t e = evict_ranks(weights_stride, batch, &ranks);
+  if (e != cudaSuccess) return cuda_fail("mla_evict_select: set-up", e);
+  constexpr int64_t warps = kEvictThreads / 32;
   const int64_t per_warp =
       ((weights_stride + ranks * warps - 1) / (ranks * warps) + 127) / 128 * 128;
   const int64_t slice = per_warp * warps;
-  // Shared memory besides the counts: 86 KB where two CTAs share an SM, else 190 KB;
-  // at least 4,096 candidates.
-  const int64_t room = ranks == 8 ? 22016 : 48640;
-  const bool cached = slice <= room - 4096;
+  // At least 256 candidates a warp beside the cached keys.
+  const bool cached = slice <= kEvictRoom - 256 * warps;
+  static_assert(kEvictRoom / warps >= 768, "staged offsets and keys");
   p.cached = static_cast<int32_t>(cached ? slice : 0);
-  const int64_t list = (room - p.cached) / warps;
-  p.candidates = static_cast<int32_t>(list < per_warp ? list : per_warp);
-  const auto kernel =
-      ranks == 1   ? mla_evict_select_kernel<false, 1024, true>
-      : ranks == 8 ? (cached ? mla_evict_select_kernel<true, 512, true>
-                             : mla_evict_select_kernel<true, 512, false>)
-                   : (cached ? mla_evict_select_kernel<true, 1024, true>
-                             : mla_evict_select_kernel<true, 1024, false>);
-  static std::atomic<uint64_t> attr_done[5], wide_done[2];
-  const int which = ranks == 1 ? 0 : (ranks == 8 ? 1 : 3) + (cached ? 0 : 1);
-  cudaError_t e = ensure_smem_attr(kernel, static_cast<int>(room * 4), attr_done[which]);
-  if (e != cudaSuccess) return cuda_fail("mla_evict_select: set-up", e);
-  if (ranks > 8) {
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail("mla_evict_select: set-up", e);
-    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-    if (!bit || !(wide_done[cached].load() & bit)) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return cuda_fail("mla_evict_select: set-up", e);
-      wide_done[cached].fetch_or(bit);
-    }
-  }
+  const int64_t list = (kEvictRoom - p.cached) / warps;
+  p.candidates = static_cast<int32_t>(
+      list < per_warp || !cached ? list : per_warp > 256 ? per_warp : 256);
+  const auto kernel = evict_kernel(ranks > 1, cached);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(batch * ranks));
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = dim3(kEvictThreads);
   cfg.dynamicSmemBytes =
       (static_cast<size_t>(p.cached) + static_cast<size_t>(p.candidates) * warps) * 4;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);

@@ -90,6 +90,15 @@ def test_long_requests_in_larger_clusters():
     _check(_weights(1, 400000, 22, "ties"), [399999], [123456])
 
 
+@pytest.mark.parametrize("lens,keep", [([3000, 200, 8192], [1500, 120, 5000]), ([20000, 9000], [11000, 3000]), ([400000], [170000])])
+@pytest.mark.parametrize("low", [np.nan, -np.inf, 0.0])
+def test_ties_of_the_lowest_weights(lens, keep, low):
+    # The last kept one is among many equal lowest weights (NaNs rank below all).
+    w = _weights(len(lens), max(lens) + 1, 31, "tail")
+    w[np.random.default_rng(5).random(w.shape) < 0.8] = low
+    _check(w, lens, keep, 3, 17)
+
+
 def test_bad_lengths_keep_nothing():
     w = _weights(4, 50, 3, "tail")
     kept, out, _, status = _select(w, [51, -1, 50, 50], [5, 5, -2, 5])
