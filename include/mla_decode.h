@@ -423,7 +423,9 @@ MLA_API int mla_decode_fp4_sparse(const void* q_fp8, const void* kv_pages_fp4,
  * tables are equal; those of the group's first request are read).  They are read
  * and attended once for all rows of the group; each request's remaining keys are
  * attended by its own rows, and the merge joins both.  The result is mla_decode's
- * on the same arguments, up to the order of its fp32 sums.
+ * on the same arguments, up to the order of its fp32 sums.  Where prefixes are so short
+ * that attending them once would take longer, the plan lets every request attend its
+ * own keys.
  *
  * Planner (host only):
  * kv_lens        host int32[batch]: whole lengths, prefix included.

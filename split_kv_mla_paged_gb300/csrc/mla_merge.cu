@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(32 * G) mla_merge_kernel(const MergeParams p) 
   merge_body<G, 4, kMaxFirst>(p);
 }
 
-template <int G>
+template <int G, bool kMaxFirst>
 __global__ void __launch_bounds__(32 * G) mla_merge_shared_kernel(const MergeParams p) {
-  merge_body<G, 4, false, true>(p);
+  merge_body<G, 4, kMaxFirst, true>(p);
 }
 
 // Grids of more than two 512-thread CTAs per SM: three per SM (at most 40
@@ -226,6 +226,9 @@ cudaError_t launch_merge(const MergeParams& mp, int kv_split, cudaStream_t strea
 
 template <int G>
 static cudaError_t launch_merge_shared_g(const MergeParams& mp, cudaStream_t stream) {
+  // The max-first form by the rule above (192 rows of 65 partials: 70.2 -> 68.2 us of
+  // the whole call, 768 of 19 75.6 -> 74.7; 48 of 9 15.8 -> 16.4 us).
+  const bool max_first = mp.rows >= 96 && mp.stride_s >= 8 * G;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(mp.rows, 4);
   cfg.blockDim = dim3(32 * G);
@@ -235,7 +238,8 @@ static cudaError_t launch_merge_shared_g(const MergeParams& mp, cudaStream_t str
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_merge_shared_kernel<G>, mp);
+  return max_first ? cudaLaunchKernelEx(&cfg, mla_merge_shared_kernel<G, true>, mp)
+                   : cudaLaunchKernelEx(&cfg, mla_merge_shared_kernel<G, false>, mp);
 }
 
 cudaError_t launch_merge_shared(const MergeParams& mp, int kv_split, cudaStream_t stream) {

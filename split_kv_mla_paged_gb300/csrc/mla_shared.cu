@@ -13,16 +13,19 @@
 // their own size finish them in half the time and they are a second launch, which
 // starts as soon as every CTA of the first has, on the SMs that the first leaves free
 // (short ones in the prefixes' CTAs cost less than that launch: 16 samples of a 128K
-// prompt 71.6 -> 70.4 us, four of a 1K prompt 16.0 -> 15.8 us).  The second launch's
+// prompt 71.6 -> 70.4 us).  Where the prefixes' tiles find room on the SMs once for
+// every request, or one request's rows fill a CTA, the plan leaves every request its
+// own keys (16 samples of a 4K prompt 21.2 -> 17.0 us).  The second launch's
 // CTAs end after the first launch (griddepcontrol.wait), for the merge, a programmatic
 // dependent of the second, waits for that one alone.
 //
 // What it must read is each prefix once, not once per request; what it must
 // compute is 2 x 1088 operations per row and key as before.  From some 50 rows on the
 // operations weigh more than the bytes.  Measured (calls in a CUDA graph): 16 samples
-// of a 128K-token prompt, 12 heads, E4M3, 70.4 us (as separate requests 198 us) where
+// of a 128K-token prompt, 12 heads, E4M3, 68.6 us (as separate requests 198 us) where
 // bytes and operations take 13.3 and 14.4 us; 8 samples x 8 drafted tokens over a
-// 32K-token prompt, 768 rows, 67 us (E4M3) and 76 us (4 bits), 14.4 us of operations.
+// 32K-token prompt, 768 rows, 4 bits, 71.4 us (each for itself; the prefix apart 74.8),
+// 14.4 us of operations; 15 samples of three 64K prompts, BF16, 71.8 us, 23.7 us of bytes.
 // A 96-row tile of 128 keys takes 2.8 us (see the split kernel: the chain through its
 // two KV stages, 350 KB of MMA operands and the softmax's instructions), and start,
 // epilogue and merge of 8 to 16 tiles a CTA some 25 us.

@@ -238,7 +238,7 @@ namespace mla {
 // nanoseconds as measured with all SMs at work: what matters are their ratios.
 static int64_t tile_ns(int kind, int nr) {
   if (kind == MLA_CACHE_BF16) return nr <= 16 ? 3300 : 3500;
-  if (kind == MLA_CACHE_FP4) return nr <= 16 ? 1750 : nr <= 32 ? 2500 : nr <= 48 ? 2800 : 4200;
+  if (kind == MLA_CACHE_FP4) return nr <= 16 ? 1750 : nr <= 32 ? 2500 : nr <= 48 ? 2800 : 3500;
   return nr <= 16 ? 1650 : nr <= 32 ? 2370 : nr <= 48 ? 2640 : 3000;
 }
 // What a second launch adds where its CTAs start as the first one's have.
@@ -315,25 +315,33 @@ extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offs
         return MLA_ERR_INVALID_ARG;
       }
     }
-    if (prefix_lens[g] > 0)
-      add(0, static_cast<int64_t>(first) * per_req, static_cast<int64_t>(last - first) * per_req,
-          first, 0, prefix_lens[g], false);
   }
-  const size_t n_prefix = segs.size();
-  for (int g = 0; g < groups; ++g)
-    for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b)
-      add(1, static_cast<int64_t>(b) * per_req, per_req, b, prefix_lens[g],
-          static_cast<int64_t>(kv_lens[b]) - prefix_lens[g], true);
-  if (segs.size() > MLA_ITEM_MAX_BATCH) {
-    set_error(who + ": too many row groups");
-    return MLA_ERR_UNSUPPORTED;
-  }
+  size_t n_prefix = 0;
   int nr[2];
-  for (int k = 0; k < 2; ++k) {
-    nr[k] = static_cast<int>((rows_max[k] + 15) / 16 * 16);
-    if (!bf16 && nr[k] > kMaxRowsPerCta) nr[k] = kMaxRowsPerCtaFp8;
-  }
-  if (n_prefix == 0) nr[0] = nr[1];
+  // The segments: with the prefixes apart (share), or every request by itself.
+  auto build = [&](bool share) {
+    segs.clear();
+    rows_max[0] = rows_max[1] = 0;
+    for (int g = 0; share && g < groups; ++g) {
+      const int first = group_offsets[g];
+      const int64_t members = group_offsets[g + 1] - first;
+      if (prefix_lens[g] > 0)
+        add(0, static_cast<int64_t>(first) * per_req, members * per_req, first, 0, prefix_lens[g],
+            false);
+    }
+    n_prefix = segs.size();
+    for (int g = 0; g < groups; ++g)
+      for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b) {
+        const int key0 = share ? prefix_lens[g] : 0;
+        add(1, static_cast<int64_t>(b) * per_req, per_req, b, key0,
+            static_cast<int64_t>(kv_lens[b]) - key0, true);
+      }
+    for (int k = 0; k < 2; ++k) {
+      nr[k] = static_cast<int>((rows_max[k] + 15) / 16 * 16);
+      if (!bf16 && nr[k] > kMaxRowsPerCta) nr[k] = kMaxRowsPerCtaFp8;
+    }
+    if (n_prefix == 0) nr[0] = nr[1];
+  };
 
   // One time per CTA for all segments, prefixes and suffixes alike: the smallest
   // whose CTAs fit one wave of the SMs, or two waves where that ends sooner; one
@@ -360,16 +368,20 @@ extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offs
     }
     return n;
   };
-  // Returns the waves times the CTAs' time, and that time, for CTAs of these rows.
+  // Returns the waves times the CTAs' time (for more segments than waves, all of their
+  // time over the SMs), and a CTA's time, for CTAs of these rows.
   auto plan_for = [&](int nr0, int nr1, int64_t* ns_out) -> int64_t {
     cost[0] = tile_ns(cache_kind, nr0);
     cost[1] = tile_ns(cache_kind, nr1);
     fixed[0] = cta_ns(nr0);
     fixed[1] = cta_ns(nr1);
-    int64_t most = 0;
+    int64_t least = 0, most = 0, sum = 0;  // least: no CTA has less than one tile
     for (size_t s = 0; s < segs.size(); ++s) {
       const int k = s < n_prefix ? 0 : 1;
-      most = std::max(most, fixed[k] + cost[k] * ceil_div(std::max<int64_t>(segs[s].keys, 1), T));
+      const int64_t one = fixed[k] + cost[k] * ceil_div(std::max<int64_t>(segs[s].keys, 1), T);
+      least = std::max(least, fixed[k] + cost[k]);
+      most = std::max(most, one);
+      sum += one;
     }
     *ns_out = most;
     int64_t best_cost = -1;
@@ -379,7 +391,7 @@ extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offs
                slots[0] + slots[1] <= MLA_MAX_SPLITS;
       };
       if (!fits(most)) continue;
-      int64_t lo = 1, hi = most;
+      int64_t lo = least, hi = most;
       while (lo < hi) {
         const int64_t mid = (lo + hi) / 2;
         if (fits(mid)) hi = mid; else lo = mid + 1;
@@ -389,20 +401,35 @@ extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offs
         *ns_out = lo;
       }
     }
-    return best_cost < 0 ? most * ceil_div(static_cast<int64_t>(segs.size()), sm_count) : best_cost;
+    return best_cost < 0 ? std::max(most, ceil_div(sum, sm_count)) : best_cost;
   };
   int64_t best = 0;
-  const int64_t apart = plan_for(nr[0], nr[1], &best);
-  if (nr[0] > nr[1]) {
-    // The suffixes in the prefixes' CTAs: their tiles take longer, but one launch is
-    // saved.
-    int64_t ns = 0;
-    if (plan_for(nr[0], nr[0], &ns) <= apart + kSecondLaunchNs) {
-      nr[1] = nr[0];
-      best = ns;
-    } else {
-      plan_for(nr[0], nr[1], &best);
+  build(false);
+  const int64_t alone = plan_for(nr[0], nr[1], &best);
+  build(true);
+  if (segs.size() > MLA_ITEM_MAX_BATCH) {
+    set_error(who + ": too many row groups");
+    return MLA_ERR_UNSUPPORTED;
+  }
+  if (n_prefix > 0) {
+    int64_t ns = 0, shared = plan_for(nr[0], nr[1], &best);
+    if (nr[0] > nr[1]) {
+      // The suffixes in the prefixes' CTAs: their tiles take longer, but one launch is
+      // saved.
+      const int64_t one = plan_for(nr[0], nr[0], &ns);
+      if (one <= shared + kSecondLaunchNs) {
+        nr[1] = nr[0];
+        shared = one;
+      } else {
+        shared += kSecondLaunchNs;
+      }
     }
+    // Prefixes whose tiles find room on the SMs once for every request, or whose rows
+    // fill CTAs already: more rows a CTA only make it slower (16 requests of 12 rows with
+    // a prefix of 4,096 keys: 21.2 us with it apart, 17.0 without, of 16,384: 23.0 and 36.5;
+    // 8 requests of 96 rows and 128K 4-bit keys: 74.8 and 71.4).
+    if (alone <= shared) build(false);
+    plan_for(nr[0], nr[1], &best);
   }
   const int64_t total = ctas_at(best, slots);
   int64_t n_ctas[2] = {0, 0};
@@ -430,13 +457,11 @@ extern "C" int mla_shared_plan(const int32_t* kv_lens, const int32_t* group_offs
   p.suffix_ctas = static_cast<int32_t>(n_ctas[1]);
   p.prefix_slots = static_cast<int32_t>(slots[0]);
   p.suffix_slots = static_cast<int32_t>(slots[1]);
-  // The merge's thread groups: mla_decode_plan's rule, or up to twice as many groups
-  // where each still has four partials (192 rows of 65: 72.9 us with 4 groups, 71.5
-  // with 8, 74.8 with 16; 768 rows of 19: 75.6 with 1, 76.5 with 2).
-  const int64_t rows = static_cast<int64_t>(batch) * per_req, most = slots[0] + slots[1];
+  // The merge's thread groups, by mla_decode_plan's rule (192 rows of 65 partials: 74.3,
+  // 70.2, 68.2, 70.3 and 74.0 us of the whole call with 1 to 16 groups).
+  const int64_t rows = static_cast<int64_t>(batch) * per_req;
   int32_t g = 16;
-  while (g > 1 && !(g * 2 <= most && rows * g <= 6 * static_cast<int64_t>(sm_count)) &&
-         !(g * 4 <= most && rows * g <= 12 * static_cast<int64_t>(sm_count)))
+  while (g > 1 && (g * 2 > slots[0] + slots[1] || rows * g > 6 * static_cast<int64_t>(sm_count)))
     g >>= 1;
   p.kv_split = g;
   p.data_len = 8 * static_cast<int64_t>(segs.size()) + 2 * static_cast<int64_t>(batch) + total;

@@ -86,20 +86,30 @@ SHAPES = [
     (12, 1, [3], [9984], [5000, 10, 1000], False),
     (12, 1, [8, 1], [512, 2048], [9000, 8000, 7000, 9001, 33, 9002, 5, 4000, 9000], False),  # two launches
     (4, 8, [3], [256], [20000, 19000, 8], True),                                          # likewise
+    # Prefixes so long that the plan attends them once for their group on one SM.
+    (12, 8, [3, 2], [3200, 32], [9, 8, 500, 8, 64], True),
+    (12, 3, [5, 2], [2080, 0], [3, 77, 40, 3, 500, 9, 10], True),
+    (48, 1, [3], [6400], [130, 1, 0], False),
+    (33, 3, [4], [1600], [300, 5, 3, 64], True),
+    (128, 8, [3], [2048], [260, 8, 9], True),
+    (12, 1, [8, 1], [16384, 2048], [9000, 8000, 7000, 9001, 33, 9002, 5, 4000, 9000], False),  # two launches
+    (4, 8, [6], [8192], [20000, 19000, 8, 9, 10, 5000], True),                             # likewise
 ]
 
 
 @pytest.mark.parametrize("kind", ["fp8", "fp4", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"h{s[0]}q{s[1]}g{'-'.join(map(str, s[2]))}")
-def test_matches_the_oracle_and_the_plain_decode(kind, shape):
+@pytest.mark.parametrize("sms", [152, 1])  # one SM: plans that share short prefixes as well
+def test_matches_the_oracle_and_the_plain_decode(kind, shape, sms):
     heads, q_len, sizes, prefixes, suffixes, causal = shape
     inp, pool, offsets, pl = _case(kind, heads, q_len, sizes, prefixes, suffixes, 11)
-    out, lse, f32 = _run(inp, pool, causal, group_offsets=offsets, prefix_lens=pl)
+    out, lse, f32 = _run(inp, pool, causal, group_offsets=offsets, prefix_lens=pl, sm_count=sms)
     ref, ref_lse = oracle.decode_rows(inp.q, inp.kv, inp.page_table, inp.kv_lens, q_len=q_len, num_heads=heads, causal=causal,
                                       softmax_scale=SOFTMAX_SCALE)
     assert_parity(out, lse, ref, ref_lse, str(shape))
     plain = _run(inp, pool, causal)
-    plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, heads, q_len, causal=causal, cache_kind=KIND[kind]).info
+    plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, heads, q_len, causal=causal, cache_kind=KIND[kind], sm_count=sms).info
+    assert sms > 1 or plan.prefix_ctas > 0 or max(prefixes) < 8000 or kind == "bf16"
     forms = {heads * q_len > 16, False} if kind == "bf16" else {n > 48 for n in (heads * q_len, plan.suffix_nr, plan.prefix_nr)}
     tol = PLAN_ABS if len(forms) == 1 and kind != "fp4" else (2.0 ** -8 if kind == "bf16" else 2.0 ** -7) * _largest_value(inp)
     assert float((f32 - plain[2]).abs().max()) <= tol
@@ -115,23 +125,25 @@ KINDS = ["fp8", "fp4", "bf16"]
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_sinks_output_scale_and_scales(kind):
+@pytest.mark.parametrize("sms", [152, 1])
+def test_sinks_output_scale_and_scales(kind, sms):
     inp, pool, offsets, pl = _case(kind, 12, 2, [3, 1], [640, 96], [2, 200, 5, 300], 5)
     sinks = np.linspace(-2.0, 3.0, 12).astype(np.float32)
     scales = {} if kind == "bf16" else dict(q_scale=1.5, kv_scale=0.37)
     for device_scales in (False, True):
         out, lse, _ = _run(inp, pool, True, group_offsets=offsets, prefix_lens=pl, sinks=sinks, output_scale=0.5, device_scales=device_scales,
-                           **scales)
+                           sm_count=sms, **scales)
         ref, ref_lse = _oracle(inp, True, sinks=sinks, output_scale=0.5, **scales)
         assert_parity(out, lse, ref, ref_lse)
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_ragged_query_counts(kind):
+@pytest.mark.parametrize("sms", [152, 1])
+def test_ragged_query_counts(kind, sms):
     inp, pool, offsets, pl = _case(kind, 12, 8, [4], [320], [8, 100, 9, 8], 6)
     ql = [1, 8, 3, 5]
     for sinks in (None, np.zeros(12, np.float32)):
-        out, lse, _ = _run(inp, pool, True, group_offsets=offsets, prefix_lens=pl, query_lens=ql, sinks=sinks)
+        out, lse, _ = _run(inp, pool, True, group_offsets=offsets, prefix_lens=pl, query_lens=ql, sinks=sinks, sm_count=sms)
         ref, ref_lse = _oracle(inp, True, query_lens=ql, sinks=sinks)
         empty = np.isinf(ref_lse)
         assert empty.any() == (sinks is None)
@@ -143,9 +155,9 @@ def test_ragged_query_counts(kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_bad_pages_and_stale_plans_are_reported(kind):
-    inp, pool, offsets, pl = _case(kind, 12, 1, [2], [64], [100, 5], 7)
-    kw = dict(group_offsets=offsets, prefix_lens=pl)
-    for row, entry in ((0, 1), (1, 2)):
+    inp, pool, offsets, pl = _case(kind, 12, 1, [2], [3200], [100, 5], 7)
+    kw = dict(group_offsets=offsets, prefix_lens=pl, sm_count=1)
+    for row, entry in ((0, 1), (1, 100)):
         table = inp.page_table.clone()
         inp.page_table[row, entry] = 10 ** 6
         with pytest.raises(mla.MlaError) as err:
@@ -153,12 +165,13 @@ def test_bad_pages_and_stale_plans_are_reported(kind):
         assert err.value.status == mla.MLA_ERR_INVALID_ARG
         inp.page_table = table
     # Lengths that have left the plan: below the prefix, and past the suffix's splits.
-    plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, 12, 1, cache_kind=KIND[kind])
+    plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, 12, 1, cache_kind=KIND[kind], sm_count=1)
+    assert plan.info.prefix_ctas > 0
     data = torch.from_numpy(plan.data).cuda()
     ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
     out = torch.empty(2, 1, 12, 512, dtype=torch.bfloat16, device="cuda")
     wide = torch.cat([inp.page_table, torch.zeros(2, 8, dtype=torch.int32)], 1).clamp(min=0).cuda()  # valid ids behind the ends
-    for lens, good in (([164, 69], True), ([164, 192], True), ([63, 69], False), ([164, 193], False), ([-5, 69], False)):
+    for lens, good in (([3300, 3205], True), ([3300, 3328], True), ([3199, 3205], False), ([3300, 3329], False), ([-5, 3205], False)):
         mla.mla_decode_shared(inp.q.cuda(), pool.cuda(), pool.shape[0], wide, wide.shape[1], torch.tensor(lens, dtype=torch.int32).cuda(), plan, data,
                               2, 1, 12, False, 1.0, 1.0, SOFTMAX_SCALE, ws, plan.workspace_bytes, out)
         if good:
@@ -172,7 +185,7 @@ def test_bad_pages_and_stale_plans_are_reported(kind):
 
 
 # Every row group of the segments' kernels: heads, q_len, group size, suffix.
-WIDTHS = {16: (12, 1, 1, 300), 32: (12, 1, 2, 300), 48: (12, 1, 4, 300), 96: (12, 8, 1, 300), "two": (12, 1, 8, 9000)}
+WIDTHS = {16: (12, 1, 1, 300), 32: (12, 2, 1, 300), 48: (12, 1, 4, 300), 96: (12, 8, 1, 300), "two": (12, 1, 8, 9000)}
 ROLES = [0, 1, 2, 3, 4, 5]
 
 
@@ -201,8 +214,9 @@ def test_expired_waits_end_the_call(kind, width):
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("suffix", [40, 9000])
 def test_graph_replays_on_another_stream(kind, suffix):
-    inp, pool, offsets, pl = _case(kind, 12, 1, [8], [512], [suffix] * 8, 9)
-    plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, 12, 1, cache_kind=KIND[kind])
+    inp, pool, offsets, pl = _case(kind, 12, 1, [8], [4096], [suffix] * 8, 9)
+    plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, 12, 1, cache_kind=KIND[kind], sm_count=20)
+    assert plan.info.prefix_ctas > 0
     data, lens = torch.from_numpy(plan.data).cuda(), inp.kv_lens.to(torch.int32).cuda()
     q, kv, pt = inp.q.cuda(), pool.cuda(), inp.page_table.cuda()
     ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")

@@ -39,15 +39,19 @@ CASES = [
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("case", CASES, ids=lambda c: f"h{c[0]}q{c[1]}g{len(c[2])}b{len(c[4])}")
-def test_segments_cover_every_row_and_key_once(case, kind):
+@pytest.mark.parametrize("sms", [152, 2])
+def test_segments_cover_every_row_and_key_once(case, kind, sms):
     heads, q_len, sizes, prefixes, suffixes, causal = case
     offsets = np.concatenate([[0], np.cumsum(sizes)])
     of = np.repeat(np.arange(len(sizes)), sizes)
     lens = [prefixes[of[b]] + suffixes[b] for b in range(len(of))]
     if min(lens) < 1:
         lens = [max(1, n) for n in lens]
-    plan = mla.mla_shared_plan(lens, offsets, prefixes, heads, q_len, causal=causal, cache_kind=kind)
+    plan = mla.mla_shared_plan(lens, offsets, prefixes, heads, q_len, causal=causal, cache_kind=kind, sm_count=sms)
     info, (segs, slots, items) = plan.info, _parts(plan)
+    shared = info.prefix_ctas > 0  # else every request has all of its keys in its own segments
+    if max(prefixes) == 0 or max(sizes) == 1:
+        assert not shared
     per = heads * q_len
     cap = 32 if kind == mla.CACHE_BF16 else 96
     seen = np.zeros((len(lens) * per, 2), int)  # rows covered by prefix and suffix segments
@@ -60,13 +64,13 @@ def test_segments_cover_every_row_and_key_once(case, kind):
         seen[first:first + n, int(suffix)] += 1
         g = of[req]
         if suffix:
-            assert key0 == prefixes[g] and row_in == first - req * per and first // per == (first + n - 1) // per == req
+            assert key0 == (prefixes[g] if shared else 0) and row_in == first - req * per and first // per == (first + n - 1) // per == req
             assert slots[req, 1] == splits <= info.suffix_slots
         else:
             assert key0 == 0 and length == prefixes[g] and req == offsets[g] and row_in == 0
             assert first >= offsets[g] * per and first + n <= offsets[g + 1] * per
             assert (slots[offsets[g]:offsets[g + 1], 0] == splits).all() and splits <= info.prefix_slots
-    has = np.repeat([prefixes[g] > 0 for g in of], per)
+    has = np.repeat([shared and prefixes[g] > 0 for g in of], per)
     assert (seen[:, 1] == 1).all() and (seen[:, 0] == has).all()
     # Items: every split of every segment once, prefixes first.
     want = {(s, i) for s in range(len(segs)) for i in range(segs[s, 6])}
@@ -75,7 +79,7 @@ def test_segments_cover_every_row_and_key_once(case, kind):
     n_prefix = int((segs[:, 5] >= 0).sum())
     assert [s < n_prefix for s, _ in got] == sorted([s < n_prefix for s, _ in got], reverse=True)
     assert info.prefix_ctas + info.suffix_ctas == len(got) and info.prefix_slots + info.suffix_slots <= mla.MAX_SPLITS
-    assert len(got) <= max(2 * 152, len(segs))
+    assert len(got) <= max(2 * sms, len(segs))
     assert plan.workspace_bytes == mla.mla_decode_workspace_size(len(lens), q_len, heads, info.prefix_slots + info.suffix_slots)
 
 
@@ -89,8 +93,14 @@ def test_long_suffixes_have_ctas_of_their_own_size():
     for kind, wide in ((mla.CACHE_FP8, 96), (mla.CACHE_FP4, 96)):
         info = mla.mla_shared_plan([40000] * 8, [0, 8], [20000 // 32 * 32], 12, 1, cache_kind=kind).info
         assert info.prefix_nr == wide and info.suffix_nr == 16
-    short = mla.mla_shared_plan([1100] * 4, [0, 4], [1024], 12, 1).info
-    assert short.prefix_nr == short.suffix_nr == 48  # one launch
+    middle = mla.mla_shared_plan([32800] * 4, [0, 4], [32768], 12, 1).info
+    assert middle.prefix_ctas > 0 and middle.prefix_nr == middle.suffix_nr == 48  # one launch
+
+
+def test_short_prefixes_are_attended_by_every_request():
+    for batch, prefix, shared in ((4, 1024, False), (30, 64, False), (16, 4096, False), (16, 8192, True), (8, 32768, True), (2, 131072, True)):
+        info = mla.mla_shared_plan([prefix + 100] * batch, [0, batch], [prefix], 12, 1).info
+        assert (info.prefix_ctas > 0) == shared, (batch, prefix)
 
 
 @pytest.mark.parametrize("bad", [
