@@ -144,7 +144,7 @@ struct SplitRange {
 
 // A split of a segment of a decode over shared prefixes, as item_segment of the
 // E4M3 kernel: keys count from the segment's first one.
-__device__ __forceinline__ bool segment_range(const DecodeParams& p, SplitRange& r) {
+__device__ __forceinline__ bool segment_range(const DecodeParams& p, int max_rows, SplitRange& r) {
   const int entry = p.cta_items[blockIdx.x];
   const int seg = entry >> MLA_ITEM_B_SHIFT;
   const int split =
@@ -156,11 +156,15 @@ __device__ __forceinline__ bool segment_range(const DecodeParams& p, SplitRange&
   const int4 a = reinterpret_cast<const int4*>(p.segs + seg)[0];
   const int4 c = reinterpret_cast<const int4*>(p.segs + seg)[1];
   const Segment s{a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  if (!segment_fits(p, s, split, max_rows)) {
+    if (threadIdx.x == 0) report(p.status, MLA_ERR_INVALID_ARG);
+    return false;
+  }
   const bool suffix = s.len < 0;
   r.q_b = suffix && p.query_lens ? p.query_lens[s.request] : p.q_len;
   const int len = suffix ? p.kv_lens[s.request] - s.key0 : s.len;
   const bool bad = len < 0 || r.q_b < 1 || r.q_b > p.q_len ||
-                   (suffix && p.causal && len < r.q_b) || split >= s.splits ||
+                   (suffix && p.causal && len < r.q_b) ||
                    s.chunk < MLA_TILE_TOKENS || (s.chunk % MLA_TILE_TOKENS) != 0 ||
                    static_cast<int64_t>(s.splits) * s.chunk < len ||
                    (s.splits > 1 && static_cast<int64_t>(s.splits - 1) * s.chunk >= len) ||
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(CfgQ<NR>::kThreads, 1)
   int b = 0;
   if constexpr (kShared) {
     if (p.chain & SHARED_RELEASE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!segment_range(p, sr)) {
+    if (!segment_range(p, NR, sr)) {
       if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
       return;
     }

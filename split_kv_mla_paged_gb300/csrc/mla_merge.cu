@@ -43,8 +43,8 @@ __device__ __forceinline__ void merge_body(const MergeParams& p) {
   if constexpr (kShared) {
     const int b = row / p.rows_per_req;
     const int2 n = p.shared_slots[b];
-    n_prefix = n.x;
-    ns = n.x + n.y;
+    n_prefix = max(0, min(n.x, p.suffix_slot));
+    ns = n_prefix + max(0, min(n.y, p.stride_s - p.suffix_slot));
     if (p.query_lens && (row - b * p.rows_per_req) / p.num_heads >= p.query_lens[b]) ns = 0;
   } else if (p.splits) {
     ns = min(p.splits[row / p.rows_per_req], p.stride_s);

@@ -231,10 +231,14 @@ struct ItemInfo {
 // a request of its own; a prefix, which every row sees whole, gets a length that
 // puts that limit behind its end.  False (reported) where the plan does not fit.
 __device__ __forceinline__ bool item_segment(const DecodeParams& p, int seg, int split,
-                                             ItemInfo& it) {
+                                             int max_rows, ItemInfo& it) {
   const int4 a = reinterpret_cast<const int4*>(p.segs + seg)[0];
   const int4 c = reinterpret_cast<const int4*>(p.segs + seg)[1];
   const Segment s{a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  if (!segment_fits(p, s, split, max_rows)) {
+    if (threadIdx.x == 0) report(p.status, MLA_ERR_INVALID_ARG);
+    return false;
+  }
   const bool suffix = s.len < 0;
   it.b = s.request;
   it.split = split;
@@ -243,7 +247,7 @@ __device__ __forceinline__ bool item_segment(const DecodeParams& p, int seg, int
   const int len = suffix ? p.kv_lens[s.request] - s.key0 : s.len;
   it.nsplit = s.splits;
   const bool bad = len < 0 || it.q_b < 1 || it.q_b > p.q_len ||
-                   (suffix && p.causal && len < it.q_b) || split >= s.splits ||
+                   (suffix && p.causal && len < it.q_b) ||
                    s.chunk < kTileTokens || (s.chunk % kTileTokens) != 0 ||
                    static_cast<int64_t>(s.splits) * s.chunk < len ||
                    (s.splits > 1 && static_cast<int64_t>(s.splits - 1) * s.chunk >= len) ||
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
     } else {
       fits = item_segment(
           p, seg, (entry >> MLA_ITEM_S_SHIFT) & ((1 << (MLA_ITEM_B_SHIFT - MLA_ITEM_S_SHIFT)) - 1),
-          first);
+          NR, first);
     }
     if (!fits) {
       if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -184,6 +184,53 @@ def test_bad_pages_and_stale_plans_are_reported(kind):
     assert_parity(out, lse, *_oracle(inp, False))
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_plan_data_that_does_not_fit_is_reported(kind):
+    # The plan's arrays of another call, or overwritten: nothing outside the batch, its
+    # pages and the workspace is read or written, and the status says so.
+    inp, pool, offsets, pl = _case(kind, 12, 1, [8], [4096], [200] * 8, 4)
+    plan = mla.mla_shared_plan(inp.kv_lens.tolist(), offsets, pl, 12, 1, cache_kind=KIND[kind], sm_count=20)
+    n, info = plan.info.num_segments, plan.info
+    assert info.prefix_ctas > 0
+    q, kv, pt, lens = inp.q.cuda(), pool.cuda(), inp.page_table.cuda(), inp.kv_lens.to(torch.int32).cuda()
+    ws = torch.zeros(plan.workspace_bytes + 4096, dtype=torch.uint8, device="cuda")
+    out = torch.full((9, 1, 12, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    FIRST, ROWS, IN_REQ, REQUEST, KEY0, LEN, SPLITS, CHUNK = range(8)
+    last = n - 1  # a suffix; segment 0 is a prefix
+    bad = [(last, REQUEST, 8), (last, REQUEST, -1), (last, FIRST, 96), (last, FIRST, -1), (last, ROWS, 97), (last, ROWS, 0), (last, IN_REQ, 5),
+           (last, IN_REQ, -1), (last, KEY0, 16), (last, KEY0, -32), (last, SPLITS, 0), (last, CHUNK, 100), (0, REQUEST, 8), (0, FIRST, 90),
+           (0, LEN, 1 << 20), (0, KEY0, 1 << 30), (0, SPLITS, 0), (0, ROWS, 1000)]
+    for seg, field, value in [(None, None, None)] + bad:
+        data = plan.data.copy()
+        if seg is not None:
+            data[8 * seg + field] = value
+        ws[:plan.workspace_bytes].zero_()
+        mla.mla_decode_shared(q, kv, kv.shape[0], pt, pt.shape[1], lens, plan, torch.from_numpy(data).cuda(), 8, 1, 12, False, 1.0, 1.0,
+                              SOFTMAX_SCALE, ws, plan.workspace_bytes, out)
+        if seg is None:
+            mla.mla_decode_status(ws)
+            continue
+        with pytest.raises(mla.MlaError) as err:
+            mla.mla_decode_status(ws)
+        assert err.value.status == mla.MLA_ERR_INVALID_ARG, (seg, field, value)
+    # Numbers of partials: at most the workspace's slots are merged.
+    data = plan.data.copy()
+    data[8 * n:8 * n + 16] = 1 << 20
+    ws[:plan.workspace_bytes].zero_()
+    mla.mla_decode_shared(q, kv, kv.shape[0], pt, pt.shape[1], lens, plan, torch.from_numpy(data).cuda(), 8, 1, 12, False, 1.0, 1.0,
+                          SOFTMAX_SCALE, ws, plan.workspace_bytes, out)
+    torch.cuda.synchronize()
+    assert (out[8] == 7.0).all() and (ws[plan.workspace_bytes:] == 0).all()
+    # One request's arrays behind a call for eight.
+    small = mla.mla_shared_plan([300], [0, 1], [0], 12, 1, cache_kind=KIND[kind])
+    data = np.resize(small.data, plan.data.shape)
+    mla.mla_decode_shared(q, kv, kv.shape[0], pt, pt.shape[1], lens, plan, torch.from_numpy(data).cuda(), 8, 1, 12, False, 1.0, 1.0,
+                          SOFTMAX_SCALE, ws, plan.workspace_bytes, out)
+    with pytest.raises(mla.MlaError):
+        mla.mla_decode_status(ws)
+    assert (out[8] == 7.0).all() and (ws[plan.workspace_bytes:] == 0).all()
+
+
 # Every row group of the segments' kernels: heads, q_len, group size, suffix.
 WIDTHS = {16: (12, 1, 1, 300), 32: (12, 2, 1, 300), 48: (12, 1, 4, 300), 96: (12, 8, 1, 300), "two": (12, 1, 8, 9000)}
 ROLES = [0, 1, 2, 3, 4, 5]
