@@ -552,7 +552,7 @@ MLA_API int mla_verify_drafts(const mla_verify_args_t* args, void* stream);
  * q_scale_dev, kv_scale_dev, softmax_scale_dev   device fp32 or NULL, as in
  *                mla_decode_options_t.
  * status         int32 or NULL: set to MLA_ERR_INVALID_ARG for a length outside [0,
- *                min(weights_stride, previous_stride, 32 * max_pages_per_req)] or a
+ *                min(weights_stride, previous_stride, 32 * max_pages_per_req, 2^31 - 129)] or a
  *                query count outside [1, q_len] (that request is skipped) or a bad
  *                page id, to MLA_ERR_TIMEOUT for a wait that ran out; never cleared.
  * All on the device; no workspace.

@@ -89,7 +89,9 @@ struct KwWalk {
 __device__ __forceinline__ int kw_len(const mla_key_weights_args_t& a, int b, bool& bad) {
   const int len = a.kv_lens[b];
   const int q_b = a.query_lens ? a.query_lens[b] : a.q_len;
-  bad = len < 0 || len > a.weights_stride || (a.previous && len > a.previous_stride) ||
+  // (Tiles are counted in 32 bits: no length that a tile's end would overflow.)
+  bad = len < 0 || len > INT32_MAX - kKwTile || len > a.weights_stride ||
+        (a.previous && len > a.previous_stride) ||
         static_cast<int64_t>(len) > static_cast<int64_t>(a.max_pages_per_req) * MLA_PAGE_SIZE ||
         q_b < 1 || q_b > a.q_len;
   return bad ? 0 : len;

@@ -8,6 +8,8 @@ l, the difference) plus the fp32 sum of 576 products, 2^-24 * 576 times the sum 
 their magnitudes at worst; 2^-22 for the exponential itself, and 2^-24 per added
 row and for decay * previous.  The relative error of the sum is ln 2 times the
 exponent's plus these."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -189,6 +191,16 @@ def test_bad_requests_are_skipped_and_reported():
         _args(inp, pool, lens, lse, out, status, **kw)
         assert int(status) == mla.MLA_ERR_INVALID_ARG
         assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2]) and (out[1] == -7.0).all()
+    # A length that 32-bit tile positions cannot hold, within strides that claim as much.
+    out = torch.full((300,), -7.0, device="cuda")
+    status.zero_()
+    lens = torch.tensor([200, 2 ** 31 - 1], dtype=torch.int32).cuda()
+    qd, kvd, pt = inp.q.cuda(), pool.cuda(), inp.page_table[0].contiguous().cuda()
+    a = mla.KeyWeightsArgs(q=qd.data_ptr(), kv_pages=kvd.data_ptr(), num_pages=kvd.shape[0], page_table=pt.data_ptr(), kv_lens=lens.data_ptr(),
+                           lse=lse.data_ptr(), weights=out.data_ptr(), weights_stride=2 ** 31, status=status.data_ptr(), max_pages_per_req=1 << 26,
+                           batch=2, q_len=1, num_heads=12, q_scale=1.0, kv_scale=1.0, softmax_scale=SOFTMAX_SCALE)
+    assert mla.load_library().mla_key_weights(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    assert int(status) == mla.MLA_ERR_INVALID_ARG and torch.equal(out, good[0])
     table = inp.page_table.clone()
     table[0, 1] = 10 ** 6
     status.zero_()
