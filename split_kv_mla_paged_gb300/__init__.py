@@ -7,6 +7,7 @@ streams.  There is no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import operator
@@ -1276,7 +1277,6 @@ def _decode_shared(q, kv_pages, page_table, lens, group_offsets, prefix_lens, nu
                            cache_kind=kind, sm_count=sm_count)
     lens_d, plan_d = torch.from_numpy(lens).to(dev), torch.from_numpy(plan.data).to(dev)
     ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dev)
-    mla_decode_workspace_init(ws, plan.workspace_bytes, stream)
     out = torch.empty((batch, q_len, num_heads, LATENT_DIM), dtype=torch.bfloat16, device=dev)
     lse = torch.empty((batch, q_len, num_heads), dtype=torch.float32, device=dev)
     out_f32 = torch.empty(out.shape, dtype=torch.float32, device=dev) if want_f32 else None
@@ -1291,11 +1291,14 @@ def _decode_shared(q, kv_pages, page_table, lens, group_offsets, prefix_lens, nu
         extra["sinks"] = torch.as_tensor(sinks, dtype=torch.float32).to(dev)
     if query_lens is not None:
         extra["query_lens"] = torch.as_tensor(query_lens, dtype=torch.int32).to(dev).contiguous()
-    mla_decode_shared(q, kv_pages, kv_pages.shape[0], page_table, page_table.shape[1], lens_d, plan,
-                      plan_d, batch, q_len, num_heads, causal, *host, ws, plan.workspace_bytes, out,
-                      lse, out_f32, output_scale=output_scale, stream=stream, **extra)
-    if check_status:
-        mla_decode_status(ws, stream)
+    with _ordered(stream, dev) as side:
+        mla_decode_workspace_init(ws, plan.workspace_bytes, side)
+        mla_decode_shared(q, kv_pages, kv_pages.shape[0], page_table, page_table.shape[1], lens_d,
+                          plan, plan_d, batch, q_len, num_heads, causal, *host, ws,
+                          plan.workspace_bytes, out, lse, out_f32, output_scale=output_scale,
+                          stream=side, **extra)
+        if check_status:
+            mla_decode_status(ws, side)
     return out, lse, out_f32
 
 
@@ -1392,13 +1395,14 @@ def key_weights(q, kv_pages, page_table, kv_lens, lse, *, num_heads: int, q_len:
     if query_lens is not None:
         query_lens = torch.as_tensor(query_lens, dtype=torch.int32).to(dev).contiguous()
     status = torch.zeros((1,), dtype=torch.int32, device=dev)
-    mla_key_weights(q, kv_pages, kv_pages.shape[0], page_table, page_table.shape[1],
-                    torch.from_numpy(lens).to(dev), lse, weights, batch, q_len, num_heads, causal,
-                    q_scale, kv_scale, softmax_scale, cache_kind=_cache_kind(kv_pages),
-                    previous=previous, decay=decay, query_lens=query_lens, status=status,
-                    stream=stream)
-    _check_status_tensor(status, stream, "key_weights: a length, query count or page id is out of "
-                                         "range, or a device wait ran out")
+    lens_d = torch.from_numpy(lens).to(dev)
+    with _ordered(stream, dev) as side:
+        mla_key_weights(q, kv_pages, kv_pages.shape[0], page_table, page_table.shape[1], lens_d, lse,
+                        weights, batch, q_len, num_heads, causal, q_scale, kv_scale, softmax_scale,
+                        cache_kind=_cache_kind(kv_pages), previous=previous, decay=decay,
+                        query_lens=query_lens, status=status, stream=side)
+    _check_status_tensor(status, "key_weights: a length, query count or page id is out of range, "
+                                 "or a device wait ran out")
     return weights
 
 
@@ -1412,22 +1416,38 @@ def verify_drafts(target_probs, draft_tokens, uniforms, *, draft_probs=None, que
     accepted = torch.empty((batch,), dtype=torch.int32, device=dev)
     new_lens = None if kv_lens is None else torch.empty_like(accepted)
     status = torch.zeros((1,), dtype=torch.int32, device=dev)
-    mla_verify_drafts(target_probs, draft_tokens, uniforms, tokens, accepted,
-                      draft_probs=draft_probs, query_lens=query_lens, kv_lens=kv_lens,
-                      new_lens=new_lens, status=status, stream=stream)
-    _check_status_tensor(status, stream, "verify_drafts: a query count or draft is out of range")
+    with _ordered(stream, dev) as side:
+        mla_verify_drafts(target_probs, draft_tokens, uniforms, tokens, accepted,
+                          draft_probs=draft_probs, query_lens=query_lens, kv_lens=kv_lens,
+                          new_lens=new_lens, status=status, stream=side)
+    _check_status_tensor(status, "verify_drafts: a query count or draft is out of range")
     return tokens, accepted, new_lens
 
 
-def _check_status_tensor(status, stream, message: str) -> None:
-    """Wait for `stream` and raise where a call's status tensor was set."""
+@contextlib.contextmanager
+def _ordered(stream, dev):
+    """`stream` (None: the current one) for work that starts behind what the current
+    stream has been given (zeroed tensors, memory that it used before) and ends ahead
+    of what it is given next (memory that the caller frees)."""
     import torch
-    dev = status.device
+    current = torch.cuda.current_stream(dev)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev)
-    (stream if stream is not None else torch.cuda.current_stream(dev)).synchronize()
-    if int(status.item()) != MLA_OK:
-        raise MlaError(int(status.item()), message)
+    if stream is None or stream == current:
+        yield current
+        return
+    stream.wait_stream(current)
+    try:
+        yield stream
+    finally:
+        current.wait_stream(stream)
+
+
+def _check_status_tensor(status, message: str) -> None:
+    """Wait for the current stream and raise where a call's status tensor was set."""
+    code = int(status.item())
+    if code != MLA_OK:
+        raise MlaError(code, message)
 
 
 def evict(pool: PagePool, kv_pages, page_lists, kv_lens, weights, keep, *, first: int = 0,
@@ -1440,7 +1460,8 @@ def evict(pool: PagePool, kv_pages, page_lists, kv_lens, weights, keep, *, first
     integers (keep one per request, or one for all); weights float32 [requests,
     keys].  Returns (new page lists, new lengths (host), new weights).  Needs free
     pages for what stays beside the pages that are in use; MlaError
-    (MLA_ERR_NO_PAGES) otherwise, with nothing changed."""
+    (MLA_ERR_NO_PAGES) otherwise.  After an error the old pages are as they were, and
+    no page is taken from the pool."""
     import torch
     lens = _host_ids(kv_lens, "kv_lens")
     batch = lens.shape[0]
@@ -1469,19 +1490,22 @@ def evict(pool: PagePool, kv_pages, page_lists, kv_lens, weights, keep, *, first
             out[b, :r.shape[0]] = r
         return torch.from_numpy(out).to(dev)
 
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev)
-    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+    try:
         kept = torch.empty((batch, most), dtype=torch.int32, device=dev)
         new_weights = torch.zeros((batch, most), dtype=torch.float32, device=dev)
         both = torch.from_numpy(np.stack([lens, keep])).to(dev)
+        old_table, new_table = table(lists), table(new_lists)
         counts, status = torch.zeros_like(both[0]), torch.zeros_like(both[0, :1])
-        mla_evict_select(weights, both[0], both[1], kept, counts, first=first, last=last,
-                         new_weights=new_weights, status=status)
-        mla_rows_move(kv_pages, kv_pages.shape[0], table(lists), kv_pages, kv_pages.shape[0],
-                      table(new_lists), kept, counts, cache_kind=_cache_kind(kv_pages),
-                      status=status)
-    _check_status_tensor(status, stream, "evict: a length or page id is out of range")
+        with _ordered(stream, dev) as side:
+            mla_evict_select(weights, both[0], both[1], kept, counts, first=first, last=last,
+                             new_weights=new_weights, status=status, stream=side)
+            mla_rows_move(kv_pages, kv_pages.shape[0], old_table, kv_pages, kv_pages.shape[0],
+                          new_table, kept, counts, cache_kind=_cache_kind(kv_pages), status=status,
+                          stream=side)
+        _check_status_tensor(status, "evict: a length or page id is out of range")
+    except BaseException:
+        pool.release(fresh)
+        raise
     for p in lists:
         pool.release(p)
     return new_lists, stay, new_weights

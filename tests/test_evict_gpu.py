@@ -203,3 +203,33 @@ def test_evict_through_the_pool(kind):
     with pytest.raises(mla.MlaError):
         mla.evict(pool, dev, [shared], [700], torch.from_numpy(w[3:]).cuda(), 3 * 32 + 1)
     assert pool.free_pages == 3 and len(held) > 0 and np.array_equal(_bytes(dev), got)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_refused_evictions_take_no_pages(kind):
+    pool = mla.PagePool(16)
+    lists = [pool.alloc(3)]
+    dev = _pool(kind, 16, 5).cuda()
+    w = torch.rand(1, 96, device="cuda")
+    for bad, kw in ((w.double(), {}), (w.cpu(), {}), (w.t(), {}), (w, dict(first=-1)), (w, dict(last=-1))):
+        with pytest.raises((ValueError, mla.MlaError)):
+            mla.evict(pool, dev, lists, [90], bad, 40, **kw)
+        assert pool.free_pages == 13 and all(pool.references(int(p)) == 1 for p in lists[0])
+
+
+def test_another_stream_waits_for_the_current_one():
+    # The zeroed outputs and the status of a call are made on the current stream.
+    side = torch.cuda.Stream()
+    pool = mla.PagePool(64)
+    lists = [pool.alloc(20)]
+    dev = _pool(mla.CACHE_FP8, 64, 5).cuda()
+    w = torch.from_numpy(_weights(1, 640, 6, "tail")).cuda()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    lists, lens, new_w = mla.evict(pool, dev, lists, [640], w, 100, stream=side)
+    ref = _plain(w[0].cpu().numpy(), 640, 100, 0, 0)
+    assert np.array_equal(new_w[0].cpu().numpy(), w[0, ref].cpu().numpy())
+    probs = torch.rand(1, 2, 64, device="cuda")
+    torch.cuda._sleep(50_000_000)
+    with pytest.raises(mla.MlaError):
+        mla.verify_drafts(probs, torch.full((1, 1), 64, dtype=torch.int32, device="cuda"), torch.rand(1, 2, device="cuda"), stream=side.cuda_stream)
