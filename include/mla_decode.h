@@ -439,9 +439,10 @@ MLA_API int mla_decode_fp4_sparse(const void* q_fp8, const void* kv_pages_fp4,
  * data_out       host int32[capacity] or NULL (then only *plan_out is set): the
  *                plan's arrays, plan_out->data_len values, to be copied to the
  *                device.
- * The plan stays valid while each request's kv_len stays within its suffix's
- * splits ((splits - 1) * chunk < kv_len - prefix <= splits * chunk, which the
- * device checks): at least until the next multiple of 128 keys past the prefix.
+ * The plan stays valid while the number of keys that each request attends by itself
+ * (those behind its prefix, or all of them) stays within its splits ((splits - 1) *
+ * chunk < keys <= splits * chunk, which the device checks): at least until their next
+ * multiple of 128.
  */
 typedef struct {
   int32_t cache_kind, batch, groups, q_len, num_heads, causal;
@@ -509,8 +510,9 @@ MLA_API int mla_decode_shared(const void* q, const void* kv_pages, int64_t num_p
  * status         int32 or NULL: set to MLA_ERR_INVALID_ARG for a query count outside
  *                [1, q_len] (that request is skipped) or a draft outside the
  *                vocabulary (it is rejected); never cleared by the call.
- * All on the device.  Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (sizes),
- * MLA_ERR_CUDA.  Zero-initialise the structure.
+ * All on the device; but for new_lens, no output may overlap an input.  Errors:
+ * MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (sizes), MLA_ERR_CUDA.  Zero-initialise
+ * the structure.
  */
 #define MLA_PROBS_F32 0
 #define MLA_PROBS_BF16 1

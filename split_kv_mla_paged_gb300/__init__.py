@@ -893,8 +893,8 @@ def mla_rows_move(src_pool, src_pages: int, src_table, dst_pool, dst_pages: int,
 def shared_groups(page_lists, kv_lens, q_len: int = 1, least: int = PAGE_SIZE):
     """Groups of consecutive requests whose page lists begin with the same pages,
     for mla_shared_plan: (group_offsets, prefix_lens).  A request joins the group
-    before it while at least `least` keys stay shared; the keys of the last q_len
-    positions are never shared."""
+    before it while at least `least` keys stay shared and no more keys are attended
+    than without it; the keys of the last q_len positions are never shared."""
     lens = _host_ids(kv_lens, "kv_lens")
     lists = [_host_ids(p, "page_lists") for p in page_lists]
     if len(lists) != lens.shape[0]:
@@ -909,7 +909,10 @@ def shared_groups(page_lists, kv_lens, q_len: int = 1, least: int = PAGE_SIZE):
             room = min(room, lists[start].shape[0], lists[b].shape[0])
             same = lists[start][:room] == lists[b][:room]
             pages = room if bool(same.all()) else int(np.argmin(same))
-            if pages * PAGE_SIZE >= max(least, PAGE_SIZE):
+            # What is not attended again: the prefix, by all requests but one.
+            before = (b - start - 1) * prefixes[-1] if b - start > 1 else 0
+            if (pages * PAGE_SIZE >= max(least, PAGE_SIZE)
+                    and (b - start) * pages * PAGE_SIZE >= before):
                 if b - start > 1:
                     prefixes[-1] = pages * PAGE_SIZE
                 else:

@@ -142,6 +142,12 @@ def test_groups_of_a_batch():
     assert offsets.tolist() == [0, 2] and prefixes.tolist() == [256]
     offsets, prefixes = mla.shared_groups(lists[:4], [300, 300, 310, 320], least=289)
     assert offsets.tolist() == [0, 1, 2, 3, 4] and prefixes.tolist() == [0] * 4
+    # One that shares little with a group that shares much stays by itself.
+    long = list(range(100))
+    offsets, prefixes = mla.shared_groups([long + [200], long + [201], long[:2] + [202], long[:2] + [203]], [3210, 3220, 90, 90])
+    assert offsets.tolist() == [0, 2, 4] and prefixes.tolist() == [3200, 64]
+    offsets, prefixes = mla.shared_groups([long + [200], long + [201], long[:60] + [202]], [3210, 3220, 1930])
+    assert offsets.tolist() == [0, 3] and prefixes.tolist() == [1920]
 
 
 @pytest.mark.parametrize("seed", range(30))
