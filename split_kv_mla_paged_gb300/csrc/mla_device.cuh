@@ -101,12 +101,13 @@ struct DecodeParams {
 __device__ __forceinline__ bool segment_fits(const DecodeParams& p, const Segment& s, int split,
                                              int max_rows) {
   const bool suffix = s.len < 0;
-  const int64_t all = static_cast<int64_t>(p.batch) * p.rows_per_req;
+  const int per_req = p.q_len * p.num_heads;  // (rows_per_req is the launch's)
+  const int64_t all = static_cast<int64_t>(p.batch) * per_req;
   const int slots = suffix ? p.max_splits - p.suffix_slot : p.suffix_slot;
   return s.request >= 0 && s.request < p.batch && s.n_rows >= 1 && s.n_rows <= max_rows &&
          s.first_row >= 0 && static_cast<int64_t>(s.first_row) + s.n_rows <= all &&
          s.row_in_req >= 0 && s.row_in_req <= s.first_row &&
-         (!suffix || s.row_in_req <= p.rows_per_req - s.n_rows) && s.key0 >= 0 &&
+         (!suffix || s.row_in_req <= per_req - s.n_rows) && s.key0 >= 0 &&
          s.key0 % MLA_PAGE_SIZE == 0 && split < s.splits && split < slots;
 }
 

@@ -210,9 +210,9 @@ def test_plan_data_that_does_not_fit_is_reported(kind):
         if seg is None:
             mla.mla_decode_status(ws)
             continue
-        with pytest.raises(mla.MlaError) as err:
-            mla.mla_decode_status(ws)
-        assert err.value.status == mla.MLA_ERR_INVALID_ARG, (seg, field, value)
+        torch.cuda.synchronize()
+        code = int(ws[:4].view(torch.int32))
+        assert code == mla.MLA_ERR_INVALID_ARG, (seg, field, value)
     # Numbers of partials: at most the workspace's slots are merged.
     data = plan.data.copy()
     data[8 * n:8 * n + 16] = 1 << 20
