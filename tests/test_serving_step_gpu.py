@@ -75,7 +75,7 @@ def test_step(kind):
     q = q.bfloat16() if bf16 else q.to(torch.float8_e4m3fn).view(torch.uint8)
     table = _table(lists)
     args = dict(num_heads=HEADS, q_len=Q, causal=True, softmax_scale=SOFTMAX_SCALE)
-    out, lse, _ = mla.decode(q.cuda(), pool, table.cuda(), lens, group_offsets=offsets, prefix_lens=prefixes, **args)
+    out, lse, _ = mla.decode(q.cuda(), pool, table.cuda(), lens, group_offsets=offsets, prefix_lens=prefixes, sm_count=1, **args)
     held = _values(kind, pool)
     ref, ref_lse = oracle.decode_rows(q, held, table, torch.tensor(lens, dtype=torch.int32), **args)
     assert_parity(out, lse, ref, ref_lse)
@@ -127,3 +127,85 @@ def test_step(kind):
         k = int(kept_lens[b])
         added = (again[b, :k] - 0.5 * kept_w[b, :k]).sum()
         assert abs(float(added) - HEADS) <= 1e-3 * HEADS
+
+
+def _step(kind, seed, batch=6, prefix=4096, own=700, sms=16):
+    """A step's calls on tensors of their own, as one function without allocations,
+    and those whose contents are its results."""
+    g = torch.Generator().manual_seed(seed)
+    bf16, rows = kind == mla.CACHE_BF16, batch * Q * HEADS
+    each, shared = (own + 31) // 32, prefix // 32
+    pages = shared + batch * each
+    if kind == mla.CACHE_FP4:
+        pool = torch.randint(0, 256, (pages, mla.FP4_PAGE_BYTES), generator=g, dtype=torch.uint8)
+        pool[:, 8192:8704] &= 7
+        pool[:, 8704:] = (torch.randn(pages, 2048, generator=g) * 0.5).to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        pool = torch.randn(pages, 32, 576, generator=g) * 0.5
+        pool = pool.bfloat16() if bf16 else pool.to(torch.float8_e4m3fn).view(torch.uint8)
+    q = torch.randn(batch, Q, HEADS, 576, generator=g) * 0.5
+    q = q.bfloat16() if bf16 else q.to(torch.float8_e4m3fn).view(torch.uint8)
+    order = torch.randperm(pages, generator=g).int()
+    table = torch.cat([order[:shared].expand(batch, -1), order[shared:].reshape(batch, each)], 1).contiguous().cuda()
+    lens = [prefix + own - 9 * b for b in range(batch)]
+    plan = mla.mla_shared_plan(lens, [0, batch], [prefix], HEADS, Q, causal=True, cache_kind=kind, sm_count=sms)
+    assert plan.info.prefix_ctas > 0
+    data = torch.from_numpy(plan.data).cuda()
+    q, pool, lens_d = q.cuda(), pool.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out = torch.empty(batch, Q, HEADS, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(batch, Q, HEADS, device="cuda")
+    weights = torch.rand(batch, lens[0], generator=g).cuda()
+    target = torch.softmax(3 * torch.randn(batch, Q, VOCAB, generator=g), -1).cuda()
+    drafts, u = target[:, :Q - 1].argmax(-1).int(), torch.rand(batch, Q, generator=g).cuda()
+    tokens, accepted, left = (torch.empty(batch, n, dtype=torch.int32, device="cuda") for n in (Q, 1, 1))
+    keep = torch.tensor([500 + 40 * b for b in range(batch)], dtype=torch.int32).cuda()
+    most = 32 * ((500 + 40 * batch) // 32 + 1)
+    kept, kept_w = torch.full((batch, most), -1, dtype=torch.int32, device="cuda"), torch.zeros(batch, most, device="cuda")
+    counts, status = torch.zeros(batch, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    moved = torch.zeros((batch * most // 32, *pool.shape[1:]), dtype=pool.dtype, device="cuda")
+    to = torch.randperm(moved.shape[0], generator=g).int().reshape(batch, -1).cuda()
+
+    def run():
+        mla.mla_decode_shared(q, pool, pages, table, table.shape[1], lens_d, plan, data, batch, Q, HEADS, True, 1.0, 1.0, SOFTMAX_SCALE, ws,
+                              plan.workspace_bytes, out, lse)
+        mla.mla_key_weights(q, pool, pages, table, table.shape[1], lens_d, lse, weights, batch, Q, HEADS, True, 1.0, 1.0, SOFTMAX_SCALE,
+                            cache_kind=kind, previous=weights, decay=0.5, status=status)
+        mla.mla_verify_drafts(target, drafts, u, tokens, accepted, kv_lens=lens_d, new_lens=left, status=status)
+        mla.mla_evict_select(weights, left, keep, kept, counts, first=4, last=8, new_weights=kept_w, status=status)
+        mla.mla_rows_move(pool, pages, table, moved, moved.shape[0], to, kept, counts, cache_kind=kind, status=status)
+
+    return run, (out, lse, weights, tokens, accepted, left, kept, kept_w, counts, moved, ws[:4], status)
+
+
+@pytest.mark.parametrize("kind", [mla.CACHE_FP8, mla.CACHE_BF16, mla.CACHE_FP4])
+def test_two_captured_steps_at_once(kind):
+    # Two steps in graphs of their own, replayed on two streams at a time: the bits of
+    # the steps called one after the other.
+    times, want, graphs = 8, [], []
+    for seed in (1, 2):
+        run, results = _step(kind, seed)
+        for _ in range(times + 1):
+            run()
+        torch.cuda.synchronize()
+        assert int(results[-1]) == 0 and not results[-2].any()
+        want.append([r.clone() for r in results])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for seed, stream in zip((1, 2), streams):
+        run, results = _step(kind, seed)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            run()
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            run()
+        graphs.append((graph, results))
+    for _ in range(times):
+        for (graph, _), stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, results), ref in zip(graphs, want):
+        for a, b in zip(results, ref):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
