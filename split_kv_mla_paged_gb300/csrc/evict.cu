@@ -14,10 +14,11 @@
 // once; the other digits are counted in the short list.  The counts are joined in
 // the first CTA of the cluster.
 //
-// Measured (calls in a CUDA graph): 16 requests of 131,072 keys, 16,384 kept, 20.8 us
-// (3 us until all weights are in shared memory, 1.8, 2.4 and 3.5 us for the passes, 1.5
+// Measured (calls in a CUDA graph): 16 requests of 131,072 keys, 16,384 kept, 20.7 us
+// (3 us until all weights are in shared memory, 1.8, 2 and 3.1 us for the passes, 1.5
 // to 2 us for each digit's search across the cluster); one of 1,048,576 keys, 131,072
-// kept, 41 us (16 CTAs read them three times from L2); 4 of 2,111 keys 7 us.
+// kept, 39 us (16 CTAs read them three times from L2: 4.5, 8 and 9 us); 4 of 2,111 keys
+// 6.3 us.
 //
 // Move.  Bytes only: a warp copies the 288 16-byte vectors of 8 E4M3 or 4 BF16 rows,
 // nine per lane and all in flight, or 8 rows of the 4-bit cache's three planes.
@@ -162,8 +163,16 @@ __global__ void __launch_bounds__(kEvictThreads, 1) mla_evict_select_kernel(cons
   // Keys of positions k .. k + 3 from their weights.  Behind the end they are 0, which
   // no weight is ranked below: as positions behind all others, they never stay.
   auto keys_of = [&](int base, int k, const float (&v)[4], uint32_t (&key)[4]) {
+    // Weights from +0 to infinity, as sums of exponentials are, need one bit only.
+    const uint32_t top = max(max(__float_as_uint(v[0]), __float_as_uint(v[1])),
+                             max(__float_as_uint(v[2]), __float_as_uint(v[3])));
+    if (top <= 0x7F800000u) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) key[u] = evict_key(v[u]);
+      for (int u = 0; u < 4; ++u) key[u] = __float_as_uint(v[u]) | 0x80000000u;
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) key[u] = evict_key(v[u]);
+    }
     if (base < p.first || base + 128 > min(tail, k1)) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -326,43 +335,34 @@ __global__ void __launch_bounds__(kEvictThreads, 1) mla_evict_select_kernel(cons
     }
     const uint32_t top = find(0, 2048);
     prefix = top << 21;
-    // Keys with that first digit are the candidates; those above it stay.
-    uint32_t listed = 0;
-    const uint32_t room = static_cast<uint32_t>(p.candidates);
+    // Keys with that first digit are the candidates, a list per lane of every 32nd word
+    // (one list in the order of the lanes, whose places a scan gave, took 41 us where this
+    // takes 39); those above it stay.
+    int listed = 0;
+    const int room = p.candidates / 32;
+    bool complete = true;
     each([&](int, const uint32_t (&key)[kBatch][4], int blocks) {
-      uint32_t is = 0;
+      complete &= listed + 4 * min(blocks, kBatch) <= room;
 #pragma unroll
       for (int m = 0; m < kBatch; ++m)
         if (m < blocks) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             if (key[m][u] > (prefix | 0x1FFFFFu)) ++above;
-            if (key[m][u] - prefix < 0x200000u) ++is;
+            if (complete && key[m][u] - prefix < 0x200000u)
+              my_list[32 * listed++ + lane] = key[m][u];
           }
         }
-      uint32_t all;  // (as one byte pair: up to 16 a lane, 512 in all)
-      uint32_t at = listed + scan_bytes(is, lane, all);
-      listed += all;
-      if (listed <= room && is) {  // (a list that is too short is not read)
-#pragma unroll
-        for (int m = 0; m < kBatch; ++m)
-          if (m < blocks) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (key[m][u] - prefix < 0x200000u) my_list[at++] = key[m][u];
-          }
-      }
     });
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) above += __shfl_xor_sync(0xffffffffu, above, off);
-    __syncwarp();
-    // fn(key, in) for the candidates, from the list, or from the run where it was
-    // too short.
+    complete = __all_sync(0xffffffffu, complete);
+    const int most_listed = __reduce_max_sync(0xffffffffu, listed);
+    // fn(key, in) for the candidates, from the lists, or from the run where one of them
+    // was too short.
     auto each_candidate = [&](auto fn) {
-      if (listed <= room) {
-        for (uint32_t i = 0; i < listed; i += 32) {
-          const bool in = i + lane < listed;
-          fn(in ? my_list[i + lane] : 0u, in);
+      if (complete) {
+        for (int i = 0; i < most_listed; ++i) {
+          const bool in = i < listed;
+          fn(in ? my_list[32 * i + lane] : 0u, in);
         }
       } else {
         each([&](int, const uint32_t (&key)[kBatch][4], int blocks) {
@@ -388,9 +388,11 @@ __global__ void __launch_bounds__(kEvictThreads, 1) mla_evict_select_kernel(cons
       prefix |= find(d, bins) << shift;
     }
     each_candidate([&](uint32_t key, bool in) {
-      above += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
-      equal += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
+      if (in && key > prefix) ++above;
+      if (in && key == prefix) ++equal;
     });
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
   } else {
     above = static_cast<uint32_t>(k1 - k0);
   }
