@@ -23,8 +23,8 @@
 //
 // Bound by the bytes of the cache.  Measured (calls in a CUDA graph): 16 x 128K keys (a
 // little fewer for 15 of them), 12 heads, E4M3, 143 us for 938 MB (6.5 TB/s, 97 % of
-// the copy bandwidth); 4 requests of up to 32,777 keys, 8 x 12 rows, BF16, 28.5 us for
-// 124 MB (start of the CTAs, then 5 or 6 tiles each); 2 x 1,000 keys, 4 bits, 8.1 us.
+// the copy bandwidth); 4 requests of up to 32,777 keys, 8 x 12 rows, BF16, 28.2 us for
+// 124 MB (start of the CTAs, then 5 or 6 tiles each); 2 x 1,000 keys, 4 bits, 8.4 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
   float* lse_s = reinterpret_cast<float*>(aux + kKwLse);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  wait_for_earlier_kernels();
   // This CTA's run of tiles: each thread counts a contiguous part of the batch.
   KwWalk walk{};
   {
@@ -651,6 +652,7 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, tmem_cols);
   }
+  let_next_kernel_start();
 }
 
 // A 2-D view [rows, 576] of 1- or 2-byte elements with a (box_x, box_y) box.
@@ -711,8 +713,21 @@ static cudaError_t launch_key_weights(const KeyWeightsParams& p, uint32_t smem, 
     }
   }
   if (!ok) return cudaErrorInvalidValue;
-  mla_key_weights_kernel<KIND><<<sms, C::kThreads, smem, st>>>(lat, rope, q_lat, q_rope, p);
-  return cudaGetLastError();
+  // From 64K keys on a programmatic dependent: its CTAs start while the kernel before it
+  // ends (the window of 4 x 32,777 keys 30.7 -> 28.1 us, calls in a row on a stream).
+  // Such a launch costs the host 1 to 1.5 us more, which shorter calls wait for (2 x
+  // 1,000 keys 9.5 -> 10.9 us).
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.a.batch * p.a.weights_stride >= 65536 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, mla_key_weights_kernel<KIND>, lat, rope, q_lat, q_rope, p);
 }
 
 }  // namespace mla

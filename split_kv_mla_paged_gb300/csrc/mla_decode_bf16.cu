@@ -347,9 +347,10 @@ __global__ void __launch_bounds__(CfgQ<NR>::kThreads, 1)
   SplitRange sr;
   int b = 0;
   if constexpr (kShared) {
-    if (p.chain & SHARED_RELEASE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.chain == 0) wait_for_earlier_kernels();  // (as in the E4M3 kernel)
+    if (p.chain & SHARED_RELEASE) let_next_kernel_start();
     if (!segment_range(p, NR, sr)) {
-      if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (p.chain & SHARED_JOIN) wait_for_earlier_kernels();
       return;
     }
   } else {
@@ -1700,7 +1701,7 @@ static cudaError_t launch_shared_bf16_t(const void* q, const void* kv, int64_t r
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = (prm.chain & SHARED_JOIN) ? 1 : 0;
+  cfg.numAttrs = (prm.chain & SHARED_RELEASE) ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, tm_kv, tm_q, prm);
 }
 

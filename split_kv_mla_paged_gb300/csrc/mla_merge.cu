@@ -32,6 +32,8 @@ __device__ __forceinline__ void merge_body(const MergeParams& p) {
   __shared__ float4 sm_o[G][32];
   // Partials are written by the preceding (programmatically dependent) grid.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (The next kernel of this library may start; it waits for this one's end.)
+  if constexpr (kShared) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int row = blockIdx.x;
   const int quarter = blockIdx.y;
   const int g = threadIdx.x >> 5;

@@ -442,8 +442,11 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
   const int ngroups = (p.rows_per_req + p.rows_per_group - 1) / p.rows_per_group;
   ItemInfo first{};
   if constexpr (kShared) {
-    // The next launch's CTAs may take the SMs that this one leaves free.
-    if (p.chain & SHARED_RELEASE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // A single launch starts while the kernel before it on the stream ends.  Of two, the
+    // first starts after it, and the second one's CTAs, which read without a wait what
+    // was written before the first, may take the SMs that the first leaves free.
+    if (p.chain == 0) wait_for_earlier_kernels();
+    if (p.chain & SHARED_RELEASE) let_next_kernel_start();
     const int entry = p.cta_items[blockIdx.x];
     const int seg = entry >> MLA_ITEM_B_SHIFT;
     bool fits = entry >= 0 && seg < p.num_segs;
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           NR, first);
     }
     if (!fits) {
-      if (p.chain & SHARED_JOIN) asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (p.chain & SHARED_JOIN) wait_for_earlier_kernels();
       return;
     }
   } else if constexpr (!kPersist) {
@@ -2223,7 +2226,7 @@ static cudaError_t launch_split_t(const void* q, const void* kv, int64_t num_pag
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = (prm.chain & SHARED_JOIN) ? 1 : 0;
+    cfg.numAttrs = (prm.chain & SHARED_RELEASE) ? 0 : 1;
     return cudaLaunchKernelEx(&cfg, mla_split_kv_kernel<NR, kGather, kMode, kFp4>, kv_lat, kv_rope,
                               q_lat, q_rope, prm);
   }

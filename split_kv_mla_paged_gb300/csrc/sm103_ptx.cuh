@@ -197,6 +197,16 @@ __device__ __forceinline__ void set_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTo));
 }
 
+// ---------------------------------------------------------------- programmatic launches
+// Waits for the kernels before this one on the stream, whose results it may then read.
+__device__ __forceinline__ void wait_for_earlier_kernels() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// The next kernel may start once every CTA of this one is here or has ended.
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05 / TMEM
 // Allocation: one full warp executes these.  The allocated base address is
 // written to shared memory at `dst`.

@@ -19,7 +19,7 @@
 // to all CTAs of the cluster; the one warp that the threshold falls into reads
 // its tokens again (from L2) and finds the token.
 //
-// Measured (calls in a CUDA graph): 64 requests x 131,072 tokens, 67 MB, 23.7 us (of
+// Measured (calls in a CUDA graph): 64 requests x 131,072 tokens, 67 MB, 23.2 us (of
 // which 1.5 us find the accepted drafts, 12-14 us read and sum the rows at 5 TB/s, 1.7
 // us exchange the sums, 0.5 to 5 us find the token); one request x 32,000 tokens 5.5 us.
 #include <cooperative_groups.h>
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
   const int ranks = static_cast<int>(cluster.num_blocks());
   const int b = blockIdx.x / ranks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int q_b = a.query_lens ? a.query_lens[b] : a.q_len;
   if (q_b < 1 || q_b > a.q_len) {  // the same for the whole cluster
     if (a.status && rank == 0 && threadIdx.x == 0) atomicCAS(a.status, 0, MLA_ERR_INVALID_ARG);
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
     const uint64_t mine = k0 < k1 ? warp_weight_sum<T, kVec>(s, k0, k1, lane) : 0;
     if (lane < ranks) cluster.map_shared_rank(sums, lane)[part] = mine;
     cluster.sync();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Every warp sums the parts before its own and all of them.
     total = before = 0;
     for (int i = lane; i < parts; i += 32) {
@@ -299,13 +301,19 @@ static cudaError_t launch_verify(const mla_verify_args_t& a, bool vector, cudaSt
   cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * static_cast<unsigned>(ranks));
   cfg.blockDim = dim3(kVerifyThreads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  // From 4M tokens on a programmatic dependent, which starts while the kernel before it
+  // ends (64 x 131,072 tokens 25.1 -> 23.7 us, calls in a row on a stream); such a launch
+  // costs the host 1 to 2 us more, which shorter calls wait for (32,000 tokens 9.5 ->
+  // 11.7 us).
+  cfg.numAttrs = static_cast<int64_t>(a.batch) * a.vocab >= (1 << 22) ? 2 : 1;
   return cudaLaunchKernelEx(&cfg,
                             vector ? mla_verify_kernel<T, 16 / sizeof(T)> : mla_verify_kernel<T, 1>, a);
 }

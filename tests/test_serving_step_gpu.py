@@ -131,7 +131,7 @@ def test_step(kind):
 
 def _step(kind, seed, batch=6, prefix=4096, own=700, sms=16):
     """A step's calls on tensors of their own, as one function without allocations,
-    and those whose contents are its results."""
+    and those tensors by name."""
     g = torch.Generator().manual_seed(seed)
     bf16, rows = kind == mla.CACHE_BF16, batch * Q * HEADS
     each, shared = (own + 31) // 32, prefix // 32
@@ -175,7 +175,11 @@ def _step(kind, seed, batch=6, prefix=4096, own=700, sms=16):
         mla.mla_evict_select(weights, left, keep, kept, counts, first=4, last=8, new_weights=kept_w, status=status)
         mla.mla_rows_move(pool, pages, table, moved, moved.shape[0], to, kept, counts, cache_kind=kind, status=status)
 
-    return run, (out, lse, weights, tokens, accepted, left, kept, kept_w, counts, moved, ws[:4], status)
+    return run, dict(q=q, pool=pool, out=out, lse=lse, weights=weights, tokens=tokens, accepted=accepted, left=left, kept=kept, kept_w=kept_w,
+                     counts=counts, moved=moved, decode_status=ws[:4], status=status)
+
+
+RESULTS = ("out", "lse", "weights", "tokens", "accepted", "left", "kept", "kept_w", "counts", "moved")
 
 
 @pytest.mark.parametrize("kind", [mla.CACHE_FP8, mla.CACHE_BF16, mla.CACHE_FP4])
@@ -184,15 +188,15 @@ def test_two_captured_steps_at_once(kind):
     # the steps called one after the other.
     times, want, graphs = 8, [], []
     for seed in (1, 2):
-        run, results = _step(kind, seed)
+        run, t = _step(kind, seed)
         for _ in range(times + 1):
             run()
         torch.cuda.synchronize()
-        assert int(results[-1]) == 0 and not results[-2].any()
-        want.append([r.clone() for r in results])
+        assert int(t["status"]) == 0 and not t["decode_status"].any()
+        want.append([t[n] for n in RESULTS])
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     for seed, stream in zip((1, 2), streams):
-        run, results = _step(kind, seed)
+        run, t = _step(kind, seed)
         torch.cuda.synchronize()
         with torch.cuda.stream(stream):
             run()
@@ -200,12 +204,63 @@ def test_two_captured_steps_at_once(kind):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=stream):
             run()
-        graphs.append((graph, results))
+        graphs.append((graph, t))
     for _ in range(times):
         for (graph, _), stream in zip(graphs, streams):
             with torch.cuda.stream(stream):
                 graph.replay()
     torch.cuda.synchronize()
-    for (_, results), ref in zip(graphs, want):
-        for a, b in zip(results, ref):
+    for (_, t), ref in zip(graphs, want):
+        assert int(t["status"]) == 0 and not t["decode_status"].any()
+        for a, b in zip((t[n] for n in RESULTS), ref):
             assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def _alternate(run, current, variants, results, times=30):
+    """Every call right behind the copies that write its inputs, on one stream: the
+    results of each variant's first call, made after a wait."""
+    want = []
+    for v in variants:
+        for c, x in zip(current, v):
+            c.copy_(x)
+        torch.cuda.synchronize()
+        run()
+        torch.cuda.synchronize()
+        want.append([r.clone() for r in results])
+    assert not all(torch.equal(a, b) for a, b in zip(*want))
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(times):
+        for v, w in zip(variants, want):
+            for c, x in zip(current, v):
+                c.copy_(x)
+            run()
+            for r, x in zip(results, w):
+                wrong += (r.contiguous().view(torch.uint8) != x.contiguous().view(torch.uint8)).sum()
+    assert int(wrong) == 0
+
+
+@pytest.mark.parametrize("kind", [mla.CACHE_FP8, mla.CACHE_BF16, mla.CACHE_FP4])
+def test_inputs_written_just_before_decode_and_weights(kind):
+    run, t = _step(kind, 5, batch=4, prefix=16384, own=900)
+    current = [t[n] for n in ("q", "pool", "weights")]
+    _alternate(run, current, [[c.clone() for c in current], [c.flip(0) for c in current]], [t[n] for n in RESULTS])
+
+
+def test_inputs_written_just_before_selection_and_verification():
+    # Sizes whose launches are programmatic dependents of the copies before them.
+    n, keep = 600_000, 5000
+    w, lens = torch.rand(1, n, device="cuda"), torch.tensor([n], dtype=torch.int32, device="cuda")
+    kept, counts = torch.empty(1, keep, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    budget, kept_w = torch.tensor([keep], dtype=torch.int32, device="cuda"), torch.empty(1, keep, device="cuda")
+    _alternate(lambda: mla.mla_evict_select(w, lens, budget, kept, counts, new_weights=kept_w), [w, lens],
+               [[torch.rand(1, n, device="cuda"), lens.clone()], [torch.rand(1, n, device="cuda"), lens - 100_000]], [kept, kept_w, counts])
+    batch, vocab = 72, 65536
+    p, u = torch.empty(batch, 2, vocab, device="cuda"), torch.empty(batch, 2, device="cuda")
+    x = torch.empty(batch, 1, dtype=torch.int32, device="cuda")
+    tokens, accepted = torch.empty(batch, 2, dtype=torch.int32, device="cuda"), torch.empty(batch, dtype=torch.int32, device="cuda")
+
+    def inputs():
+        t = torch.softmax(2 * torch.randn_like(p), -1)
+        return [t, torch.rand_like(u), t[:, :1].argmax(-1).int()]
+
+    _alternate(lambda: mla.mla_verify_drafts(p, x, u, tokens, accepted), [p, u, x], [inputs(), inputs()], [tokens, accepted])
