@@ -15,7 +15,9 @@
 // of shared memory to loads in flight next to the resident Q.
 //
 // Persistent CTAs, one per SM, take equal contiguous runs of the batch's 128-key
-// tiles, counted on the device from kv_lens, so no plan is needed.  Up to 128 rows
+// tiles, counted on the device from kv_lens, so no plan is needed.  (Runs of pages, so
+// that no CTA has a tile more than another, took 31.9 us for the window below: a tile of
+// one page keeps a quarter of the bytes in flight.)  Up to 128 rows
 // Q stays in shared memory; beyond that a run is worked off in chunks
 // of 8 tiles, one row group after the other, whose repeated reads L2 serves.  Every
 // weight is the sum of one thread, in the order of the rows: results do not depend on
