@@ -16,8 +16,8 @@
 //
 // Persistent CTAs, one per SM, take equal contiguous runs of the batch's 128-key
 // tiles, counted on the device from kv_lens, so no plan is needed.  (Runs of pages, so
-// that no CTA has a tile more than another, took 31.9 us for the window below: a tile of
-// one page keeps a quarter of the bytes in flight.)  Up to 128 rows
+// that no CTA has a tile more than another, took the window below from 28.2 to 31.9 us:
+// a tile of one page keeps a quarter of the bytes in flight.)  Up to 128 rows
 // Q stays in shared memory; beyond that a run is worked off in chunks
 // of 8 tiles, one row group after the other, whose repeated reads L2 serves.  Every
 // weight is the sum of one thread, in the order of the rows: results do not depend on
@@ -25,8 +25,8 @@
 //
 // Bound by the bytes of the cache.  Measured (calls in a CUDA graph): 16 x 128K keys (a
 // little fewer for 15 of them), 12 heads, E4M3, 143 us for 938 MB (6.5 TB/s, 97 % of
-// the copy bandwidth); 4 requests of up to 32,777 keys, 8 x 12 rows, BF16, 28.2 us for
-// 124 MB (start of the CTAs, then 5 or 6 tiles each); 2 x 1,000 keys, 4 bits, 8.4 us.
+// the copy bandwidth); 4 requests of up to 32,777 keys, 8 x 12 rows, BF16, 33.7 us for
+// 124 MB (start of the CTAs, then 5 or 6 tiles each, MMAs and epilogue in turn); 2 x 1,000 keys, 4 bits, 8.4 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -60,8 +60,15 @@ struct KeyWeightsParams {
   int32_t stages, q_buffers;
   // Accumulators of a score, each over its share of the blocks, added in fp32 by
   // the epilogue: the tensor core drops bits at every instruction that adds to an
-  // accumulator, the more the larger it is.  As many as TMEM holds twice.
-  int32_t sums;  // 2, 4 or (BF16, whose scores take twice the instructions) 8
+  // accumulator, the more the larger it is.  As many as TMEM holds twice, one S^T buffer
+  // for each epilogue warpgroup; BF16, whose scores take twice the instructions, at
+  // least 4, for more than 64 rows in one buffer.  (With 2 in two buffers the weights of
+  // 96 rows were up to twice as far off as those of a product in fp32, and the window
+  // above took 28.2 us where it takes 33.7.  Accumulators in turn, a fifth one free when a
+  // tile begins, took 32.4; all scores in registers before the first weight 32.6: the
+  // ring holds less than a tile next to Q, so that loads wait with the MMAs.)
+  int32_t sums;       // 2, 4 or (BF16) 8
+  int32_t s_buffers;  // 2 or 1
   uint32_t q_bytes;  // of one buffer
   long long wait_cycles;
   int32_t debug_expire;
@@ -233,7 +240,9 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
     walk.left = hi - lo;
   }
   const uint32_t s_cols = p.sums * p.nr;  // of one S^T buffer
-  const uint32_t tmem_cols = 2 * s_cols <= 128 ? 128 : 2 * s_cols <= 256 ? 256 : 512;
+  const uint32_t s_next = p.s_buffers == 2 ? s_cols : 0;  // from the first to the second
+  const uint32_t s_all = p.s_buffers * s_cols;
+  const uint32_t tmem_cols = s_all <= 128 ? 128 : s_all <= 256 ? 256 : 512;
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), tmem_cols);
     tmem_relinquish();
@@ -378,7 +387,8 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
     int st = 0, round = 0, nq = 0;
     bool ok = true, live = true, new_q = true;
     uint32_t qb = 0;
-    int used0 = 0, used1 = 0;  // uses of the S^T buffers
+    int used0 = 0, used1 = 0;  // steps of the epilogue warpgroups
+    int before = 0;            // the warpgroup of the step before
     for (int step = 0; live; ++step) {
       ok = !expired(WAIT_TILE_FULL, step);
       if (new_q) {
@@ -392,10 +402,13 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
         qb = sbase + q_at + buf * p.q_bytes;
         ++nq;
       }
-      const int sb = kw_buffer(p, walk, step), use_s = sb ? used1 : used0;
-      (sb ? used1 : used0) += 1;
+      const int sb = kw_buffer(p, walk, step);
+      const int last = p.s_buffers == 2 ? sb : before;  // who read the buffer last
+      const int use_s = last ? used1 : used0;
       if (ok && use_s > 0)
-        ok = mbar_wait_abort(misc(S_FREE + sb), (use_s - 1) & 1, p.wait_cycles, abort_flag);
+        ok = mbar_wait_abort(misc(S_FREE + last), (use_s - 1) & 1, p.wait_cycles, abort_flag);
+      (sb ? used1 : used0) += 1;
+      before = sb;
       for (int d = 0; d < C::kBlocks; ++d) {
         if (ok) ok = mbar_wait_abort(full(st), round & 1, p.wait_cycles, abort_flag);
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
@@ -407,7 +420,7 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
           const int n_sub = rope ? 2 : 4;
           const int acc = d * p.sums / C::kBlocks;
           const bool first = d == 0 || (d - 1) * p.sums / C::kBlocks != acc;
-          const uint32_t to = tmem + sb * s_cols + acc * p.nr;
+          const uint32_t to = tmem + sb * s_next + acc * p.nr;
 #pragma unroll
           for (int sub = 0; sub < 4; ++sub) {
             if (sub < n_sub) {
@@ -504,7 +517,7 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
         const bool whole = !a.causal || (walk.t + 1) * kKwTile <= walk.len - walk.q_b + 1 +
                                                                      row0 / a.num_heads;
         float sum0 = 0.0f, sum1 = 0.0f;
-        const uint32_t at = tmem + lane_addr + e * s_cols;
+        const uint32_t at = tmem + lane_addr + e * s_next;
 #pragma unroll 1
         for (int r0 = 0; r0 < rows; r0 += 16) {
           uint32_t v0[16], v1[16];
@@ -716,7 +729,7 @@ static cudaError_t launch_key_weights(const KeyWeightsParams& p, uint32_t smem, 
   }
   if (!ok) return cudaErrorInvalidValue;
   // From 64K keys on a programmatic dependent: its CTAs start while the kernel before it
-  // ends (the window of 4 x 32,777 keys 30.7 -> 28.1 us, calls in a row on a stream).
+  // ends (the window of 4 x 32,777 keys 2.5 us less, calls in a row on a stream).
   // Such a launch costs the host 1 to 1.5 us more, which shorter calls wait for (2 x
   // 1,000 keys 9.5 -> 10.9 us).
   cudaLaunchConfig_t cfg = {};
@@ -790,7 +803,8 @@ extern "C" int mla_key_weights(const mla_key_weights_args_t* args, void* stream)
   p.groups = (p.rows_per_req + kKwMaxRows - 1) / kKwMaxRows;
   p.group_rows = (p.rows_per_req + p.groups - 1) / p.groups;
   p.nr = (p.group_rows + 15) / 16 * 16;
-  p.sums = bf16 && p.nr <= 32 ? 8 : p.nr <= 64 ? 4 : 2;
+  p.sums = bf16 && p.nr <= 32 ? 8 : bf16 || p.nr <= 64 ? 4 : 2;
+  p.s_buffers = p.sums * p.nr <= 256 ? 2 : 1;
   p.q_bytes = static_cast<uint32_t>(p.nr) * (bf16 ? 1152 : 576);
   p.q_bytes = (p.q_bytes + 1023) / 1024 * 1024;
   // Two Q buffers where six stages still fit beside them.

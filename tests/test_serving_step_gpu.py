@@ -264,3 +264,52 @@ def test_inputs_written_just_before_selection_and_verification():
         return [t, torch.rand_like(u), t[:, :1].argmax(-1).int()]
 
     _alternate(lambda: mla.mla_verify_drafts(p, x, u, tokens, accepted), [p, u, x], [inputs(), inputs()], [tokens, accepted])
+
+
+def _ops():
+    """The calls that can start while the kernel before them ends, each with an input
+    that decides its result and its results, at sizes where it does."""
+    run, t = _step(mla.CACHE_FP8, 9, batch=4, prefix=16384, own=900)  # (its own eviction is small)
+    yield run, t["q"], [t[n] for n in RESULTS]
+    n, keep = 600_000, 5000
+    w, lens = torch.rand(1, n, device="cuda"), torch.tensor([n], dtype=torch.int32, device="cuda")
+    kept, counts = torch.empty(1, keep, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    budget = torch.tensor([keep], dtype=torch.int32, device="cuda")
+    yield (lambda: mla.mla_evict_select(w, lens, budget, kept, counts)), w, [kept, counts]
+    p, u = torch.softmax(2 * torch.randn(72, 2, 65536, device="cuda"), -1), torch.rand(72, 2, device="cuda")
+    x, tokens = p[:, :1].argmax(-1).int(), torch.empty(72, 2, dtype=torch.int32, device="cuda")
+    accepted = torch.empty(72, dtype=torch.int32, device="cuda")
+    yield (lambda: mla.mla_verify_drafts(p, x, u, tokens, accepted)), u, [tokens, accepted]
+
+
+@pytest.mark.parametrize("before", ["nothing", "copy", "zero", "kernel", "join"])
+def test_captured_behind_other_work(before):
+    for run, inp, results in _ops():
+        good, blank = inp.clone(), [r.clone() for r in results]
+        run()
+        torch.cuda.synchronize()
+        want = [r.clone() for r in results]
+        side, other = torch.cuda.Stream(), torch.empty_like(inp)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            if before in ("copy", "join"):
+                inp.copy_(good)
+            elif before == "zero":
+                other.view(torch.uint8).zero_()
+            elif before == "kernel":
+                torch.bitwise_or(good.view(torch.uint8), 0, out=inp.view(torch.uint8))
+            if before == "join":  # behind the nodes of two streams
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    other.copy_(good)
+                torch.cuda.current_stream().wait_stream(side)
+            run()
+        for _ in range(3):
+            if before in ("copy", "join", "kernel"):
+                inp.view(torch.uint8).zero_()
+            for r, x in zip(results, blank):
+                r.copy_(x)
+            graph.replay()
+            torch.cuda.synchronize()
+            for r, x in zip(results, want):
+                assert torch.equal(r.view(torch.uint8), x.view(torch.uint8))
