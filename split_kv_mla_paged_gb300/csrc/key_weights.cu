@@ -26,7 +26,8 @@
 // Bound by the bytes of the cache.  Measured (calls in a CUDA graph): 16 x 128K keys (a
 // little fewer for 15 of them), 12 heads, E4M3, 143 us for 938 MB (6.5 TB/s, 97 % of
 // the copy bandwidth); 4 requests of up to 32,777 keys, 8 x 12 rows, BF16, 33.7 us for
-// 124 MB (start of the CTAs, then 5 or 6 tiles each, MMAs and epilogue in turn); 2 x 1,000 keys, 4 bits, 8.4 us.
+// 124 MB (start of the CTAs, then 5 or 6 tiles each, MMAs and epilogue in turn); 2 x
+// 1,000 keys, 4 bits, 8.4 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
