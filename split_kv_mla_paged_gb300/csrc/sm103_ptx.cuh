@@ -207,6 +207,17 @@ __device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- clusters
+// A barrier of the cluster in two halves, every thread of every CTA in each.  Shared
+// memory of another CTA may be accessed only once that CTA has started: behind the
+// first such barrier.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05 / TMEM
 // Allocation: one full warp executes these.  The allocated base address is
 // written to shared memory at `dst`.

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
     if (a.status && rank == 0 && threadIdx.x == 0) atomicCAS(a.status, 0, MLA_ERR_INVALID_ARG);
     return;
   }
+  cluster_arrive();  // this CTA has started (waited for ahead of the first remote store)
   const int n = q_b - 1;  // drafts
   const T* target = reinterpret_cast<const T*>(a.target_probs) + b * a.target_batch_stride;
   const T* draft =
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
   uint64_t total = 0, before = 0;
   for (int round = 0; round < 2; ++round) {
     const uint64_t mine = k0 < k1 ? warp_weight_sum<T, kVec>(s, k0, k1, lane) : 0;
+    if (round == 0) cluster_wait();  // every CTA of the cluster has started
     if (lane < ranks) cluster.map_shared_rank(sums, lane)[part] = mine;
     cluster.sync();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
