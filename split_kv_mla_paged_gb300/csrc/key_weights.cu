@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
       c = static_cast<float>(x);
       c_low = static_cast<float>(x - c);
     }
-    bool ok = true, live = true, new_q = true, stale = true;
+    bool ok = true, failed = false, live = true, new_q = true, stale = true;
     int rows = 0;  // of the group that are real query rows
     int used = 0;  // uses of this warpgroup's buffer
     for (int step = 0; live; ++step) {
@@ -509,8 +509,13 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
         ++used;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
-          fail();
-          break;
+          // On to the end without work: the group's other warps, which may have seen the
+          // barrier complete before the abort flag, meet this one at the named barriers
+          // of the steps to come.
+          if (!failed) fail();
+          failed = true;
+          live = kw_next(p, walk, new_q);
+          continue;
         }
         tc_fence_after();
         // Keys that every row sees need no mask; under causal row r of query token
