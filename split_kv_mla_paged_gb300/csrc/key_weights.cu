@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(aux + 280);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + 284);
   int64_t* scan = reinterpret_cast<int64_t*>(aux + 288);           // up to 20 warps' sums
-  volatile int* start = reinterpret_cast<volatile int*>(aux + 456);  // request, tile, tiles
+  volatile int* start = reinterpret_cast<volatile int*>(aux + 456);  // request, tile
+  volatile int* taken = reinterpret_cast<volatile int*>(aux + 464);  // blocks that the MMA warp took
   float* lse_s = reinterpret_cast<float*>(aux + kKwLse);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
   };
   auto expired = [&](int role, int i) { return p.debug_expire == ((role << 24) | i); };
 
+  int64_t copied = 0;  // blocks that this warp copied
   if (warp == 0) {
     // ================= TMA producer =================
     if (lane == 0) {
@@ -370,13 +372,9 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
       live = kw_next(p, walk, new_q);
     }
     if (!ok) fail();
-    // Copies in flight land before the CTA can exit.  (A stage's full barrier is at
-    // most one phase behind this warp.)
+    copied = issued;
+    // Q in flight lands before the CTA can exit.
     if (lane == 0) {
-      constexpr int kStride = C::kFp4 ? 5 : 1;  // blocks between two copies
-      const int64_t last = C::kFp4 ? issued * 5 : issued;
-      for (int64_t k = last - kStride + (C::kFp4 ? 4 : 0); k >= 0 && k >= last - p.stages; k -= kStride)
-        mbar_wait(full(static_cast<int>(k % p.stages)), (k / p.stages) & 1, kWaitLimitCycles);
       for (int n = max(0, nq - p.q_buffers); n < nq; ++n)
         mbar_wait(misc(Q_FULL + (p.q_buffers == 2 ? (n & 1) : 0)),
                   (p.q_buffers == 2 ? (n >> 1) : n) & 1, kWaitLimitCycles);
@@ -448,6 +446,7 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
       live = kw_next(p, walk, new_q);
     }
     if (!ok) fail();
+    if (lane == 0) *taken = round * p.stages + st;
     // This warp's MMAs complete before the CTA releases TMEM.
     if (elect_one()) umma_commit(misc(FINAL));
     __syncwarp();
@@ -672,6 +671,18 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, tmem_cols);
+  }
+  // Copies in flight land before the CTA can exit: those of the blocks that the MMA warp
+  // has not seen land, after an expired wait.  Their stages have not been filled again, so
+  // the barriers are in these blocks' phases.  (Of the others a 4-bit tile's expanders may
+  // be phases ahead, and a wait for them would run to its limit.)
+  if (warp == 0 && lane == 0) {
+    constexpr int kStride = C::kFp4 ? 5 : 1;  // blocks between two copies
+    for (int64_t i = copied - 1; i >= 0; --i) {
+      const int64_t k = i * kStride + (C::kFp4 ? 4 : 0);
+      if (k < *taken) break;
+      mbar_wait(full(static_cast<int>(k % p.stages)), (k / p.stages) & 1, kWaitLimitCycles);
+    }
   }
   let_next_kernel_start();
 }

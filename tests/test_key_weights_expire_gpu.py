@@ -1,6 +1,7 @@
 """GPU: expired waits of key weights where the epilogue warps still have steps with
 new query rows before them, at whose named barriers they have to meet."""
 import functools
+import time
 
 import pytest
 import torch
@@ -31,15 +32,16 @@ def _inputs(kind, case):
     return inp.q.cuda(), pool.cuda(), inp.page_table.cuda(), torch.zeros(len(lens), q_len, heads, device="cuda")
 
 
-@pytest.mark.parametrize("kind", ["fp8", "bf16", "fp4"])
-@pytest.mark.parametrize("case", sorted(CASES))
 @pytest.mark.parametrize("role,step", [(0, 0), (0, 2), (1, 0), (1, 1), (1, 3), (3, 0), (3, 1), (3, 2)])
+@pytest.mark.parametrize("case", sorted(CASES))
+@pytest.mark.parametrize("kind", ["fp8", "bf16", "fp4"])
 def test_the_call_ends_and_the_next_one_is_right(kind, case, role, step):
     heads, q_len, lens = CASES[case]
     qd, kvd, pt, lse = _inputs(kind, case)
     kw = dict(num_heads=heads, q_len=q_len, causal=q_len > 1, softmax_scale=SOFTMAX_SCALE)
     ref = mla.key_weights(qd, kvd, pt, lens, lse, **kw)
     for _ in range(10):
+        began = time.monotonic()
         mla.mla_debug_set_expire(role, step)
         try:
             with pytest.raises(mla.MlaError) as err:
@@ -47,4 +49,5 @@ def test_the_call_ends_and_the_next_one_is_right(kind, case, role, step):
             assert err.value.status == mla.MLA_ERR_TIMEOUT
         finally:
             mla.mla_debug_set_expire(-1)
+        assert time.monotonic() - began < 1.0  # no wait ran to its limit of some two seconds
     assert torch.equal(mla.key_weights(qd, kvd, pt, lens, lse, **kw), ref)
