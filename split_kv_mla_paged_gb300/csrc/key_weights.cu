@@ -611,10 +611,10 @@ __global__ void __launch_bounds__(KwCfg<KIND>::kThreads, 1)
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int d = d0 + 2 * m;
-        sc[m] = ldg_stream8(at + kFp4ScaleOffset + (d * 4 + (lane & 3)) * MLA_PAGE_SIZE + tok8);
+        sc[m] = ldg_stream8_coherent(at + kFp4ScaleOffset + (d * 4 + (lane & 3)) * MLA_PAGE_SIZE + tok8);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          v[m][k] = ldg_stream(at + (tok8 + par + 2 * k) * kFp4RowCodes + d * 64 + (lane & 3) * 16);
+          v[m][k] = ldg_stream_coherent(at + (tok8 + par + 2 * k) * kFp4RowCodes + d * 64 + (lane & 3) * 16);
       }
     };
     load(pg);

@@ -374,6 +374,23 @@ __device__ __forceinline__ bool item_info(const DecodeParams& p, int b, int spli
   return true;
 }
 
+// Codes and scales of a 4-bit page.  kShared: a decode over shared prefixes may be a
+// programmatic dependent of the kernel that wrote the pages.
+template <bool kShared>
+__device__ __forceinline__ uint4 fp4_load16(const uint8_t* p) {
+  if constexpr (kShared)
+    return ldg_stream_coherent(p);
+  else
+    return ldg_stream(p);
+}
+template <bool kShared>
+__device__ __forceinline__ uint2 fp4_load8(const uint8_t* p) {
+  if constexpr (kShared)
+    return ldg_stream8_coherent(p);
+  else
+    return ldg_stream8(p);
+}
+
 // 4-bit cache: pool page of the item's compact page pi (counted like positions,
 // or like the selection's entries); -1 where it is not loaded.  Bad ids are
 // reported by the producer, which reads page 0 in their place, as here.  key0
@@ -1179,9 +1196,9 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           src = page + (tok8 + par) * kFp4RowCodes + d * 64 + (lane & 3) * 16;
           return page + kFp4ScaleOffset + (d * 4 + (lane & 3)) * MLA_PAGE_SIZE + tok8;
         };
-        sc = ldg_stream8(locate(0));
+        sc = fp4_load8<kShared>(locate(0));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = ldg_stream(src + k * (2 * kFp4RowCodes));
+        for (int k = 0; k < 4; ++k) v[k] = fp4_load16<kShared>(src + k * (2 * kFp4RowCodes));
         const uint32_t c0 = (((lane & 3) * 2) ^ par) * 16;  // swizzled chunk of token par
 #pragma unroll 1
         for (int ch = ew, n = 0; ch < n_chunks; ch += W, ++n) {
@@ -1190,7 +1207,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           const uint32_t scw[2] = {(sc.x >> (8 * par)) & 0x000F000Fu,
                                    (sc.y >> (8 * par)) & 0x000F000Fu};
           hidden = hidden_next;
-          sc = ldg_stream8(locate(n + 1));
+          sc = fp4_load8<kShared>(locate(n + 1));
           if (round > 0) {
             bool w = mbar_wait_abort<kFp4>(empty_blk(st, d), (round - 1) & 1, p.wait_cycles,
                                            abort_flag);
@@ -1217,7 +1234,7 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           auto step = [&](int k, uint2 t) {
             const uint2 a = fp4_expand8(v[k].x, t), bb = fp4_expand8(v[k].y, t);
             const uint2 cc = fp4_expand8(v[k].z, t), dd = fp4_expand8(v[k].w, t);
-            v[k] = ldg_stream(src + k * (2 * kFp4RowCodes));
+            v[k] = fp4_load16<kShared>(src + k * (2 * kFp4RowCodes));
             uint8_t* dst = row + k * 256;
             const uint32_t c = c0 ^ (2 * k * 16);
             *reinterpret_cast<uint4*>(dst + c) = make_uint4(a.x, a.y, bb.x, bb.y);
@@ -1299,9 +1316,9 @@ __global__ void __launch_bounds__(Cfg<NR, kFp4>::kThreads, 1)
           src = p.kv_fp4 + static_cast<int64_t>(max(pg, 0)) * MLA_FP4_PAGE_BYTES;
         };
         auto codes_of = [&](int k) {
-          return ldg_stream(src + (half + 2 * k + par) * kFp4RowCodes + blk * 16);
+          return fp4_load16<kShared>(src + (half + 2 * k + par) * kFp4RowCodes + blk * 16);
         };
-        auto scales = [&]() { return ldg_stream(src + kFp4ScaleOffset + blk * MLA_PAGE_SIZE + half); };
+        auto scales = [&]() { return fp4_load16<kShared>(src + kFp4ScaleOffset + blk * MLA_PAGE_SIZE + half); };
         locate(0);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = codes_of(k);
