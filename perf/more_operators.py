@@ -249,16 +249,20 @@ def prepare(case, seed):
     if op == "verify":
         b, n, v = case["batch"], case["q"], case["vocab"]
         dt = torch.float32 if case["dtype"] == "fp32" else torch.bfloat16
-        target, draft = torch.empty(b, n, v, device="cuda", dtype=dt), torch.empty(b, max(n - 1, 1), v, device="cuda", dtype=dt)
+        target, draft = torch.empty(b, n, v, device="cuda", dtype=dt), torch.empty(b, n - 1, v, device="cuda", dtype=dt)
         for i in range(b):  # a model's next-token logits, and those of a smaller model that mostly agrees
             z = 3.0 * torch.randn(n, v, device="cuda", generator=gen)
             target[i] = torch.softmax(z, -1)
-            draft[i, :n - 1] = torch.softmax(z[:n - 1] + 0.4 * torch.randn(n - 1, v, device="cuda", generator=gen), -1)
-        if case["drafts"] == "sampled":
+            draft[i] = torch.softmax(z[:n - 1] + 0.4 * torch.randn(n - 1, v, device="cuda", generator=gen), -1)
+        if n == 1:  # single tokens: nothing was drafted
+            tokens = torch.zeros(b, 0, device="cuda")
+        elif case["drafts"] == "sampled":
             tokens = torch.stack([torch.multinomial(draft[i].float(), 1, generator=gen)[:, 0] for i in range(b)])
         else:  # drafts that were looked up: no probabilities of their own
-            tokens, draft = target[:, :max(n - 1, 1)].float().argmax(-1), None
-        s.update(target=target, draft=draft, tokens=tokens[:, :n - 1].int().contiguous(), u=torch.rand(b, n, device="cuda", generator=gen),
+            tokens = target[:, :n - 1].float().argmax(-1)
+        if case["drafts"] != "sampled":
+            draft = None
+        s.update(target=target, draft=draft, tokens=tokens.int().contiguous(), u=torch.rand(b, n, device="cuda", generator=gen),
                  lens_d=torch.randint(n, 100000, (b,), device="cuda", generator=gen).int(), q_len=n)
         return s
     lens = _lens(case)
