@@ -21,7 +21,7 @@ def cases():
     return module
 
 
-@pytest.mark.parametrize("q,drafts,dtype", itertools.product([1, 2, 3, 4, 5, 8], ["sampled", "fixed"], ["fp32", "bf16"]))
+@pytest.mark.parametrize("q,drafts,dtype", list(itertools.product([1, 2, 3, 4, 5, 8], ["sampled", "fixed"], ["fp32", "bf16"])))
 def test_verification_in_every_form(cases, q, drafts, dtype):
     case = dict(op="verify", batch=3, q=q, vocab=1000, dtype=dtype, drafts=drafts)
     state = cases.prepare(case, 11)
