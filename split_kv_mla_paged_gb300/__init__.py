@@ -285,8 +285,6 @@ def _ptr(t) -> Optional[int]:
         return None
     if isinstance(t, np.ndarray):
         return t.ctypes.data
-    if isinstance(t, int):
-        return t
     return t.data_ptr()
 
 
@@ -722,12 +720,13 @@ def mla_decode_shared(q, kv_pages, num_pages: int, page_table, max_pages_per_req
         raise ValueError("q must be BF16 for a BF16 cache, E4M3 otherwise")
     if not _is_pool(kv_pages, kind):
         raise ValueError("kv_pages is not a pool of the plan's cache kind")
-    opts = _fp4_options(
-        _device_tensor(q_scale_dev, "q_scale_dev", dev, f32, 1),
-        _device_tensor(kv_scale_dev, "kv_scale_dev", dev, f32, 1),
-        _device_tensor(softmax_scale_dev, "softmax_scale_dev", dev, f32, 1), output_scale,
-        _device_tensor(sinks, "sinks", dev, f32, num_heads),
-        _device_tensor(query_lens, "query_lens", dev, i32, batch), None, None, PHASE_ALL)
+    _device_tensor(q_scale_dev, "q_scale_dev", dev, f32, 1)
+    _device_tensor(kv_scale_dev, "kv_scale_dev", dev, f32, 1)
+    _device_tensor(softmax_scale_dev, "softmax_scale_dev", dev, f32, 1)
+    _device_tensor(sinks, "sinks", dev, f32, num_heads)
+    _device_tensor(query_lens, "query_lens", dev, i32, batch)
+    opts = _fp4_options(q_scale_dev, kv_scale_dev, softmax_scale_dev, output_scale, sinks,
+                        query_lens, None, None, PHASE_ALL)
     _call_on(dev, load_library().mla_decode_shared, q_at,
              _device_pool(kv_pages, "kv_pages", dev, num_pages, kind), num_pages,
              _device_tensor(page_table, "page_table", dev, i32, batch * max_pages_per_req),
