@@ -68,6 +68,18 @@ __device__ __forceinline__ uint64_t prob_rest(float p, float q) {
   return rest > 0 ? static_cast<uint64_t>(rest) : 0;
 }
 
+// floor(u total) for u in [0, 1): the float's integer significand times total, shifted by
+// its exponent, so that no bit of either is lost.
+__device__ __forceinline__ uint64_t threshold(float u, uint64_t total) {
+  const uint32_t bits = __float_as_uint(u) & 0x7FFFFFFFu;  // (-0 is 0)
+  const int e = max(static_cast<int>(bits >> 23), 1);  // u = m 2^(e - 150), e <= 126
+  const uint64_t m = (bits & 0x7FFFFFu) | (bits >> 23 ? 0x800000u : 0u);
+  const int shift = 150 - e;
+  const uint64_t lo = m * total, hi = __umul64hi(m, total);  // hi < 2^24
+  if (shift < 64) return (hi << (64 - shift)) | (lo >> shift);
+  return shift < 128 ? hi >> (shift - 64) : 0;
+}
+
 template <typename T>
 __device__ __forceinline__ float prob_float(T v);
 template <>
@@ -240,7 +252,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
     }
     if (total != 0 || (!s.q && s.drop < 0)) {
       const float uc = fminf(fmaxf(u_next, 0.0f), 0.99999994f);  // NaN: 0
-      const uint64_t limit = __umul64hi(__float2ull_rn(uc * 18446744073709551616.0f), total);
+      const uint64_t limit = threshold(uc, total);
       // The part whose sums pass the limit: cumulated weight > limit first there.
       if (k0 < k1 && mine != 0 && before <= limit && limit - before < mine) {
         uint64_t run = before;
