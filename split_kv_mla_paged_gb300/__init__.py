@@ -1505,11 +1505,10 @@ def evict(pool: PagePool, kv_pages, page_lists, kv_lens, weights, keep, *, first
                           new_table, kept, counts, cache_kind=_cache_kind(kv_pages), status=status,
                           stream=side)
         _check_status_tensor(status, "evict: a length or page id is out of range")
+        pool.release(np.concatenate(lists))  # all of them or none
     except BaseException:
         pool.release(fresh)
         raise
-    for p in lists:
-        pool.release(p)
     return new_lists, stay, new_weights
 
 
