@@ -1452,18 +1452,32 @@ def _check_status_tensor(status, message: str) -> None:
         raise MlaError(code, message)
 
 
+def _check_held(pool: PagePool, lists) -> None:
+    """Raise MlaError where a listed page is not held as often as it is listed."""
+    pages = np.concatenate(lists)
+    kept = pool.fork(pages, PAGE_SIZE * pages.shape[0], 1)[0][0]  # (raises for one that is not held)
+    pool.release(kept)
+    ids, times = np.unique(pages, return_counts=True)
+    for page, n in zip(ids[times > 1], times[times > 1]):
+        if pool.references(page) < n:
+            raise MlaError(MLA_ERR_INVALID_ARG, "evict: a listed page is not held (so often)")
+
+
 def evict(pool: PagePool, kv_pages, page_lists, kv_lens, weights, keep, *, first: int = 0,
           last: int = 0, stream=None):
     """Keep the `keep` keys of each request that have the largest weights (the
     first `first` and last `last` ones always), in fresh pages of the pool, and
-    give the old pages back.
+    give the old pages back.  A request that loses no key keeps its pages (those behind
+    its last key are given back), but for a partly filled last page that is shared.
+    Every other request gets pages of its own, as each has weights of its own: forks that
+    shared a prefix share nothing of what stays.
 
     page_lists: each request's page ids (host lists); kv_lens and keep: host
     integers (keep one per request, or one for all); weights float32 [requests,
-    keys].  Returns (new page lists, new lengths (host), new weights).  Needs free
-    pages for what stays beside the pages that are in use; MlaError
-    (MLA_ERR_NO_PAGES) otherwise.  After an error the old pages are as they were, and
-    no page is taken from the pool."""
+    keys].  Returns (new page lists, new lengths (host), new weights, as wide as the
+    most keys that stay).  Needs free pages for what moves beside the pages that are in
+    use; MlaError (MLA_ERR_NO_PAGES) otherwise.  After an error the old pages are as they
+    were, and no page is taken from the pool."""
     import torch
     lens = _host_ids(kv_lens, "kv_lens")
     batch = lens.shape[0]
@@ -1482,8 +1496,16 @@ def evict(pool: PagePool, kv_pages, page_lists, kv_lens, weights, keep, *, first
             raise ValueError("page id outside the pool")
     stay = np.minimum(lens, keep).astype(np.int32)
     need = (stay + PAGE_SIZE - 1) // PAGE_SIZE
-    fresh = pool.alloc(int(need.sum()))
-    new_lists = np.split(fresh, np.cumsum(need)[:-1])
+    in_place = np.asarray([k == n and (n % PAGE_SIZE == 0 or pool.references(p[m - 1]) == 1)
+                           for p, n, k, m in zip(lists, lens, stay, need)])
+    if in_place.any():
+        _check_held(pool, lists)
+    leave = [p[m:] if here else p for p, m, here in zip(lists, need, in_place)]
+    moved = np.where(in_place, 0, stay).astype(np.int32)
+    taken = np.where(in_place, 0, need)
+    fresh = pool.alloc(int(taken.sum()))
+    new_lists = [p[:m].copy() if here else f for p, m, here, f in
+                 zip(lists, need, in_place, np.split(fresh, np.cumsum(taken)[:-1]))]
     dev, most = kv_pages.device, max(1, int(stay.max()))
 
     def table(rows):
@@ -1495,17 +1517,18 @@ def evict(pool: PagePool, kv_pages, page_lists, kv_lens, weights, keep, *, first
     try:
         kept = torch.empty((batch, most), dtype=torch.int32, device=dev)
         new_weights = torch.zeros((batch, most), dtype=torch.float32, device=dev)
-        both = torch.from_numpy(np.stack([lens, keep])).to(dev)
+        host = torch.from_numpy(np.stack([lens, keep, moved])).to(dev)
         old_table, new_table = table(lists), table(new_lists)
-        counts, status = torch.zeros_like(both[0]), torch.zeros_like(both[0, :1])
+        counts, status = torch.zeros_like(host[0]), torch.zeros_like(host[0, :1])
         with _ordered(stream, dev) as side:
-            mla_evict_select(weights, both[0], both[1], kept, counts, first=first, last=last,
+            mla_evict_select(weights, host[0], host[1], kept, counts, first=first, last=last,
                              new_weights=new_weights, status=status, stream=side)
-            mla_rows_move(kv_pages, kv_pages.shape[0], old_table, kv_pages, kv_pages.shape[0],
-                          new_table, kept, counts, cache_kind=_cache_kind(kv_pages), status=status,
-                          stream=side)
+            if moved.any():
+                mla_rows_move(kv_pages, kv_pages.shape[0], old_table, kv_pages, kv_pages.shape[0],
+                              new_table, kept, host[2], cache_kind=_cache_kind(kv_pages),
+                              status=status, stream=side)
         _check_status_tensor(status, "evict: a length or page id is out of range")
-        pool.release(np.concatenate(lists))  # all of them or none
+        pool.release(np.concatenate(leave))  # all of them or none
     except BaseException:
         pool.release(fresh)
         raise

@@ -63,3 +63,41 @@ def test_what_stays_is_moved_and_the_old_pages_are_free():
         pos = np.sort(np.argsort(-w[b, :n].numpy(), kind="stable")[:lens[b]])
         assert torch.equal(_rows(data, new[b], lens[b]), _rows(before, lists[b], n)[pos])
         assert torch.equal(new_w[b, :lens[b]], w[b, pos])
+
+
+def test_a_request_that_loses_nothing_keeps_its_pages(moves):
+    # 96 and 50 keys stay; of the third's 96 keys 40; the second's unused page is given back.
+    pool, data, w = mla.PagePool(16), _data(16), torch.rand(3, 96)
+    lists, before = [pool.alloc(3), pool.alloc(3), pool.alloc(3)], data.clone()
+    new, lens, new_w = mla.evict(pool, data, lists, [96, 50, 96], w, [96, 200, 40])
+    assert lens.tolist() == [96, 50, 40] and moves == [[0, 0, 40]]
+    assert new[0].tolist() == lists[0].tolist() and new[1].tolist() == lists[1][:2].tolist()
+    assert pool.free_pages == 16 - 3 - 2 - 2 and not set(new[2]) & set(lists[2])
+    for b in range(2):
+        assert torch.equal(_rows(data, new[b], lens[b]), _rows(before, lists[b], lens[b])) and torch.equal(new_w[b, :lens[b]], w[b, :lens[b]])
+    # All within their budgets, without a free page.
+    held = pool.alloc(pool.free_pages)
+    again, lens, _ = mla.evict(pool, data, new, lens, new_w, 96)
+    assert [p.tolist() for p in again] == [p.tolist() for p in new] and pool.free_pages == 0 and len(moves) == 1 and len(held) == 9
+
+
+def test_a_shared_partly_filled_page_does_not_stay(moves):
+    # 50 keys in pages that another request holds as well: what is appended next is the request's own.
+    pool, data = mla.PagePool(16), _data(16)
+    pages = pool.alloc(2)
+    other = pool.fork(pages, 64, 1)[0][0]
+    for lens, private in (([50], True), ([64], False)):
+        new, _, _ = mla.evict(pool, data, [pages], lens, torch.rand(1, 64), 64)
+        assert (set(new[0]).isdisjoint(other)) == private and pool.references(other[0]) == (1 if private else 2)
+        if private:  # (back to the start)
+            pool.release(new[0])
+            pages = pool.fork(other, 64, 1)[0][0]
+
+
+def test_pages_that_stay_have_to_be_held():
+    pool, data, w = mla.PagePool(16), _data(16), torch.rand(2, 96)
+    good = pool.alloc(3)
+    for lists, keep in (([good, [12, 13, 14]], 96), ([good, good], 96), ([good, good], [96, 40])):
+        with pytest.raises(mla.MlaError):
+            mla.evict(pool, data, lists, [96, 96], w, keep)
+        assert pool.free_pages == 13 and all(pool.references(int(p)) == 1 for p in good)
