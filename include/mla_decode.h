@@ -543,19 +543,27 @@ MLA_API int mla_verify_drafts(const mla_verify_args_t* args, void* stream);
  * with the scores s of the definition above and the decode's LSE, of the whole key
  * range: a decode over key windows or selected pages gives no such LSE.  With sinks
  * a row's weights sum to less than 1.  Rows without a visible key (LSE -inf) add
- * nothing.  What lies behind kv_lens stays as it was.
+ * nothing.  What lies behind kv_lens stays as it was.  In a loop over steps, keys that
+ * left the cache meanwhile (rejected drafts) have left their weight behind in the places of
+ * those that were written next: previous_lens, mla_verify_drafts' new_lens of the step
+ * before, keeps it out.
  *
  * Zero-initialise the structure.
  * q, kv_pages    as for mla_decode_shared's cache kinds, 16-byte aligned.
  * lse            fp32 [batch][q_len][num_heads].
  * weights        fp32 [batch][weights_stride], kv_lens[b] <= weights_stride.
  * previous       fp32 [batch][previous_stride] or NULL (nothing is added; decay is
- *                then not used), previous_stride >= kv_lens[b].  May be weights.
+ *                then not used), previous_stride >= min(kv_lens[b], previous_lens[b]).
+ *                May be weights.
+ * previous_lens  int32 [batch] or NULL (kv_lens): keys from previous_lens[b] on had no
+ *                weight before, whatever previous holds there.
  * q_scale_dev, kv_scale_dev, softmax_scale_dev   device fp32 or NULL, as in
  *                mla_decode_options_t.
  * status         int32 or NULL: set to MLA_ERR_INVALID_ARG for a length outside [0,
- *                min(weights_stride, previous_stride, 32 * max_pages_per_req, 2^31 - 129)] or a
- *                query count outside [1, q_len] (that request is skipped) or a bad
+ *                min(weights_stride, 32 * max_pages_per_req, 2^31 - 129)], or without
+ *                previous_lens above previous_stride, or a query count outside [1, q_len]
+ *                (that request is skipped), for a negative previous length or one that
+ *                previous_stride does not hold (the nearest one counts) or a bad
  *                page id, to MLA_ERR_TIMEOUT for a wait that ran out; never cleared.
  * All on the device; no workspace.
  */
@@ -577,6 +585,7 @@ typedef struct {
   int32_t* status;
   int32_t max_pages_per_req, batch, q_len, num_heads, causal, cache_kind;
   float q_scale, kv_scale, softmax_scale, decay;
+  const int32_t* previous_lens;
 } mla_key_weights_args_t;
 
 MLA_API int mla_key_weights(const mla_key_weights_args_t* args, void* stream);

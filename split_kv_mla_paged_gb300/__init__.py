@@ -132,7 +132,7 @@ class KeyWeightsArgs(ctypes.Structure):
                 ("num_heads", ctypes.c_int32), ("causal", ctypes.c_int32),
                 ("cache_kind", ctypes.c_int32), ("q_scale", ctypes.c_float),
                 ("kv_scale", ctypes.c_float), ("softmax_scale", ctypes.c_float),
-                ("decay", ctypes.c_float)]
+                ("decay", ctypes.c_float), ("previous_lens", ctypes.c_void_p)]
 
 
 class _SharedPlanInfo(ctypes.Structure):
@@ -822,11 +822,12 @@ def mla_key_weights(q, kv_pages, num_pages: int, page_table, max_pages_per_req: 
                     weights, batch: int, q_len: int, num_heads: int, causal: bool, q_scale: float,
                     kv_scale: float, softmax_scale: float, *, cache_kind: int, previous=None,
                     decay: float = 1.0, query_lens=None, q_scale_dev=None, kv_scale_dev=None,
-                    softmax_scale_dev=None, status=None, stream=None) -> None:
+                    softmax_scale_dev=None, status=None, previous_lens=None, stream=None) -> None:
     """Attention weight that each cached key received from the rows of a decode
     with log-sum-exps lse: weights[b][j] = decay * previous[b][j] + the rows' sum
     (see mla_key_weights in mla_decode.h).  weights and previous are float32
-    [batch, keys] and may be the same tensor."""
+    [batch, keys] and may be the same tensor; of previous only the first
+    previous_lens[b] keys count (int32 on the device; None: all)."""
     import torch
     i32, f32 = torch.int32, torch.float32
     dev = _device_of(q, "q")
@@ -848,7 +849,8 @@ def mla_key_weights(q, kv_pages, num_pages: int, page_table, max_pages_per_req: 
         _device_tensor(kv_scale_dev, "kv_scale_dev", dev, f32, 1),
         _device_tensor(softmax_scale_dev, "softmax_scale_dev", dev, f32, 1),
         _device_tensor(status, "status", dev, i32, 1), max_pages_per_req, batch, q_len, num_heads,
-        1 if causal else 0, cache_kind, q_scale, kv_scale, softmax_scale, decay)
+        1 if causal else 0, cache_kind, q_scale, kv_scale, softmax_scale, decay,
+        _device_tensor(previous_lens, "previous_lens", dev, i32, batch))
     _call_on(dev, load_library().mla_key_weights, ctypes.byref(a), stream=stream)
 
 
@@ -1382,10 +1384,13 @@ def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> 
 
 def key_weights(q, kv_pages, page_table, kv_lens, lse, *, num_heads: int, q_len: int, causal: bool,
                 softmax_scale: float, q_scale: float = 1.0, kv_scale: float = 1.0, previous=None,
-                decay: float = 1.0, query_lens=None, stream=None):
+                decay: float = 1.0, query_lens=None, previous_lens=None, stream=None):
     """Run mla_key_weights with the arguments and the LSE of a decode; kv_lens is a
     host sequence.  previous float32 [batch, keys] is updated in place, or zeros as
-    wide as the longest request are; returns it."""
+    wide as the longest request are; returns it.  Of previous only the first
+    previous_lens[b] keys count (a tensor or a host sequence; None: all): the lengths that
+    mla_verify_drafts or evict left, so that what rejected drafts received does not pass to
+    the keys in their places."""
     import torch
     dev = q.device
     lens = _host_ids(kv_lens.cpu() if hasattr(kv_lens, "cpu") else kv_lens, "kv_lens")
@@ -1394,6 +1399,8 @@ def key_weights(q, kv_pages, page_table, kv_lens, lse, *, num_heads: int, q_len:
     if weights is None:
         weights = torch.zeros((batch, max(1, int(lens.max()) if batch else 1)), dtype=torch.float32,
                               device=dev)
+    if previous_lens is not None:
+        previous_lens = torch.as_tensor(previous_lens, dtype=torch.int32).to(dev).contiguous()
     if query_lens is not None:
         query_lens = torch.as_tensor(query_lens, dtype=torch.int32).to(dev).contiguous()
     status = torch.zeros((1,), dtype=torch.int32, device=dev)
@@ -1402,7 +1409,8 @@ def key_weights(q, kv_pages, page_table, kv_lens, lse, *, num_heads: int, q_len:
         mla_key_weights(q, kv_pages, kv_pages.shape[0], page_table, page_table.shape[1], lens_d, lse,
                         weights, batch, q_len, num_heads, causal, q_scale, kv_scale, softmax_scale,
                         cache_kind=_cache_kind(kv_pages), previous=previous, decay=decay,
-                        query_lens=query_lens, status=status, stream=side)
+                        query_lens=query_lens, status=status, previous_lens=previous_lens,
+                        stream=side)
     _check_status_tensor(status, "key_weights: a length, query count or page id is out of range, "
                                  "or a device wait ran out")
     return weights
