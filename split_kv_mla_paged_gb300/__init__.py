@@ -1384,23 +1384,30 @@ def copy_pages(src_pool, dst_pool, src_ids, dst_ids, rows=None, stream=None) -> 
 
 def key_weights(q, kv_pages, page_table, kv_lens, lse, *, num_heads: int, q_len: int, causal: bool,
                 softmax_scale: float, q_scale: float = 1.0, kv_scale: float = 1.0, previous=None,
-                decay: float = 1.0, query_lens=None, previous_lens=None, stream=None):
+                decay: float = 1.0, query_lens=None, previous_lens=None, capacity: int = 0,
+                stream=None):
     """Run mla_key_weights with the arguments and the LSE of a decode; kv_lens is a
-    host sequence.  previous float32 [batch, keys] is updated in place, or zeros as
-    wide as the longest request are; returns it.  Of previous only the first
-    previous_lens[b] keys count (a tensor or a host sequence; None: all): the lengths that
-    mla_verify_drafts or evict left, so that what rejected drafts received does not pass to
-    the keys in their places."""
+    host sequence.  previous float32 [batch, keys] is updated in place where it is wide
+    enough for kv_lens.  Otherwise, and without it, the weights are a new tensor, zeros
+    behind the requests' ends, as wide as the longest request or `capacity` keys if that
+    is more.  Of previous only the first previous_lens[b] keys count (a tensor or a host
+    sequence; None: as many as it holds): the lengths that mla_verify_drafts or evict left, so
+    that what rejected drafts received does not pass to the keys in their places.  Returns
+    the weights."""
     import torch
     dev = q.device
     lens = _host_ids(kv_lens.cpu() if hasattr(kv_lens, "cpu") else kv_lens, "kv_lens")
     batch = lens.shape[0]
-    weights = previous
-    if weights is None:
-        weights = torch.zeros((batch, max(1, int(lens.max()) if batch else 1)), dtype=torch.float32,
-                              device=dev)
+    if previous is not None and previous.dim() != 2:
+        raise ValueError("previous must be [batch, keys]")
+    longest = max(1, int(lens.max()) if batch else 1)
     if previous_lens is not None:
         previous_lens = torch.as_tensor(previous_lens, dtype=torch.int32).to(dev).contiguous()
+    weights = previous
+    if previous is None or previous.shape[1] < longest:
+        weights = torch.zeros((batch, max(longest, capacity)), dtype=torch.float32, device=dev)
+        if previous is not None and previous_lens is None:
+            previous_lens = torch.full((batch,), previous.shape[1], dtype=torch.int32, device=dev)
     if query_lens is not None:
         query_lens = torch.as_tensor(query_lens, dtype=torch.int32).to(dev).contiguous()
     status = torch.zeros((1,), dtype=torch.int32, device=dev)

@@ -1,11 +1,18 @@
-"""GPU: key weights over the steps of a serving loop: rejected drafts whose places are
-written again."""
+"""GPU: key weights over the steps of a serving loop: caches that grow, rejected drafts
+whose places are written again, and evictions in between.
+
+Tolerances as in test_key_weights_gpu: the weights of a step are within its relative
+bound of the definition in 64 bits with the device's LSE; all terms are positive, so that
+the sum over steps is within the largest of those bounds and 2^-24 for each step's
+rounding of decay * previous and of the addition."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 import split_kv_mla_paged_gb300 as mla
+from oracle import cache
 from split_kv_mla_paged_gb300 import build as mla_build
 from synth import SOFTMAX_SCALE
 from test_key_weights_gpu import _case
@@ -92,3 +99,97 @@ def test_a_structure_without_previous_weights_ignores_the_rest():
                            max_pages_per_req=pt.shape[1], batch=1, q_len=1, num_heads=12, q_scale=1.0, kv_scale=1.0, softmax_scale=SOFTMAX_SCALE)
     assert mla.load_library().mla_key_weights(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
     assert int(status) == 0 and (out > 0).all()
+
+
+def test_widths_of_new_and_narrow_weights():
+    lens = [200, 100]
+    inp, pool, _, _ = _case("fp8", 12, 1, lens, 4)
+    args = (inp.q.cuda(), pool.cuda(), inp.page_table.cuda())
+    lse, kw = torch.full((2, 1, 12), 5.0, device="cuda"), dict(num_heads=12, q_len=1, causal=False, softmax_scale=SOFTMAX_SCALE)
+    assert mla.key_weights(*args, lens, lse, **kw).shape == (2, 200)
+    w = mla.key_weights(*args, lens, lse, capacity=300, **kw)
+    assert w.shape == (2, 300) and not w[0, 200:].any() and not w[1, 100:].any()
+    assert mla.key_weights(*args, lens, lse, previous=w, **kw) is w
+    narrow = torch.ones(2, 150, device="cuda")
+    wide = mla.key_weights(*args, lens, lse, previous=narrow, decay=0.5, capacity=256, **kw)
+    alone = mla.key_weights(*args, lens, lse, **kw)
+    want = torch.zeros(2, 256, device="cuda")
+    want[:, :200] = alone
+    want[0, :150] += 0.5
+    want[1, :100] += 0.5
+    assert wide.shape == (2, 256) and torch.equal(wide, want) and (narrow == 1.0).all()
+    with pytest.raises(ValueError):
+        mla.key_weights(*args, lens, lse, previous=torch.ones(300, device="cuda"), **kw)
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_a_loop_over_steps(kind):
+    heads, q_len, vocab, decay, total, batch, steps = 12, 4, 501, 0.8, 160, 3, 7
+    g = torch.Generator().manual_seed(40)
+    bf16 = kind == "bf16"
+    pages = mla.PagePool(total)
+    pool = mla.fp4_pool(total) if kind == "fp4" else torch.zeros(total, 32, 576, dtype=torch.bfloat16 if bf16 else torch.uint8, device="cuda")
+    kv_lens = [400, 333, 64]
+    lists = [pages.alloc((n + 31) // 32) for n in kv_lens]
+
+    def table():
+        out = torch.zeros(batch, max(len(p) for p in lists), dtype=torch.int32)
+        for b, p in enumerate(lists):
+            out[b, :len(p)] = torch.from_numpy(np.asarray(p, np.int32))
+        return out.cuda()
+
+    def write(starts, ends):
+        at = [(b, j) for b in range(batch) for j in range(starts[b], ends[b])]
+        t, status = table(), torch.zeros(1, dtype=torch.int32, device="cuda")
+        mla.mla_prologue(len(at), positions=_i32([j for _, j in at]), kv_rows=torch.randn(len(at), 576, generator=g).bfloat16().cuda(),
+                         req_idx=_i32([b for b, _ in at]), page_table=t, max_pages_per_req=t.shape[1], batch=batch, kv_pages=pool, num_pages=total,
+                         cache_kind=KINDS[kind], status=status)
+        assert int(status) == 0
+
+    def values():
+        host = pool.cpu()
+        if kind == "fp4":
+            return cache.fp4_decode(host.numpy())
+        return host.double().numpy() if bf16 else cache.e4m3_values()[host.numpy()]
+
+    write([0] * batch, kv_lens)
+    weights, ref, bound, rejected, evicted = None, [np.zeros(n) for n in kv_lens], 0.0, 0, 0
+    for step in range(steps):
+        # The block of the next token and three drafts behind what is cached.
+        ends = [n + q_len for n in kv_lens]
+        lists = [np.concatenate([p, pages.alloc((n + 31) // 32 - len(p))]) if (n + 31) // 32 > len(p) else p for p, n in zip(lists, ends)]
+        write(kv_lens, ends)
+        seen, kv_lens = kv_lens, ends
+        q = torch.randn(batch, q_len, heads, 576, generator=g) * 0.5
+        q = q.bfloat16() if bf16 else q.to(torch.float8_e4m3fn).view(torch.uint8)
+        args = dict(num_heads=heads, q_len=q_len, causal=True, softmax_scale=SOFTMAX_SCALE)
+        _, lse, _ = mla.decode(q.cuda(), pool, table(), kv_lens, **args)
+        weights = mla.key_weights(q.cuda(), pool, table(), kv_lens, lse, previous=weights, previous_lens=None if weights is None else seen,
+                                  decay=decay, capacity=410, **args)
+        held, qv = values(), q.double().numpy() if bf16 else cache.e4m3_values()[q.numpy()]
+        for b, n in enumerate(kv_lens):
+            k = held[lists[b]].reshape(-1, 576)[:n]
+            s = np.einsum("ihd,jd->ihj", qv[b], k) * SOFTMAX_SCALE
+            limit = n - q_len + np.arange(q_len)
+            s = np.where(np.arange(n)[None, None] <= limit[:, None, None], s, -np.inf)
+            l = lse[b].cpu().double().numpy()[..., None]
+            new = np.exp(s - l).sum((0, 1))
+            new[:len(ref[b])] += decay * ref[b]
+            ref[b] = new
+            size = (np.abs(s[np.isfinite(s)]).max() + np.abs(l).max()) * np.log2(np.e)
+            products = SOFTMAX_SCALE * np.log2(np.e) * np.einsum("ihd,jd->ihj", np.abs(qv[b]), np.abs(k)).max()
+            bound = max(bound, np.log(2.0) * 2.0 ** -24 * (4 * size + 576 * products) + 2.0 ** -22 + 2.0 ** -24 * (heads * q_len + 2))
+            got = weights[b, :n].cpu().double().numpy()
+            assert (np.abs(got - ref[b]) <= (bound + 2 * (step + 1) * 2.0 ** -24) * ref[b]).all()
+        target = torch.softmax(2 * torch.randn(batch, q_len, vocab, generator=g), -1)
+        drafts, u = target[:, :q_len - 1].argmax(-1).int(), torch.rand(batch, q_len, generator=g) * 0.1
+        _, accepted, lens_d = mla.verify_drafts(target.cuda(), drafts.cuda(), u.cuda(), kv_lens=_i32(kv_lens))
+        kv_lens = lens_d.tolist()
+        rejected += int((q_len - 1 - accepted).sum())
+        ref = [r[:n] for r, n in zip(ref, kv_lens)]
+        if step in (2, 4):
+            lists, kept, weights = mla.evict(pages, pool, lists, kv_lens, weights, [300, 200, 500], first=4, last=16)
+            ref = [r[:0] if n == 0 else w[:n].cpu().double().numpy() for r, n, w in zip(ref, kept.tolist(), weights)]
+            kv_lens = kept.tolist()
+            evicted += 1
+    assert rejected > 0 and evicted == 2 and weights.shape[1] >= max(kv_lens)
