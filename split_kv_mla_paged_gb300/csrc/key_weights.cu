@@ -69,6 +69,10 @@ struct KeyWeightsParams {
   // above took 28.2 us where it takes 33.7.  Accumulators in turn, a fifth one free when a
   // tile begins, took 32.4; all scores in registers before the first weight 32.6: the
   // ring holds less than a tile next to Q, so that loads wait with the MMAs.)
+  // E4M3 and 4-bit scores take half of BF16's instructions: two accumulators for more than
+  // 64 rows, whose weights are as far off as those of 64 rows with four (1.2e-7 of the
+  // weight in the mean square for 64, 96 and 128 rows; a product in fp32 0.7e-7 to 0.8e-7, most
+  // of it the rounding of the exponents, as here; BF16 with four 4.0e-7, in fp32 2.4e-7).
   int32_t sums;       // 2, 4 or (BF16) 8
   int32_t s_buffers;  // 2 or 1
   uint32_t q_bytes;  // of one buffer
