@@ -895,7 +895,10 @@ def shared_groups(page_lists, kv_lens, q_len: int = 1, least: int = PAGE_SIZE):
     """Groups of consecutive requests whose page lists begin with the same pages,
     for mla_shared_plan: (group_offsets, prefix_lens).  A request joins the group
     before it while at least `least` keys stay shared and no more keys are attended
-    than without it; the keys of the last q_len positions are never shared."""
+    than without it; the keys of the last q_len positions are never shared.  Requests that
+    share pages but do not follow one another are not found, and a group has one prefix: of
+    samples of several prompts behind one system text, either the text is shared by all or
+    each prompt by its own."""
     lens = _host_ids(kv_lens, "kv_lens")
     lists = [_host_ids(p, "page_lists") for p in page_lists]
     if len(lists) != lens.shape[0]:

@@ -18,7 +18,8 @@
 // (3 us until all weights are in shared memory, 1.8, 2 and 3.1 us for the passes, 1.5
 // to 2 us for each digit's search across the cluster); one of 1,048,576 keys, 131,072
 // kept, 39 us (16 CTAs read them three times from L2: 4.5, 8 and 9 us); 4 of 2,111 keys
-// 6.3 us.
+// 6.3 us.  The launch is planned by the weights' stride, as the lengths are on the device:
+// the 16 requests in rows of 1M weights take 3 us more, the 4 in rows of 128K 4 us.
 //
 // Move.  Bytes only: a warp copies the 288 16-byte vectors of 8 E4M3 or 4 BF16 rows,
 // nine per lane and all in flight, or 8 rows of the 4-bit cache's three planes.

@@ -23,11 +23,13 @@
 // weight is the sum of one thread, in the order of the rows: results do not depend on
 // how the tiles are divided.
 //
-// Bound by the bytes of the cache.  Measured (calls in a CUDA graph): 16 x 128K keys (a
-// little fewer for 15 of them), 12 heads, E4M3, 143 us for 938 MB (6.5 TB/s, 97 % of
-// the copy bandwidth); 4 requests of up to 32,777 keys, 8 x 12 rows, BF16, 33.7 us for
-// 124 MB (start of the CTAs, then 5 or 6 tiles each, MMAs and epilogue in turn); 2 x
-// 1,000 keys, 4 bits, 8.4 us.
+// E4M3 and BF16 caches of few rows: bound by the bytes of the cache.  Measured (calls in a
+// CUDA graph): 16 x 128K keys (a little fewer for 15 of them), 12 heads, E4M3, 143 to 145
+// us for 938 MB (6.5 TB/s, 95 to 97 % of the copy bandwidth); 16 x 128K, BF16, 357 us (100 %);
+// 96 rows 200 and 455 us; 4 requests of up to 32,777 keys, 8 x 12 rows, BF16, 33.7 us for
+// 124 MB (start of the CTAs, then 5 or 6 tiles each, MMAs and epilogue in turn).  4 bits: 16 x
+// 128K 231 us, where the bytes take 106: a tile takes 2.1 us, its loads and then its
+// expansion; 2 x 1,000 keys 8.3 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

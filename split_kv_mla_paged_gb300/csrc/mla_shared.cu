@@ -26,8 +26,8 @@
 // operations weigh more than the bytes.  Measured (calls in a CUDA graph): 16 samples
 // of a 128K-token prompt, 12 heads, E4M3, 68.6 us (as separate requests 198 us) where
 // bytes and operations take 13.3 and 14.4 us; 8 samples x 8 drafted tokens over a
-// 32K-token prompt, 768 rows, 4 bits, 71.4 us (each for itself; the prefix apart 74.8),
-// 14.4 us of operations; 15 samples of three 64K prompts, BF16, 71.8 us, 23.7 us of bytes.
+// 32K-token prompt, 768 rows, 4 bits, 72.7 us (each for itself; 3.4 more with the prefix
+// apart, when it was chosen), 14.4 us of operations; 15 samples of three 64K prompts, BF16, 71.8 us, 23.7 us of bytes.
 // A 96-row tile of 128 keys takes 2.8 us (see the split kernel: the chain through its
 // two KV stages, 350 KB of MMA operands and the softmax's instructions), and start,
 // epilogue and merge of 8 to 16 tiles a CTA some 25 us.
