@@ -1,4 +1,4 @@
-"""GPU: the serving loop that the README shows, run as it stands there."""
+"""GPU: the serving loop of the user's documentation, run as it stands there."""
 import os
 import re
 
@@ -11,12 +11,12 @@ from split_kv_mla_paged_gb300 import build as mla_build
 
 pytestmark = pytest.mark.gpu
 
-README = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+DOCUMENT = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
 
 
 def test_the_serving_loop():
     mla_build.build()
-    blocks = re.findall(r"```python\n(.*?)```", open(README).read(), re.S)
+    blocks = re.findall(r"```python\n(.*?)```", open(DOCUMENT).read(), re.S)
     code = [b for b in blocks if "for step in range(steps)" in b]
     assert len(code) == 1
     q_len, heads, vocab, total, prompt, steps = 4, 12, 777, 4000, 18985, 12
