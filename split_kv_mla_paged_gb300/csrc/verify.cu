@@ -171,13 +171,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 2)
   const int ranks = static_cast<int>(cluster.num_blocks());
   const int b = blockIdx.x / ranks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  cluster_arrive();  // this CTA has started (waited for ahead of the first remote store)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int q_b = a.query_lens ? a.query_lens[b] : a.q_len;
   if (q_b < 1 || q_b > a.q_len) {  // the same for the whole cluster
     if (a.status && rank == 0 && threadIdx.x == 0) atomicCAS(a.status, 0, MLA_ERR_INVALID_ARG);
+    cluster_wait();
     return;
   }
-  cluster_arrive();  // this CTA has started (waited for ahead of the first remote store)
   const int n = q_b - 1;  // drafts
   const T* target = reinterpret_cast<const T*>(a.target_probs) + b * a.target_batch_stride;
   const T* draft =
